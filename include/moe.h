@@ -11,7 +11,9 @@
  *                          (moe_cache_lookup_fill_split + moe_cache_wait_fills: hits computed during fills)
  *   moe_grouped_ffn        grouped SwiGLU expert FFN (f32, bf16 or MXFP4 weights)
  *   moe_combine            gate-weighted merge of the expert outputs
+ *   moe_layer_decode       all of the above for a few tokens in two kernels
  *   moe_layer_stream_*     whole-layer double buffering for prefill
+ *   moe_w4_linear          linear product with 4-bit weights and group scales
  *
  * Conventions
  *  - Pointers are device pointers unless the name ends in _host.
@@ -360,6 +362,63 @@ int moe_grouped_ffn_down(int wdt, const void* slot_pool, size_t slot_stride, con
  * cache waves.  y: [T][H] of ydt. */
 int moe_combine(const float* out_rows, const float* topk_w, const int32_t* inv_rows, const float* shared_out,
                 int T, int k, int H, void* y, int ydt, hipStream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* One layer for a few tokens: routing, expert FFN, shared expert and combine in
+ * one call of two kernels (the pages' decode step runs one token through every
+ * layer, "The gap it targets"; at that size the launches and round trips between
+ * the layer's steps cost as much as the weights).
+ *     y[t] = sum_j topk_w[t][j] * FFN_e(x[t]),  e = topk_ids[t][j]  (+ FFN_shared(x[t]))
+ * with FFN, weight layouts and roundings of moe_grouped_ffn and the order of sums of
+ * moe_combine; the K order inside a product differs from moe_grouped_ffn's, so the two
+ * agree within rounding, not bit for bit.
+ *   logits    [T][E] f32: routed as moe_route_topk does, topk_ids and topk_w [T][k] are
+ *             written; NULL: topk_ids and topk_w are read as given (routing of the
+ *             caller's own, or of an earlier moe_route)
+ *   slot_of_expert  [E]; a pair whose expert has no slot (-1), or whose given id lies
+ *             outside [0, E), contributes nothing to y (a cache wave or an expert shard
+ *             gives its part of the sum)
+ *   y         [T][H] of ydt (MOE_F32 or MOE_BF16)
+ *   workspace >= moe_layer_decode_workspace() bytes, written by the call (two calls that
+ *             may overlap need one each)
+ * bf16 or MXFP4 weights (MOE_EUNSUPPORTED otherwise), T <= MOE_LAYER_DECODE_MAX_T and
+ * T*k <= MOE_LAYER_DECODE_MAX_PAIRS (MOE_EUNSUPPORTED beyond: use the separate calls).
+ * Asynchronous, allocates nothing, may be captured into a graph. */
+#define MOE_LAYER_DECODE_MAX_T 64
+#define MOE_LAYER_DECODE_MAX_PAIRS 512
+size_t moe_layer_decode_workspace(int T, int k, int E, int H, int I, int I_shared, int wdt);
+int moe_layer_decode(int wdt, const void* slot_pool, size_t slot_stride, const int32_t* slot_of_expert,
+                     const void* shared_w, int I_shared, const void* x, const float* logits, int T, int k, int E,
+                     int H, int I, int32_t* topk_ids, float* topk_w, void* y, int ydt, void* workspace,
+                     size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Linear product with 4-bit weights, for the dense products around the experts
+ * (projections, a head over the vocabulary) of a model whose weights are 4-bit (the
+ * pages' MXFP4 build, "Results").
+ *     y[t][n] = sum_k x[t][k] * W[n][k]  (+ bias[n])
+ *   MOE_MXFP4: W = E2M1(code) * 2^(scale - 127), blocks of 32 along k (OCP MX v1.0)
+ *   MOE_INT4:  W = s * (q - z), q the code 0..15, s (f16) and z (0..255) one per row
+ *              and group of `group` = 32, 64 or 128 consecutive k
+ * N >= 1, K a positive multiple of 32 and at most 2^20 (the last group may be partial,
+ * group must be 32 for MOE_MXFP4), N * K < 2^40.
+ *
+ * moe_w4_pack lays the weights out once for the products:
+ *   codes   [N][K/2], element 2i of a row in the low nibble of byte i
+ *   scales  MOE_MXFP4: E8M0 bytes [N][K/32]; MOE_INT4: f16 [N][ceil(K/group)]
+ *   zeros   MOE_INT4: uint8 [N][ceil(K/group)], NULL: 8 everywhere; MOE_MXFP4: NULL
+ *   w       moe_w4_bytes() bytes (0 for invalid shapes)
+ *
+ * moe_w4_linear: x rows of K bf16, x_ld elements apart (x_ld >= K, a multiple of 8, at
+ * most 2^22); y rows of N elements of ydt (MOE_F32 or MOE_BF16), y_ld >= N apart; bias [N] f32 or
+ * NULL.  Any T >= 0: the weights stream once per 64 tokens.  Products are exact, sums are in
+ * f32 in a fixed order, one rounding to ydt.  Asynchronous, no workspace. */
+enum { MOE_INT4 = 4 };
+size_t moe_w4_bytes(int fmt, int N, int K, int group);
+int moe_w4_pack(int fmt, const uint8_t* codes, const void* scales, const uint8_t* zeros, int N, int K, int group,
+                void* w, hipStream_t stream);
+int moe_w4_linear(int fmt, const void* w, int N, int K, int group, const void* x, int64_t x_ld, int T,
+                  const float* bias, void* y, int64_t y_ld, int ydt, hipStream_t stream);
 
 /* ------------------------------------------------------------------------- */
 /* Whole-layer streaming for prefill.  The pages: in prefill, whole layers are

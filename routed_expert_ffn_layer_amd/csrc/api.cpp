@@ -197,6 +197,133 @@ int moe_combine(const float* out_rows, const float* topk_w, const int32_t* inv_r
 }
 
 // ---------------------------------------------------------------------------
+size_t moe_layer_decode_workspace(int T, int k, int E, int H, int I, int I_shared, int wdt) {
+  const CallRange range_(__func__);
+  if (wdt != MOE_BF16 && wdt != MOE_MXFP4) return 0;
+  return moe_grouped_ffn_workspace(T, k, E, H, I, I_shared, wdt);
+}
+
+int moe_layer_decode(int wdt, const void* slot_pool, size_t slot_stride, const int32_t* slot_of_expert,
+                     const void* shared_w, int I_shared, const void* x, const float* logits, int T, int k, int E,
+                     int H, int I, int32_t* topk_ids, float* topk_w, void* y, int ydt, void* workspace,
+                     size_t ws_bytes, hipStream_t stream) {
+  const CallRange range_(__func__);
+  static_assert(MOE_LAYER_DECODE_MAX_T == moe::kDecodeLayerMaxT &&
+                    MOE_LAYER_DECODE_MAX_PAIRS == moe::kDecodeLayerMaxPairs,
+                "limits of the header and the kernels");
+  if (int rc = check_routing(T, E, k)) return rc;
+  if (int rc = check_dims(wdt, H, I, "moe_layer_decode")) return rc;
+  if (wdt != MOE_BF16 && wdt != MOE_MXFP4)
+    return fail(MOE_EUNSUPPORTED, "moe_layer_decode: weight type %d (bf16 and MXFP4 only)", wdt);
+  if (ydt != MOE_F32 && ydt != MOE_BF16) return fail(MOE_EINVAL, "moe_layer_decode: ydt must be MOE_F32 or MOE_BF16");
+  if (shared_w) {
+    if (int rc = check_dims(wdt, H, I_shared, "moe_layer_decode shared expert")) return rc;
+    REQUIRE_PTR(shared_w);
+  } else {
+    I_shared = 0;
+  }
+  if (T > MOE_LAYER_DECODE_MAX_T || T * k > MOE_LAYER_DECODE_MAX_PAIRS)
+    return fail(MOE_EUNSUPPORTED, "moe_layer_decode: T=%d, T*k=%d beyond %d tokens, %d pairs", T, T * k,
+                MOE_LAYER_DECODE_MAX_T, MOE_LAYER_DECODE_MAX_PAIRS);
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(slot_pool);
+  REQUIRE_PTR(slot_of_expert);
+  REQUIRE_PTR(x);
+  if (logits) REQUIRE_PTR(logits);
+  REQUIRE_PTR(topk_ids);
+  REQUIRE_PTR(topk_w);
+  REQUIRE_PTR(y);
+  REQUIRE_PTR(workspace);
+  const size_t eb = moe_expert_bytes(wdt, H, I);
+  REQUIRE(slot_stride >= eb && slot_stride % 16 == 0,
+          "slot_stride=%zu must be >= expert bytes %zu and a multiple of 16", slot_stride, eb);
+  if (eb >= (size_t)1 << 31 || (shared_w && moe_expert_bytes(wdt, H, I_shared) >= (size_t)1 << 31))
+    return fail(MOE_EUNSUPPORTED, "moe_layer_decode: experts of 2 GiB or more");
+  const size_t need = moe::ffn_workspace_bytes(wdt, T, k, H, I, I_shared);
+  if (ws_bytes < need) return fail(MOE_ECAPACITY, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  moe::DecodeLayerArgs a;
+  a.slot_pool = static_cast<const uint8_t*>(slot_pool);
+  a.slot_stride = slot_stride;
+  a.slot_of_expert = slot_of_expert;
+  a.shared_w = static_cast<const uint8_t*>(shared_w);
+  a.x = static_cast<const uint16_t*>(x);
+  a.logits = logits;
+  a.ids = topk_ids;
+  a.w = topk_w;
+  a.h = static_cast<uint16_t*>(workspace);
+  a.y = y;
+  a.T = T;
+  a.k = k;
+  a.E = E;
+  a.H = H;
+  a.I = I;
+  a.I_shared = I_shared;
+  a.h_ld = I > I_shared ? I : I_shared;
+  hipError_t e = moe::launch_decode_layer(wdt, a, ydt == MOE_BF16, stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_layer_decode launch");
+}
+
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_w4(int fmt, int N, int K, int group, const char* what) {
+  if (fmt != MOE_MXFP4 && fmt != MOE_INT4) return fail(MOE_EINVAL, "%s: unknown 4-bit format %d", what, fmt);
+  if (N < 1 || K < 32 || K % 32 || K > 1 << 20 || (int64_t)N * K >= (int64_t)1 << 40)
+    return fail(MOE_EINVAL, "%s: N=%d must be >= 1, K=%d a multiple of 32 up to 2^20, N*K < 2^40", what, N, K);
+  if (fmt == MOE_MXFP4 ? group != 32 : (group != 32 && group != 64 && group != 128))
+    return fail(MOE_EINVAL, "%s: group=%d (MXFP4: 32; INT4: 32, 64 or 128)", what, group);
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_w4_bytes(int fmt, int N, int K, int group) {
+  const CallRange range_(__func__);
+  return check_w4(fmt, N, K, group, "moe_w4_bytes") ? 0 : moe::w4_bytes(fmt, N, K, group);
+}
+
+int moe_w4_pack(int fmt, const uint8_t* codes, const void* scales, const uint8_t* zeros, int N, int K, int group,
+                void* w, hipStream_t stream) {
+  const CallRange range_(__func__);
+  if (int rc = check_w4(fmt, N, K, group, "moe_w4_pack")) return rc;
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(scales);
+  REQUIRE_PTR(w);
+  REQUIRE(fmt == MOE_INT4 || !zeros, "moe_w4_pack: MXFP4 has no zeros");
+  hipError_t e = moe::launch_w4_pack(fmt, codes, scales, zeros, N, K, group, static_cast<uint8_t*>(w), stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_w4_pack launch");
+}
+
+int moe_w4_linear(int fmt, const void* w, int N, int K, int group, const void* x, int64_t x_ld, int T,
+                  const float* bias, void* y, int64_t y_ld, int ydt, hipStream_t stream) {
+  const CallRange range_(__func__);
+  if (int rc = check_w4(fmt, N, K, group, "moe_w4_linear")) return rc;
+  REQUIRE(T >= 0 && T <= 1 << 20, "moe_w4_linear: T=%d must be in [0, 2^20]", T);
+  REQUIRE(ydt == MOE_F32 || ydt == MOE_BF16, "moe_w4_linear: ydt must be MOE_F32 or MOE_BF16");
+  REQUIRE(x_ld >= K && x_ld % 8 == 0 && x_ld <= 1 << 22, "moe_w4_linear: x_ld=%lld (>= K, a multiple of 8, <= 2^22)",
+          (long long)x_ld);
+  REQUIRE(y_ld >= N, "moe_w4_linear: y_ld=%lld < N=%d", (long long)y_ld, N);
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(y);
+  if (bias) REQUIRE_PTR(bias);
+  moe::W4Args a;
+  a.w = static_cast<const uint8_t*>(w);
+  a.x = static_cast<const uint16_t*>(x);
+  a.bias = bias;
+  a.y = y;
+  a.x_ld = x_ld;
+  a.y_ld = y_ld;
+  a.T = T;
+  a.N = N;
+  a.K = K;
+  a.group = group;
+  hipError_t e = moe::launch_w4_linear(fmt, a, ydt == MOE_BF16, stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_w4_linear launch");
+}
+
+// ---------------------------------------------------------------------------
 size_t moe_grouped_ffn_workspace(int T, int k, int E, int H, int I, int I_shared, int wdt) {
   const CallRange range_(__func__);
   (void)E;

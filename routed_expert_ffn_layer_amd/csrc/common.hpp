@@ -16,7 +16,7 @@ constexpr int kWave = 64;
 
 // W_MXFP4_A8: MXFP4 weights whose gate/up activations are MXFP8 (the native FP4 x
 // FP8 path); the weights and their layout are W_MXFP4's.
-enum WType { W_F32 = 0, W_BF16 = 1, W_MXFP4 = 2, W_MXFP4_A8 = 3 };
+enum WType { W_F32 = 0, W_BF16 = 1, W_MXFP4 = 2, W_MXFP4_A8 = 3, W_INT4 = 4 };
 
 // Everything the grouped FFN kernels need, passed by value.
 struct FfnArgs {

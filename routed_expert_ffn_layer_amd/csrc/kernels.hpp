@@ -58,4 +58,38 @@ hipError_t launch_native_gate_up(const FfnArgs& a, hipStream_t st);
 size_t ffn_workspace_bytes(int wtype, int T, int k, int H, int I, int I_shared);
 size_t ffn_workspace_xq_offset(int T, int k, int I, int I_shared);
 
+// One layer for a few tokens in two kernels (decode_layer.hip).  wtype: 1 bf16, 2 mxfp4.
+constexpr int kDecodeLayerMaxT = 64, kDecodeLayerMaxPairs = 512;
+struct DecodeLayerArgs {
+  const uint8_t* slot_pool;
+  uint64_t slot_stride;
+  const int32_t* slot_of_expert;  // [E], -1: the expert contributes nothing
+  const uint8_t* shared_w;        // nullable
+  const uint16_t* x;              // [T][H] bf16
+  const float* logits;            // [T][E], or null: ids and w are given
+  int32_t* ids;                   // [T][k]
+  float* w;                       // [T][k]
+  uint16_t* h;                    // workspace: [T*k + T][h_ld] bf16
+  void* y;                        // [T][H]
+  int T, k, E, H, I, I_shared, h_ld;
+};
+hipError_t launch_decode_layer(int wtype, const DecodeLayerArgs& a, bool bf16_out, hipStream_t st);
+
+// Linear product with 4-bit weights (w4.hip).
+constexpr int kW4Mxfp4 = 2, kW4Int4 = 4;
+struct W4Args {
+  const uint8_t* w;    // laid out by launch_w4_pack
+  const uint16_t* x;   // rows of K bf16, x_ld elements apart
+  const float* bias;   // [N] or null
+  void* y;             // rows of N, y_ld elements apart
+  int64_t x_ld, y_ld;
+  int T, N, K, group;
+};
+// Bytes of the codes and of the whole laid-out matrix.
+size_t w4_code_bytes(int N, int K);
+size_t w4_bytes(int fmt, int N, int K, int group);
+hipError_t launch_w4_pack(int fmt, const uint8_t* codes, const void* scales, const uint8_t* zeros, int N, int K,
+                          int group, uint8_t* w, hipStream_t st);
+hipError_t launch_w4_linear(int fmt, const W4Args& a, bool bf16_out, hipStream_t st);
+
 }  // namespace moe

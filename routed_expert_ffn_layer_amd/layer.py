@@ -62,6 +62,17 @@ def forward(b: LayerBuffers, logits, x, slot_pool, slot_stride, slot_of_expert, 
     return b.y
 
 
+def forward_decode(b: LayerBuffers, logits, x, slot_pool, slot_stride, slot_of_expert, shared_w=None, stream=None):
+    """The layer of `forward` for a few tokens (T <= 64, T*k <= 512, bf16 or MXFP4
+    weights) in one library call of two kernels; b.topk_ids and b.topk_w are written,
+    or with logits None read as the routing.  The permutation and the expert rows of
+    b are not touched."""
+    moe.moe_layer_decode(b.wdt, slot_pool, slot_stride, slot_of_expert, shared_w,
+                         b.I_shared if shared_w is not None else 0, x, logits, b.T, b.k, b.E, b.H, b.I, b.topk_ids,
+                         b.topk_w, b.y, b.ydt, b.workspace, stream)
+    return b.y
+
+
 def forward_cached(b: LayerBuffers, cache: moe.MoeCache, layer, logits, x, slot_pool, slot_stride, shared_w=None,
                    stream=None):
     """Experts come from the global-LRU slot cache; one FFN pass per cache wave."""

@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "lib", "libmoe.so")
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY, MOE_EHIP, MOE_ENOMEM, MOE_ESTATE = range(7)
-MOE_F32, MOE_BF16, MOE_MXFP4, MOE_MXFP4_A8 = 0, 1, 2, 3
+MOE_F32, MOE_BF16, MOE_MXFP4, MOE_MXFP4_A8, MOE_INT4 = 0, 1, 2, 3, 4
+MOE_LAYER_DECODE_MAX_T, MOE_LAYER_DECODE_MAX_PAIRS = 64, 512
 
 _lib = None
 
@@ -56,7 +57,8 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_last_error", "moe_expert_by
            "moe_cache_lookup_fill_split", "moe_cache_wait_fills", "moe_cache_set_fill_fraction",
            "moe_cache_lookup_fill_inplace", "moe_cache_step_inplace", "moe_grouped_ffn_addr", "moe_route", "moe_cache_resize", "moe_route_project",
            "moe_grouped_ffn_workspace", "moe_grouped_ffn_kind", "moe_mx8_quantize", "moe_grouped_ffn", "moe_grouped_ffn_gate_up", "moe_grouped_ffn_down", "moe_grouped_ffn_noalloc",
-           "moe_combine", "moe_layer_stream_create", "moe_layer_stream_destroy", "moe_layer_stream_fill",
+           "moe_combine", "moe_layer_decode", "moe_layer_decode_workspace", "moe_w4_bytes", "moe_w4_pack",
+           "moe_w4_linear", "moe_layer_stream_create", "moe_layer_stream_destroy", "moe_layer_stream_fill",
            "moe_layer_stream_acquire", "moe_layer_stream_release"]
 
 
@@ -102,6 +104,13 @@ def lib():
     L.moe_grouped_ffn_down.argtypes = ffn_args
     L.moe_grouped_ffn_noalloc.argtypes = [i, P, sz, P, P, i, P, P, P, i, i, i, i, i, P, P, P]
     L.moe_combine.argtypes = [P, P, P, P, i, i, i, P, i, P]
+    L.moe_layer_decode_workspace.restype = sz
+    L.moe_layer_decode_workspace.argtypes = [i, i, i, i, i, i, i]
+    L.moe_layer_decode.argtypes = [i, P, sz, P, P, i, P, P, i, i, i, i, i, P, P, P, i, P, sz, P]
+    L.moe_w4_bytes.restype = sz
+    L.moe_w4_bytes.argtypes = [i, i, i, i]
+    L.moe_w4_pack.argtypes = [i, P, P, P, i, i, i, P, P]
+    L.moe_w4_linear.argtypes = [i, P, i, i, i, P, ctypes.c_int64, i, P, P, ctypes.c_int64, i, P]
     L.moe_layer_stream_create.argtypes = [ctypes.POINTER(LayerStreamDesc), ctypes.POINTER(P)]
     L.moe_layer_stream_destroy.argtypes = [P]
     L.moe_layer_stream_fill.argtypes = [P, i, i]
@@ -226,6 +235,37 @@ def moe_combine(out_rows, topk_w, inv_rows, shared_out, y, ydt, stream=None):
     H = y.shape[-1]
     _check(lib().moe_combine(_ptr(out_rows), _ptr(topk_w), _ptr(inv_rows), _ptr(shared_out), T, k, H, _ptr(y), ydt,
                              _stream(stream)))
+
+
+def moe_layer_decode_workspace(T, k, E, H, I, I_shared, wdt):
+    return int(lib().moe_layer_decode_workspace(T, k, E, H, I, I_shared, wdt))
+
+
+def moe_layer_decode(wdt, slot_pool, slot_stride, slot_of_expert, shared_w, I_shared, x, logits, T, k, E, H, I,
+                     topk_ids, topk_w, y, ydt, workspace, stream=None):
+    """logits None: topk_ids and topk_w are read instead of written."""
+    _check(lib().moe_layer_decode(wdt, _ptr(slot_pool), slot_stride, _ptr(slot_of_expert), _ptr(shared_w), I_shared,
+                                  _ptr(x), _ptr(logits), T, k, E, H, I, _ptr(topk_ids), _ptr(topk_w), _ptr(y), ydt,
+                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def moe_w4_bytes(fmt, N, K, group):
+    return int(lib().moe_w4_bytes(fmt, N, K, group))
+
+
+def moe_w4_pack(fmt, codes, scales, zeros, N, K, group, w, stream=None):
+    _check(lib().moe_w4_pack(fmt, _ptr(codes), _ptr(scales), _ptr(zeros), N, K, group, _ptr(w), _stream(stream)))
+
+
+def moe_w4_linear(fmt, w, N, K, group, x, bias, y, stream=None):
+    """x [T][K] bf16 and y [T][N] (f32 or bf16) with unit stride along their rows."""
+    import torch
+    ydt = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(y.dtype, -1)
+    T = x.shape[0]
+    # the stride of a single row's dimension means nothing
+    x_ld, y_ld = (x.stride(0), y.stride(0)) if T > 1 else (K, N)
+    _check(lib().moe_w4_linear(fmt, _ptr(w), N, K, group, _ptr(x), x_ld, T, _ptr(bias), _ptr(y), y_ld, ydt,
+                               _stream(stream)))
 
 
 class MoeCache:
