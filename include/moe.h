@@ -381,8 +381,9 @@ int moe_combine(const float* out_rows, const float* topk_w, const int32_t* inv_r
  *   y         [T][H] of ydt (MOE_F32 or MOE_BF16)
  *   workspace >= moe_layer_decode_workspace() bytes, written by the call (two calls that
  *             may overlap need one each)
- * bf16 or MXFP4 weights (MOE_EUNSUPPORTED otherwise), T <= MOE_LAYER_DECODE_MAX_T and
- * T*k <= MOE_LAYER_DECODE_MAX_PAIRS (MOE_EUNSUPPORTED beyond: use the separate calls).
+ * bf16 or MXFP4 weights (MOE_EUNSUPPORTED otherwise), T <= MOE_LAYER_DECODE_MAX_T,
+ * T*k <= MOE_LAYER_DECODE_MAX_PAIRS, H <= 65536 and experts under 2 GiB
+ * (MOE_EUNSUPPORTED beyond: use the separate calls).
  * Asynchronous, allocates nothing, may be captured into a graph. */
 #define MOE_LAYER_DECODE_MAX_T 64
 #define MOE_LAYER_DECODE_MAX_PAIRS 512

@@ -197,10 +197,28 @@ int moe_combine(const float* out_rows, const float* topk_w, const int32_t* inv_r
 }
 
 // ---------------------------------------------------------------------------
+namespace {
+
+// Row stride of the intermediate: whole column steps of W2 (MXFP4: 128).
+int decode_h_ld(int I, int I_shared, int wdt) {
+  const int w = I > I_shared ? I : I_shared;
+  return wdt == MOE_MXFP4 ? (w + 127) / 128 * 128 : w;
+}
+
+size_t decode_plan_offset(int T, int k, int I, int I_shared, int wdt) {
+  const size_t rows = (size_t)T * k + (I_shared > 0 ? T : 0);
+  return (rows * decode_h_ld(I, I_shared, wdt) * 2 + 255) / 256 * 256;
+}
+
+}  // namespace
+
 size_t moe_layer_decode_workspace(int T, int k, int E, int H, int I, int I_shared, int wdt) {
   const CallRange range_(__func__);
   if (wdt != MOE_BF16 && wdt != MOE_MXFP4) return 0;
-  return moe_grouped_ffn_workspace(T, k, E, H, I, I_shared, wdt);
+  if (T < 0 || k < 1 || H <= 0 || I <= 0 || I_shared < 0) return 0;
+  (void)E;
+  // the SwiGLU intermediate, then the first kernel's routing for the second
+  return decode_plan_offset(T, k, I, I_shared, wdt) + moe::decode_layer_plan_bytes();
 }
 
 int moe_layer_decode(int wdt, const void* slot_pool, size_t slot_stride, const int32_t* slot_of_expert,
@@ -239,9 +257,13 @@ int moe_layer_decode(int wdt, const void* slot_pool, size_t slot_stride, const i
           "slot_stride=%zu must be >= expert bytes %zu and a multiple of 16", slot_stride, eb);
   if (eb >= (size_t)1 << 31 || (shared_w && moe_expert_bytes(wdt, H, I_shared) >= (size_t)1 << 31))
     return fail(MOE_EUNSUPPORTED, "moe_layer_decode: experts of 2 GiB or more");
-  const size_t need = moe::ffn_workspace_bytes(wdt, T, k, H, I, I_shared);
+  if (H > moe::kDecodeLayerMaxH)
+    return fail(MOE_EUNSUPPORTED, "moe_layer_decode: H=%d beyond %d", H, moe::kDecodeLayerMaxH);
+  const size_t plan_at = decode_plan_offset(T, k, I, I_shared, wdt);
+  const size_t need = plan_at + moe::decode_layer_plan_bytes();
   if (ws_bytes < need) return fail(MOE_ECAPACITY, "workspace %zu bytes < %zu needed", ws_bytes, need);
   moe::DecodeLayerArgs a;
+  a.plan = static_cast<uint8_t*>(workspace) + plan_at;
   a.slot_pool = static_cast<const uint8_t*>(slot_pool);
   a.slot_stride = slot_stride;
   a.slot_of_expert = slot_of_expert;
@@ -258,7 +280,7 @@ int moe_layer_decode(int wdt, const void* slot_pool, size_t slot_stride, const i
   a.H = H;
   a.I = I;
   a.I_shared = I_shared;
-  a.h_ld = I > I_shared ? I : I_shared;
+  a.h_ld = decode_h_ld(I, I_shared, wdt);
   hipError_t e = moe::launch_decode_layer(wdt, a, ydt == MOE_BF16, stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_layer_decode launch");
 }

@@ -13,240 +13,688 @@
 // columns holds the products of all pairs in LDS and adds them there, so neither the
 // expert rows nor the permutation ever reach memory.
 //
+// Pairs are sorted by expert and cut into runs (pairs of one expert that one matrix
+// tile serves); a run's weights stream once past all of its tokens.
+//
 // Every sum has a fixed order (K parts in ascending order, then the pairs of a token in
 // ascending j), so results are the same on every run.
 #include "kernels.hpp"
 #include "stream_tile.hpp"
-#include "topk.hpp"
 
 namespace moe {
 
-constexpr int kDlMaxPairs = kDecodeLayerMaxPairs, kDlMaxT = kDecodeLayerMaxT;
-constexpr int kNoExpert = 0x7fffffff;
-constexpr int kGuWaves = 8, kGuTiles = 2;  // gate/up: waves of a block (K parts), row tiles per work item
-constexpr int kDnWaves = 16;               // down: waves of a block
+constexpr int kDlMaxPairs = kDecodeLayerMaxPairs;
+constexpr int kDlWaves = 16;  // waves of a block, one block per CU
+constexpr int kDlThreads = 64 * kDlWaves;
 
-// Routing of the batch as a block sees it (LDS).
-struct __align__(16) DlPlan {
-  int32_t id[kDlMaxPairs];    // expert of pair p
-  float w[kDlMaxPairs];       // its gate weight
-  int32_t key[kDlMaxPairs];   // the expert if it has a slot, else kNoExpert; padded to a multiple of 4
-  int32_t sorted[kDlMaxPairs];  // pairs by (key, p)
-  int32_t run_n[kDlMaxPairs];   // by position: pairs of the run that begins here, 0 if none does
-  int32_t run_at[kDlMaxPairs];  // first position of run i
-  int32_t slot[1024];
+// A run: pairs of one expert (or tokens of the shared expert) that one matrix tile serves.
+struct __align__(16) DlRun {
+  uint64_t w;  // the expert's weights
+  int32_t at;  // its first position in sorted order (shared expert: its first token)
+  int32_t m;   // pairs
+};
+constexpr int kDlMaxRuns = kDlMaxPairs + kDecodeLayerMaxT;
+
+// What gate/up's first block leaves in the workspace for the second kernel.
+struct __align__(16) DlShared {
+  int32_t runs, pad[3];
+  DlRun run[kDlMaxRuns];        // the shared expert's first
+  int32_t sorted[kDlMaxPairs];  // by position: the pair
+  int32_t valid[kDlMaxPairs];   // by pair: its expert has a slot
 };
 
-// Phase 1: ids, gate weights (and the slot table) into LDS.
+size_t decode_layer_plan_bytes() { return sizeof(DlShared); }
+
+// Routing of the batch as a gate/up block sees it (LDS).
+struct __align__(16) DlPlan {
+  DlRun run[kDlMaxRuns];
+  int32_t id[kDlMaxPairs];   // expert of pair p
+  int32_t key[kDlMaxPairs];  // the same if it has a slot, else -1
+  uint16_t group[1024];      // first position of each expert's pairs
+  uint16_t sorted[kDlMaxPairs];  // by position: the pair
+};
+
+// Largest of v over the wave, in a scalar register: five in-register steps (shifts
+// by 1, 2, 4, 8 inside a row of 16 lanes, then two broadcasts of a row's last lane).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define MOE_DPP_MAX(ctrl, rows) \
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false))
+  MOE_DPP_MAX(0x111, 0xf);  // row_shr:1
+  MOE_DPP_MAX(0x112, 0xf);  // row_shr:2
+  MOE_DPP_MAX(0x114, 0xf);  // row_shr:4
+  MOE_DPP_MAX(0x118, 0xf);  // row_shr:8
+  MOE_DPP_MAX(0x142, 0xa);  // row_bcast:15 into rows 1 and 3
+  MOE_DPP_MAX(0x143, 0xc);  // row_bcast:31 into rows 2 and 3
+#undef MOE_DPP_MAX
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Inclusive prefix sum over the wave, with the same in-register steps.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+#define MOE_DPP_ADD(ctrl, rows) v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false)
+  MOE_DPP_ADD(0x111, 0xf);
+  MOE_DPP_ADD(0x112, 0xf);
+  MOE_DPP_ADD(0x114, 0xf);
+  MOE_DPP_ADD(0x118, 0xf);
+  MOE_DPP_ADD(0x142, 0xa);
+  MOE_DPP_ADD(0x143, 0xc);
+#undef MOE_DPP_ADD
+  return v;
+}
+
+// Top-k of one token by one wave, lane l holding experts 64 i + l as order-preserving
+// keys (zero past E and once taken).  k rounds take the largest key of the wave, the lowest
+// index among equals; with up to 256 experts each lane first sorts its own four (larger
+// first, then lower index), so that a round looks at the heads only, with more it looks
+// for its largest every round (sorting 8 or 16 costs more than it saves).  Then the softmax
+// of the k values.  The rounds stay in registers, and k is small, where a bitwise select
+// takes 32 rounds whatever k is.
 template <int EPL>
-__device__ __forceinline__ void dl_route_t(DlPlan& s, const DecodeLayerArgs& a) {
-  for (int t = threadIdx.x >> 6; t < a.T; t += blockDim.x >> 6)
-    topk_row<EPL>(a.logits + (size_t)t * a.E, a.E, a.k, s.id + t * a.k, s.w + t * a.k);
-}
-
-__device__ __forceinline__ void dl_load_slots(DlPlan& s, const DecodeLayerArgs& a) {
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) s.slot[e] = a.slot_of_expert[e];
-}
-
-// Phase 2: sort the pairs by expert (stable) and cut every expert's pairs into runs of
-// up to 16.  Pair p's position is the number of pairs with a smaller (key, p): n^2 / threads
-// compares of LDS broadcasts.  Returns the number of runs (the same in every thread).
-__device__ __forceinline__ int dl_plan(DlPlan& s, const DecodeLayerArgs& a) {
-  const int n = a.T * a.k, n4 = (n + 3) & ~3, p = threadIdx.x;
-  if (p < n4) {
-    int key = kNoExpert;
-    if (p < n) {
-      const int e = s.id[p];
-      if (e >= 0 && e < a.E && s.slot[e] >= 0) key = e;
-    }
-    s.key[p] = key;
+__device__ __forceinline__ void topk_few(const float* __restrict__ row, int E, int k, int32_t* ids, float* w) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key[EPL];
+  int grp[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = i * 64 + lane;
+    const uint32_t b = e < E ? __float_as_uint(row[e]) : 0u;
+    // larger value, larger key; -0.0 and +0.0 the same
+    key[i] = e >= E ? 0u : (b << 1) == 0u ? 0x80000000u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    grp[i] = i;
   }
-  __syncthreads();
+  constexpr bool SORT = EPL <= 4;
+#pragma unroll
+  for (int i = 1; SORT && i < EPL; ++i)
+#pragma unroll
+    for (int j = i; j > 0; --j) {
+      const bool swap = key[j] > key[j - 1];
+      const uint32_t hi = swap ? key[j] : key[j - 1], lo = swap ? key[j - 1] : key[j];
+      const int gh = swap ? grp[j] : grp[j - 1], gl = swap ? grp[j - 1] : grp[j];
+      key[j - 1] = hi;
+      key[j] = lo;
+      grp[j - 1] = gh;
+      grp[j] = gl;
+    }
+  uint32_t mine = 0;
+  int my_id = 0;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    uint32_t head = key[0];
+    int head_grp = grp[0];
+#pragma unroll
+    for (int i = 1; !SORT && i < EPL; ++i) {
+      head_grp = key[i] > head ? i : head_grp;
+      head = max(head, key[i]);
+    }
+    const uint32_t best = wave_max(head);
+    uint64_t m = __ballot(head == best);
+    if (m & (m - 1)) {  // equal heads: the lowest expert
+      const uint32_t inv = head == best ? 0xffffu - (uint32_t)(head_grp * 64 + lane) : 0u;
+      m = __ballot(inv == wave_max(inv));
+    }
+    const int at = __builtin_ctzll(m);
+    const int id = __builtin_amdgcn_readlane(head_grp, at) * 64 + at;
+    if (lane == at) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if constexpr (SORT) {
+          key[i] = i + 1 < EPL ? key[i + 1] : 0u;
+          grp[i] = i + 1 < EPL ? grp[i + 1] : 0;
+        } else {
+          key[i] = i == head_grp ? 0u : key[i];
+        }
+      }
+    }
+    if (lane == j) {
+      mine = best;
+      my_id = id;
+    }
+  }
+  const float v = __uint_as_float((mine & 0x80000000u) ? mine ^ 0x80000000u : ~mine);
+  const float top = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 0));
+  const float ex = expf(v - top);
+  float sum = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j)
+    sum += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ex), j));
+  if (lane < k) {
+    ids[lane] = my_id;
+    w[lane] = ex / sum;
+  }
+}
+
+template <int EPL>
+__device__ __forceinline__ void dl_route(DlPlan& s, float* w, const DecodeLayerArgs& a) {
+  for (int t = threadIdx.x >> 6; t < a.T; t += kDlWaves)
+    topk_few<EPL>(a.logits + (size_t)t * a.E, a.E, a.k, s.id + t * a.k, w + t * a.k);
+}
+
+// Groups the pairs by expert, in ascending token order, and cuts every expert's pairs into
+// runs of up to P.  Each expert has a bit mask of the tokens that chose it: its count is
+// the mask's population, a pair's place in its group the population below its token, and
+// one scan over the experts (thread e holds expert e) places groups and runs.  Given
+// routing may name an expert twice in one token, which a mask cannot hold: then every
+// pair counts the pairs before it of the same expert instead (n compares each).
+// slots: the slot table; mask: E 64-bit words; part: 2 * kDlWaves words (all LDS).
+// Returns the number of runs, the shared expert's included (the same in every thread); ends
+// with a barrier.
+static_assert(kDlThreads >= 1024 && kDlMaxPairs <= kDlThreads && kDecodeLayerMaxT <= 64, "thread e holds expert e");
+
+__device__ __forceinline__ int dl_plan(DlPlan& s, const int32_t* slots, uint64_t* mask, uint32_t* part,
+                                       const DecodeLayerArgs& a, int P) {
+  const int n = a.T * a.k, p = threadIdx.x, wv = p >> 6, t = p / a.k;
+  int e = -1;
   if (p < n) {
-    const int key = s.key[p];
-    int less = 0, before = 0, same = 0;
-    for (int q = 0; q < n4; q += 4) {
-      const int4 kq = *reinterpret_cast<const int4*>(s.key + q);
-      less += (kq.x < key) + (kq.y < key) + (kq.z < key) + (kq.w < key);
-      same += (kq.x == key) + (kq.y == key) + (kq.z == key) + (kq.w == key);
-      before += (kq.x == key && q < p) + (kq.y == key && q + 1 < p) + (kq.z == key && q + 2 < p) +
-                (kq.w == key && q + 3 < p);
+    const int id = s.id[p];
+    e = id >= 0 && id < a.E && slots[id] >= 0 ? id : -1;
+    s.key[p] = e;
+  }
+  bool twice = false;
+  if (e >= 0) {
+    const uint64_t bit = 1ull << t;
+    twice = (atomicOr(reinterpret_cast<unsigned long long*>(mask + e), bit) & bit) != 0;
+  }
+  twice = __syncthreads_or(twice);
+  // thread e: pairs of expert e in the low half word, its runs in the high one
+  uint32_t count = 0;
+  if (p < a.E) {
+    if (!twice) {
+      count = __popcll(mask[p]);
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < n; ++q) count += s.key[q] == p;
     }
-    const int at = less + before;
-    s.sorted[at] = p;
-    s.run_n[at] = key != kNoExpert && before % 16 == 0 ? min(16, same - before) : 0;
+  }
+  const uint32_t runs_here = (count + P - 1) / P;
+  const uint32_t packed = count | runs_here << 16, scan = wave_scan(packed);
+  if ((p & 63) == 63) part[wv] = scan;
+  __syncthreads();
+  uint32_t base = 0, total = 0;
+#pragma unroll
+  for (int q = 0; q < kDlWaves; ++q) {
+    const uint32_t v = part[q];
+    base += q < wv ? v : 0u;
+    total += v;
+  }
+  base += scan - packed;
+  const int sh_runs = a.shared_w ? (a.T + P - 1) / P : 0;
+  if (p < sh_runs) s.run[p] = DlRun{reinterpret_cast<uint64_t>(a.shared_w), p * P, min(P, a.T - p * P)};
+  if (count > 0) {
+    const uint64_t w = reinterpret_cast<uint64_t>(a.slot_pool) + (uint64_t)slots[p] * a.slot_stride;
+    const int at = base & 0xffff, r = sh_runs + (base >> 16);
+#pragma unroll 1
+    for (int i = 0; i < (int)runs_here; ++i) s.run[r + i] = DlRun{w, at + i * P, min(P, (int)count - i * P)};
+  }
+  if (p < a.E) s.group[p] = base & 0xffff;
+  __syncthreads();
+  if (e >= 0) {
+    int before = 0;
+    if (!twice) {
+      before = __popcll(mask[e] & ((1ull << t) - 1));
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < p; ++q) before += s.key[q] == e;
+    }
+    s.sorted[s.group[e] + before] = (uint16_t)p;
   }
   __syncthreads();
-  int runs = 0;
-  const int lane = p & 63;
-  const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
-  for (int c = 0; c < n; c += 64) {
-    const uint64_t m = __ballot(c + lane < n && s.run_n[c + lane] > 0);
-    if (c + lane == p && ((m >> lane) & 1)) s.run_at[runs + __popcll(m & below)] = p;
-    runs += __popcll(m);
-  }
-  __syncthreads();
-  return runs;
+  return sh_runs + (total >> 16);
 }
 
-template <int WT>
-__device__ __forceinline__ int dl_token_offset(int lane, int n, int ld) {
-  return min(a_token(lane), n - 1) * ld * 2;
+struct RunRef {
+  const uint8_t* w;
+  int at, m;
+};
+__device__ __forceinline__ RunRef read_run(const DlRun* r) {
+  const u32x4 v = *reinterpret_cast<const u32x4*>(r);
+  RunRef o;
+  o.w = (const uint8_t*)((uint64_t)(uint32_t)uniform((int)v[1]) << 32 | (uint32_t)uniform((int)v[0]));
+  o.at = uniform((int)v[2]);
+  o.m = uniform((int)v[3]);
+  return o;
+}
+
+// Copies m token rows (H bf16 each, padded with zeros to `padded` 16-byte pieces) into LDS
+// rows of row_bytes, by `threads` threads of which this is number `me`; token(i) is row
+// i's token.  Four pieces per thread are requested before the first is stored.
+template <typename Token>
+__device__ __forceinline__ void copy_rows(uint8_t* rows, int row_bytes, const uint16_t* x, int H, int m, int me,
+                                          int threads, const Token& token) {
+  const int padded = (row_bytes - 16) / 16, total = m * padded;
+#pragma unroll 1
+  for (int c0 = me; c0 < total; c0 += 4 * threads) {
+    u32x4 v[4];
+    int at[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = min(c0 + j * threads, total - 1), i = c / padded, pc = c - i * padded;
+      at[j] = i * row_bytes + pc * 16;
+      v[j] = ldg16(x + (size_t)token(i) * H + min(pc, H / 8 - 1) * 8);
+      if (pc >= H / 8) v[j] = u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4*>(rows + at[j]) = v[j];  // the last piece may repeat
+  }
 }
 
 // ---------------------------------------------------------------------------
-// Gate/up.  Work items (run, kGuTiles row tiles of W13) are dealt to the blocks in turn;
-// the 8 waves split K, and the block adds their parts in LDS, applies SwiGLU and writes
-// h.  A W13 row tile holds 8 gate rows and the 8 up rows beside them.
+// Gate/up.  The row tiles of W13 of all runs form one list, cut into equal contiguous
+// ranges, one per block (one block of 16 waves per CU), so a block meets few runs and
+// copies each run's token rows into LDS once.  The 16 waves split K (wave w takes column
+// steps w, w + 16, ...) and stream their part of the range through kBufs register buffers
+// of kUnits weight fragments: loads run across tiles and runs, up to 8 KB in flight per
+// wave, and nothing but weights goes through vector memory.  At the end of a tile the
+// block adds the 16 parts in LDS (two buffers, one barrier per tile that does not wait
+// for loads), applies SwiGLU and writes h.  A W13 row tile holds 8 gate rows and the 8
+// up rows beside them.
+//
+// Two things shape the loops.  Every issue requests its loads, past the end from an empty
+// buffer, which reads nothing: were they conditional, the wait for a fragment could not count
+// the younger loads and would drain the pipeline.  And the code is kept short (few
+// buffers, run descriptors ready in LDS, no division): a small launch pays for every
+// line of instructions it fetches for the first time.
 // ---------------------------------------------------------------------------
 template <int WT>
-__global__ __launch_bounds__(64 * kGuWaves) void decode_gate_up(DecodeLayerArgs a) {
-  __shared__ DlPlan s;
-  __shared__ float red[kGuTiles][kGuWaves][256];  // [tile][K part][token][row]
-  const int lane = threadIdx.x & 63, kp = uniform(threadIdx.x >> 6);
-  const int n = a.T * a.k;
-  dl_load_slots(s, a);
-  if (a.logits) {
-    if (a.E <= 64) dl_route_t<1>(s, a);
-    else if (a.E <= 128) dl_route_t<2>(s, a);
-    else if (a.E <= 256) dl_route_t<4>(s, a);
-    else if (a.E <= 512) dl_route_t<8>(s, a);
-    else dl_route_t<16>(s, a);
-  } else {
-    for (int p = threadIdx.x; p < n; p += blockDim.x) s.id[p] = a.ids[p];
+struct GuTune {
+  static constexpr int units = WT == W_BF16 ? 4 : 2, bufs = WT == W_BF16 ? 2 : 4;
+};
+
+// LDS: DlPlan, the parts of two tiles, the slot table with the gate weights and partial
+// ranks, and the token rows.
+constexpr int kDlRouting = (1024 + kDlMaxPairs + kDlWaves) * 4;
+static int gu_row_bytes(int wtype, int H) { return (wtype == W_MXFP4 ? (H + 127) / 128 * 128 : H) * 2 + 16; }
+static constexpr size_t kGuLds = 160 * 1024;
+static size_t gu_red_bytes(int P) { return (size_t)2 * kDlWaves * 256 * ((P + 3) / 4); }
+
+// Byte offsets and size of one expert's matrices (the slot layout of include/moe.h).
+template <int WT>
+struct ExpertShape {
+  int n13, n2, c13, c2, s13, bytes;  // column steps; bytes of W13, W2 codes and W13 scales; the whole
+  __device__ __forceinline__ ExpertShape(int H, int I) {
+    n13 = ksteps<WT>(H);
+    n2 = ksteps<WT>(I);
+    c13 = 2 * I / 16 * n13 * 1024;
+    c2 = H / 16 * n2 * 1024;
+    s13 = WT == W_MXFP4 ? 2 * I / 16 * ((n13 + 15) / 16) * 1024 : 0;
+    bytes = c13 + c2 + s13 + (WT == W_MXFP4 ? H / 16 * ((n2 + 15) / 16) * 1024 : 0);
   }
-  __syncthreads();
-  if (a.logits && blockIdx.x == 0) {
-    for (int p = threadIdx.x; p < n; p += blockDim.x) {
+};
+
+template <int WT, int U>
+struct GuBuf {
+  u32x4 w[U];
+  uint32_t sc[U];
+};
+
+// resident: all T token rows fit the LDS rows and are copied there once, beside the top-k.
+template <int WT>
+__global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, int P, int row_bytes, bool resident) {
+  constexpr int U = GuTune<WT>::units, B = GuTune<WT>::bufs;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  DlPlan& s = *reinterpret_cast<DlPlan*>(lds);
+  float* red = reinterpret_cast<float*>(lds + sizeof(DlPlan));  // [buffer][element v][part][lane]
+  const int red_tile = kDlWaves * 64 * ((P + 3) / 4);
+  int32_t* slots = reinterpret_cast<int32_t*>(lds + sizeof(DlPlan) + (size_t)red_tile * 8);
+  uint8_t* rows = reinterpret_cast<uint8_t*>(slots) + kDlRouting;
+  const int lane = threadIdx.x & 63, g = lane >> 4, kp = uniform(threadIdx.x >> 6);
+  const int n = a.T * a.k, p = threadIdx.x;
+  uint64_t* masks = reinterpret_cast<uint64_t*>(red);  // until the first tile ends: 8 KB
+  {
+    const int my_slot = p < a.E ? a.slot_of_expert[p] : -1;  // E <= 1024 = kDlThreads
+    float* w = reinterpret_cast<float*>(slots + 1024);
+    if (a.logits) {
+      if (a.E <= 64) dl_route<1>(s, w, a);
+      else if (a.E <= 128) dl_route<2>(s, w, a);
+      else if (a.E <= 256) dl_route<4>(s, w, a);
+      else if (a.E <= 512) dl_route<8>(s, w, a);
+      else dl_route<16>(s, w, a);
+    } else if (p < n) {
+      s.id[p] = a.ids[p];
+    }
+    if (p < a.E) {
+      slots[p] = my_slot;
+      masks[p] = 0;
+    }
+    if (resident) {  // few tokens: by the waves that have no top-k to do
+      const int skip = a.T <= kDlWaves / 2 ? a.T * 64 : 0;
+      if (p >= skip)
+        copy_rows(rows, row_bytes, a.x, a.H, a.T, p - skip, kDlThreads - skip, [](int i) { return i; });
+    }
+    __syncthreads();
+    if (a.logits && blockIdx.x == 0 && p < n) {
       a.ids[p] = s.id[p];
-      a.w[p] = s.w[p];
+      a.w[p] = w[p];
     }
   }
-  const int runs = uniform(dl_plan(s, a));
-  const int g_sh = a.shared_w ? (a.I_shared / 8 + kGuTiles - 1) / kGuTiles : 0;
-  const int g_rt = (a.I / 8 + kGuTiles - 1) / kGuTiles;
-  const int sh_items = (a.T + 15) / 16 * g_sh;
-  const int nk = ksteps<WT>(a.H), s0 = kp * nk / kGuWaves, s1 = (kp + 1) * nk / kGuWaves;
-  const __amdgpu_buffer_rsrc_t xbuf = make_rsrc(a.x, (size_t)a.T * a.H * 2);
-  for (int item = blockIdx.x; item < sh_items + runs * g_rt; item += gridDim.x) {
-    const bool shared = item < sh_items;
-    const int it = shared ? item : item - sh_items, per = shared ? g_sh : g_rt;
-    const int run = it / per, tile0 = (it - run * per) * kGuTiles;
-    const int Ie = shared ? a.I_shared : a.I;
-    const int at = shared ? run * 16 : uniform(s.run_at[run]);
-    const int m = shared ? min(16, a.T - at) : uniform(s.run_n[at]);
-    const uint8_t* slot = shared ? a.shared_w : a.slot_pool + (uint64_t)uniform(s.slot[uniform(s.key[uniform(s.sorted[at])])]) * a.slot_stride;
-    const Mat w = w13_mat<WT>(slot, a.H, Ie);
-    const int tok = min(a_token(lane), m - 1);
-    const int row_off = (shared ? at + tok : s.sorted[at + tok] / a.k) * a.H * 2;
-    const int tiles = min(kGuTiles, Ie / 8 - tile0);
-    for (int t = 0; t < tiles; ++t) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-      stream_tile<WT>(w, tile0 + t, s0, s1, xbuf, row_off, acc);
+  const int runs = uniform(dl_plan(s, slots, masks, reinterpret_cast<uint32_t*>(slots + 1024 + kDlMaxPairs), a, P));
+  if (blockIdx.x == 0) {
+    DlShared* out = static_cast<DlShared*>(a.plan);
+    if (p == 0) out->runs = runs;
+    if (p < runs) out->run[p] = s.run[p];
+    if (p < n) {
+      out->sorted[p] = s.sorted[p];
+      out->valid[p] = s.key[p] >= 0;
+    }
+  }
+  const int sh_runs = a.shared_w ? (a.T + P - 1) / P : 0;
+  const int sh_tiles = a.I_shared / 8, rt_tiles = a.I / 8;
+  const int sh_total = sh_runs * sh_tiles, total = sh_total + (runs - sh_runs) * rt_tiles;
+  const int lo = (int)((int64_t)blockIdx.x * total / gridDim.x), hi = (int)((int64_t)(blockIdx.x + 1) * total / gridDim.x);
+  if (lo >= hi) return;
+  const ExpertShape<WT> rt(a.H, a.I), sh(a.H, a.I_shared);
+  const int nk = rt.n13, nu = (nk + kDlWaves - 1) / kDlWaves, nc = (nu + U - 1) / U;  // steps, units, chunks of a tile
+  const int run0 = lo < sh_total ? lo / max(sh_tiles, 1) : sh_runs + (lo - sh_total) / rt_tiles;
+  const int tile0 = lo < sh_total ? lo - run0 * sh_tiles : lo - sh_total - (run0 - sh_runs) * rt_tiles;
+
+  // Issue side: the next chunk to request.
+  int iq = lo, ic = 0, irun = run0 - 1, itile = tile0, iper = 0, isc = 0;
+  const uint8_t* iw = nullptr;
+  int ibytes = 0;
+  auto issue_run = [&]() {
+    ++irun;
+    const bool shared = irun < sh_runs;
+    iw = read_run(s.run + irun).w;
+    ibytes = shared ? sh.bytes : rt.bytes;
+    iper = shared ? sh_tiles : rt_tiles;
+    isc = shared ? sh.c13 + sh.c2 : rt.c13 + rt.c2;
+  };
+  issue_run();
+  auto issue = [&](GuBuf<WT, U>& b) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int step = (ic * U + u) * kDlWaves + kp;
+      const bool live = iq < hi && step < nk;
+      const __amdgpu_buffer_rsrc_t buf = make_rsrc(iw, live ? ibytes : 0);
+      b.w[u] = bld16(buf, lane * 16, live ? (itile * nk + step) * 1024 : 0);
+      if constexpr (WT == W_MXFP4)
+        b.sc[u] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+            buf, lane * 16, live ? isc + (itile * ((nk + 15) / 16) + step / 16) * 1024 + step % 16 / 4 * 4 : 0, 0);
+    }
+    if (++ic == nc) {
+      ic = 0;
+      ++iq;
+      if (++itile == iper && iq < hi) {
+        itile = 0;
+        issue_run();
+      }
+    }
+  };
+  GuBuf<WT, U> buf[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) issue(buf[b]);
+
+  // Compute side.
+  int q = lo, cc = 0, run = run0 - 1, tile = tile0, per = 0, at = 0, m = 0, half = 0;
+  const uint8_t* my_row = rows;
+  auto enter_run = [&]() {  // the token rows of the next run into LDS
+    ++run;
+    const RunRef r = read_run(s.run + run);
+    at = r.at;
+    m = r.m;
+    per = run < sh_runs ? sh_tiles : rt_tiles;
+    auto token = [&](int i) { return run < sh_runs ? at + i : s.sorted[at + i] / a.k; };
+    const int i = min(a_token(lane), m - 1);
+    if (resident) {
+      my_row = rows + token(i) * row_bytes;
+      return;
+    }
+    copy_rows(rows, row_bytes, a.x, a.H, m, p, kDlThreads, token);
+    my_row = rows + i * row_bytes;
+    lds_barrier();
+  };
+  enter_run();
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (;;) {
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int step = (cc * U + u) * kDlWaves + kp;
+        if (step < nk) {
+          if constexpr (WT == W_BF16) {
+            acc = mfma16(*reinterpret_cast<const u32x4*>(my_row + step * 64 + 16 * g), as_bf16x8(buf[b].w[u]), acc);
+          } else {
+            const float sc = scale_of_word(buf[b].sc[u], step);
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+              acc = mfma16(*reinterpret_cast<const u32x4*>(my_row + step * 256 + 64 * g + 16 * f),
+                           fp4x8_to_bf16x8(buf[b].w[u][f], sc), acc);
+          }
+        }
+      }
+      issue(buf[b]);
+      if (++cc < nc) continue;
+      cc = 0;
+      float* part = red + half * red_tile;
+      const int nv = (m + 3) / 4;
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        if (4 * v < m) red[t][kp][64 * v + lane] = acc[v];
-    }
-    __syncthreads();
-    for (int o = threadIdx.x; o < tiles * m * 8; o += 64 * kGuWaves) {
-      const int t = o / (m * 8), i = o / 8 - t * m, c = o & 7;
-      float gate = 0.f, up = 0.f;
+        if (v < nv) part[(v * kDlWaves + kp) * 64 + lane] = acc[v];
+      acc = f32x4{0.f, 0.f, 0.f, 0.f};
+      lds_barrier();
+      // element v of tile q by wave (q nv + v) % 16: lane = (token % 4, stored row)
+      const int v = (kp - q * nv) & (kDlWaves - 1);
+      if (v < nv) {
+        float sum = 0.f;
 #pragma unroll
-      for (int q = 0; q < kGuWaves; ++q) {
-        gate += red[t][q][16 * i + c];
-        up += red[t][q][16 * i + c + 8];
+        for (int w = 0; w < kDlWaves; ++w) sum += part[(v * kDlWaves + w) * 64 + lane];
+        const float up = __shfl_xor(sum, 8, 64);
+        const int i = g + 4 * v;
+        if (i < m && (lane & 8) == 0) {
+          const int row = run < sh_runs ? n + at + i : s.sorted[at + i];
+          uint16_t* h = a.h + (size_t)row * a.h_ld;
+          h[tile * 8 + (lane & 7)] = f32_to_bf16_rne(silu_f32(sum) * up);
+          if (WT == W_MXFP4 && tile + 1 == per)  // zeros up to the next whole column step
+            for (int z = per * 8; z % 128; z += 8) h[z + (lane & 7)] = 0;
+        }
       }
-      const int row = shared ? n + at + i : s.sorted[at + i];
-      a.h[(size_t)row * a.h_ld + (tile0 + t) * 8 + c] = f32_to_bf16_rne(silu_f32(gate) * up);
+      half ^= 1;
+      if (++q >= hi) return;
+      if (++tile == per) {
+        tile = 0;
+        enter_run();
+      }
     }
-    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
-// Down and combine.  A block owns one row tile of W2 (16 columns of y) for every pair:
-// its waves take (run, K part) tasks in turn, the products of all pairs meet in LDS, and
-// the block adds each token's pairs in ascending j.
+// Down and combine.  A block owns one row tile of W2 (16 columns of y) for every pair.
+// K is cut into `parts` (a power of two up to 16): wave w takes part w % parts of the runs
+// w / parts, w / parts + 16 / parts, ... and streams them (weights, and the run's h
+// fragments, which come from L2) without meeting the others; the parts of all pairs
+// collect in LDS, and the block adds the parts, then each token's pairs in ascending j.
 // ---------------------------------------------------------------------------
+template <int WT>
+struct DnTune {
+  static constexpr int units = WT == W_BF16 ? 4 : 2;
+};
+
+template <int WT, int U>
+struct DnBuf {
+  u32x4 w[U], h[U][StepFrags<WT>::value];
+  uint32_t sc[U];
+};
+
 template <int WT, bool BF16OUT>
-__global__ __launch_bounds__(64 * kDnWaves) void decode_down(DecodeLayerArgs a, int parts) {
-  __shared__ DlPlan s;
+__global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int P, int log_parts) {
+  constexpr int U = DnTune<WT>::units, NB = StepFrags<WT>::value;
+  __shared__ DlShared s;
+  __shared__ float w[kDlMaxPairs];
   extern __shared__ float val[];  // [part][pair, then shared token][16]
-  const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
-  const int n = a.T * a.k, rows = n + (a.shared_w ? a.T : 0);
-  dl_load_slots(s, a);
-  for (int p = threadIdx.x; p < n; p += blockDim.x) {
-    s.id[p] = a.ids[p];
-    s.w[p] = a.w[p];
+  const int lane = threadIdx.x & 63, g = lane >> 4, wv = uniform(threadIdx.x >> 6);
+  const int n = a.T * a.k, nrows = n + (a.shared_w ? a.T : 0), p = threadIdx.x;
+  const int sh_runs = a.shared_w ? (a.T + P - 1) / P : 0;
+  const int tile = blockIdx.x;
+  const DlShared* in = static_cast<const DlShared*>(a.plan);
+  const int runs = in->runs;
+  {
+    const int pr = min(p, n + sh_runs - 1), pp = min(p, n - 1);  // all loads at once, none conditional
+    const u32x4 r = ldg16(in->run + pr);
+    const int so = in->sorted[pp], va = in->valid[pp];
+    const float wp = a.w[pp];
+    if (p < n + sh_runs) *reinterpret_cast<u32x4*>(s.run + p) = r;
+    if (p < n) {
+      s.sorted[p] = so;
+      s.valid[p] = va;
+      w[p] = wp;
+    }
   }
   __syncthreads();
-  const int runs = uniform(dl_plan(s, a));
-  const int sh_runs = a.shared_w ? (a.T + 15) / 16 : 0;
-  const int tile = blockIdx.x;
-  const __amdgpu_buffer_rsrc_t hbuf = make_rsrc(a.h, (size_t)rows * a.h_ld * 2);
-  for (int task = wv; task < (sh_runs + runs) * parts; task += kDnWaves) {
-    const int r0 = task / parts, part = task - r0 * parts;
+  const int hbytes = nrows * a.h_ld * 2;
+  const ExpertShape<WT> rt(a.H, a.I), sh(a.H, a.I_shared);
+  const int parts = 1 << log_parts, part = wv & (parts - 1), stride = kDlWaves >> log_parts;
+
+  // Issue side: run ir, steps is .. ie-1 of it.
+  int ir = (wv >> log_parts) - stride, is = 0, ie = 0, i_off = 0, i_w2 = 0, i_sc = 0;
+  const uint8_t* iw = nullptr;
+  int ibytes = 0;
+  auto issue_run = [&]() {
+    ir += stride;
+    const int r0 = min(ir, runs - 1);
     const bool shared = r0 < sh_runs;
-    const int run = shared ? r0 : r0 - sh_runs;
-    const int at = shared ? run * 16 : uniform(s.run_at[run]);
-    const int m = shared ? min(16, a.T - at) : uniform(s.run_n[at]);
-    const int Ie = shared ? a.I_shared : a.I;
-    const uint8_t* slot = shared ? a.shared_w : a.slot_pool + (uint64_t)uniform(s.slot[uniform(s.key[uniform(s.sorted[at])])]) * a.slot_stride;
-    const Mat w = w2_mat<WT>(slot, a.H, Ie);
-    const int tok = min(a_token(lane), m - 1);
-    const int row_off = (shared ? n + at + tok : s.sorted[at + tok]) * a.h_ld * 2;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    stream_tile<WT>(w, tile, part * w.nK / parts, (part + 1) * w.nK / parts, hbuf, row_off, acc);
+    const RunRef r = read_run(s.run + r0);
+    const int nk = shared ? sh.n2 : rt.n2;
+    iw = r.w;
+    ibytes = shared ? sh.bytes : rt.bytes;
+    i_w2 = (shared ? sh.c13 : rt.c13) + tile * nk * 1024;
+    i_sc = (shared ? sh.c13 + sh.c2 + sh.s13 : rt.c13 + rt.c2 + rt.s13) + tile * ((nk + 15) / 16) * 1024;
+    is = part * nk >> log_parts;
+    ie = (part + 1) * nk >> log_parts;
+    const int i = min(a_token(lane), r.m - 1);
+    i_off = (shared ? n + r.at + i : s.sorted[r.at + i]) * a.h_ld * 2 + (WT == W_MXFP4 ? 64 : 16) * g;
+  };
+  auto issue = [&](DnBuf<WT, U>& b) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int i = (lane >> 4) + 4 * v;
-      if (i < m) {
-        const int row = shared ? n + at + i : s.sorted[at + i];
-        val[((size_t)part * rows + row) * 16 + (lane & 15)] = acc[v];
+    for (int u = 0; u < U; ++u) {
+      const int step = is + u;
+      const bool live = ir < runs && step < ie;
+      const __amdgpu_buffer_rsrc_t wbuf = make_rsrc(iw, live ? ibytes : 0), hbuf = make_rsrc(a.h, live ? hbytes : 0);
+      b.w[u] = bld16(wbuf, lane * 16, live ? i_w2 + step * 1024 : 0);
+      if constexpr (WT == W_MXFP4)
+        b.sc[u] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+            wbuf, lane * 16, live ? i_sc + step / 16 * 1024 + step % 16 / 4 * 4 : 0, 0);
+#pragma unroll
+      for (int f = 0; f < NB; ++f) b.h[u][f] = bld16(hbuf, i_off + 16 * f, live ? step * (WT == W_MXFP4 ? 256 : 64) : 0);
+    }
+    is += U;
+    if (is >= ie && ir < runs) issue_run();
+  };
+  int cr = wv >> log_parts, cs = 0, ce = 0, at = 0, m = 0;
+  if (cr < runs) {
+    auto enter_run = [&]() {
+      const RunRef r = read_run(s.run + cr);
+      at = r.at;
+      m = r.m;
+      const int nk = cr < sh_runs ? sh.n2 : rt.n2;
+      cs = part * nk >> log_parts;
+      ce = (part + 1) * nk >> log_parts;
+    };
+    DnBuf<WT, U> buf[2];
+    issue_run();
+    issue(buf[0]);
+    issue(buf[1]);
+    enter_run();
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (bool more = true; more;) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (cs + u < ce) {
+            if constexpr (WT == W_BF16) {
+              acc = mfma16(buf[b].h[u][0], as_bf16x8(buf[b].w[u]), acc);
+            } else {
+              const float sc = scale_of_word(buf[b].sc[u], cs + u);
+#pragma unroll
+              for (int f = 0; f < 4; ++f) acc = mfma16(buf[b].h[u][f], fp4x8_to_bf16x8(buf[b].w[u][f], sc), acc);
+            }
+          }
+        }
+        issue(buf[b]);
+        cs += U;
+        if (cs < ce) continue;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int i = g + 4 * v;
+          if (i < m) {
+            const int row = cr < sh_runs ? n + at + i : s.sorted[at + i];
+            val[(part * nrows + row) * 16 + (lane & 15)] = acc[v];
+          }
+        }
+        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        cr += stride;
+        more = cr < runs;
+        if (!more) break;
+        enter_run();
       }
     }
   }
   __syncthreads();
-  for (int o = threadIdx.x; o < a.T * 16; o += blockDim.x) {
-    const int t = o >> 4, c = o & 15;
+  if (parts > 1) {
+    for (int o = threadIdx.x; o < nrows * 16; o += kDlThreads) {
+      float d = val[o];
+#pragma unroll 4
+      for (int q = 1; q < parts; ++q) d += val[q * nrows * 16 + o];
+      val[o] = d;
+    }
+    __syncthreads();
+  }
+  for (int o = threadIdx.x; o < a.T * 16; o += kDlThreads) {
+    const int tk = o >> 4, c = o & 15;
     float y = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-      const int p = t * a.k + j;
-      if (s.key[p] == kNoExpert) continue;
-      float d = 0.f;
-      for (int q = 0; q < parts; ++q) d += val[((size_t)q * rows + p) * 16 + c];
-      y = fmaf(s.w[p], d, y);
+#pragma unroll 1
+    for (int j0 = 0; j0 < a.k; j0 += 4) {  // four pairs' LDS reads at a time
+      float d[4], wj[4];
+      int ok[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int pr = tk * a.k + min(j0 + j, a.k - 1);
+        ok[j] = j0 + j < a.k ? s.valid[pr] : 0;
+        wj[j] = w[pr];
+        d[j] = val[pr * 16 + c];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (ok[j]) y = fmaf(wj[j], d[j], y);
     }
-    if (a.shared_w) {
-      float d = 0.f;
-      for (int q = 0; q < parts; ++q) d += val[((size_t)q * rows + n + t) * 16 + c];
-      y += d;
-    }
-    const size_t at = (size_t)t * a.H + tile * 16 + c;
+    if (a.shared_w) y += val[(n + tk) * 16 + c];
+    const size_t out = (size_t)tk * a.H + tile * 16 + c;
     if (BF16OUT)
-      static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_rne(y);
+      static_cast<uint16_t*>(a.y)[out] = f32_to_bf16_rne(y);
     else
-      static_cast<float*>(a.y)[at] = y;
+      static_cast<float*>(a.y)[out] = y;
   }
 }
 
 template <int WT>
 static hipError_t launch_t(const DecodeLayerArgs& a, bool bf16_out, hipStream_t st) {
-  // an upper bound on the work items: every pair its own run
-  const int64_t n = (int64_t)a.T * a.k;
-  const int64_t bound = (a.shared_w ? (int64_t)(a.T + 15) / 16 * ((a.I_shared / 8 + kGuTiles - 1) / kGuTiles) : 0) +
-                        n * ((a.I / 8 + kGuTiles - 1) / kGuTiles);
-  const unsigned grid = (unsigned)(bound < 512 ? bound : 512);
-  hipLaunchKernelGGL(decode_gate_up<WT>, dim3(grid), dim3(64 * kGuWaves), 0, st, a);
+  const int n = a.T * a.k;
+  const int rb = gu_row_bytes(WT, a.H);
+  int P = 16;
+  while (P > 1 && sizeof(DlPlan) + gu_red_bytes(P) + kDlRouting + (size_t)P * rb > kGuLds) --P;
+  const bool resident = a.T <= P;
+  if (P > a.T) P = a.T;  // a token routes to an expert once, unless the caller's routing repeats it
+  const size_t lds = sizeof(DlPlan) + gu_red_bytes(P) + kDlRouting + (size_t)P * rb;
+  const int64_t bound = (a.shared_w ? (int64_t)(a.T + P - 1) / P * (a.I_shared / 8) : 0) + (int64_t)n * (a.I / 8);
+  const unsigned grid = (unsigned)(bound < 256 ? bound : 256);
+  hipLaunchKernelGGL(decode_gate_up<WT>, dim3(grid), dim3(kDlThreads), lds, st, a, P, rb, resident);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int parts = n <= 16 ? 2 : 1;
-  const size_t lds = (size_t)parts * (n + (a.shared_w ? a.T : 0)) * 64;
-  const dim3 g2(a.H / 16), b2(64 * kDnWaves);
+  // K parts of the down product: enough (run, part) tasks for the waves when every pair is
+  // a run of its own, each part at least one chunk of steps long, and LDS for the parts
+  const int nrows = n + (a.shared_w ? a.T : 0);
+  const int ks = WT == W_MXFP4 ? 128 : 32;
+  int nk = (a.I + ks - 1) / ks;
+  if (a.shared_w && (a.I_shared + ks - 1) / ks < nk) nk = (a.I_shared + ks - 1) / ks;
+  int lp = 0;
+  while (lp < 4 && (2 << lp) * DnTune<WT>::units <= nk && (nrows << lp) < 64 && (size_t)(2 << lp) * nrows * 64 <= 65536) ++lp;
+  const size_t lds2 = (size_t)(nrows << lp) * 64;
+  const dim3 g2(a.H / 16), b2(kDlThreads);
   if (bf16_out)
-    hipLaunchKernelGGL((decode_down<WT, true>), g2, b2, lds, st, a, parts);
+    hipLaunchKernelGGL((decode_down<WT, true>), g2, b2, lds2, st, a, P, lp);
   else
-    hipLaunchKernelGGL((decode_down<WT, false>), g2, b2, lds, st, a, parts);
+    hipLaunchKernelGGL((decode_down<WT, false>), g2, b2, lds2, st, a, P, lp);
   return hipGetLastError();
 }
 

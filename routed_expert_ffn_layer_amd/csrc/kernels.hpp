@@ -70,9 +70,12 @@ struct DecodeLayerArgs {
   int32_t* ids;                   // [T][k]
   float* w;                       // [T][k]
   uint16_t* h;                    // workspace: [T*k + T][h_ld] bf16
+  void* plan;                     // workspace: decode_layer_plan_bytes()
   void* y;                        // [T][H]
   int T, k, E, H, I, I_shared, h_ld;
 };
+size_t decode_layer_plan_bytes();
+constexpr int kDecodeLayerMaxH = 65536;  // one token row fits the gate/up kernel's LDS
 hipError_t launch_decode_layer(int wtype, const DecodeLayerArgs& a, bool bf16_out, hipStream_t st);
 
 // Linear product with 4-bit weights (w4.hip).

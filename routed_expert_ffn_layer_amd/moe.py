@@ -125,14 +125,27 @@ def _check(rc):
         raise MoeError(rc, lib().moe_last_error().decode())
 
 
+_torch_mod = None
+
+
+def _torch():
+    global _torch_mod
+    if _torch_mod is None:
+        import torch
+        torch.cuda.init()
+        _torch_mod = torch
+    return _torch_mod
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        # the current stream of the current device: torch.cuda.current_stream() without its
+        # Python object (2.6 us a call against 0.3, as long as a small kernel)
+        return ctypes.c_void_p(_torch()._C._cuda_getCurrentRawStream(_torch_mod.cuda.current_device()))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
