@@ -26,6 +26,7 @@ namespace moe {
 constexpr int kDlMaxPairs = kDecodeLayerMaxPairs;
 constexpr int kDlWaves = 16;  // waves of a block, one block per CU
 constexpr int kDlThreads = 64 * kDlWaves;
+constexpr int kDlOneQuadT = 8;  // batches whose down runs hold up to 4 pairs, larger ones up to 8
 
 // A run: pairs of one expert (or tokens of the shared expert) that one matrix tile serves.
 struct __align__(16) DlRun {
@@ -38,7 +39,7 @@ constexpr int kDlMaxRuns = kDlMaxPairs + kDecodeLayerMaxT;
 // What gate/up's first block leaves in the workspace for the second kernel.
 struct __align__(16) DlShared {
   int32_t runs, pad[3];
-  DlRun run[kDlMaxRuns];        // the shared expert's first
+  DlRun run[kDlMaxRuns];        // cut for the second kernel; the shared expert's first
   int32_t sorted[kDlMaxPairs];  // by position: the pair
   int32_t valid[kDlMaxPairs];   // by pair: its expert has a slot
 };
@@ -90,14 +91,14 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 // of the k values.  The rounds stay in registers, and k is small, where a bitwise select
 // takes 32 rounds whatever k is.
 template <int EPL>
-__device__ __forceinline__ void topk_few(const float* __restrict__ row, int E, int k, int32_t* ids, float* w) {
+__device__ __forceinline__ void topk_few(const float (&row)[EPL], int E, int k, int32_t* ids, float* w) {
   const int lane = threadIdx.x & 63;
   uint32_t key[EPL];
   int grp[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = i * 64 + lane;
-    const uint32_t b = e < E ? __float_as_uint(row[e]) : 0u;
+    const uint32_t b = __float_as_uint(row[i]);
     // larger value, larger key; -0.0 and +0.0 the same
     key[i] = e >= E ? 0u : (b << 1) == 0u ? 0x80000000u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
     grp[i] = i;
@@ -163,14 +164,31 @@ __device__ __forceinline__ void topk_few(const float* __restrict__ row, int E, i
   }
 }
 
+// Tokens w, w + 16, ... by wave w; a row is requested before the one ahead of it is searched.
 template <int EPL>
 __device__ __forceinline__ void dl_route(DlPlan& s, float* w, const DecodeLayerArgs& a) {
-  for (int t = threadIdx.x >> 6; t < a.T; t += kDlWaves)
-    topk_few<EPL>(a.logits + (size_t)t * a.E, a.E, a.k, s.id + t * a.k, w + t * a.k);
+  const int lane = threadIdx.x & 63;
+  float row[EPL], next[EPL];
+  auto load = [&](float(&r)[EPL], int t) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = min(i * 64 + lane, a.E - 1);
+      r[i] = a.logits[(size_t)min(t, a.T - 1) * a.E + e];
+    }
+  };
+  int t = threadIdx.x >> 6;
+  load(row, t);
+#pragma unroll 1
+  for (; t < a.T; t += kDlWaves) {
+    load(next, t + kDlWaves);
+    topk_few<EPL>(row, a.E, a.k, s.id + t * a.k, w + t * a.k);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) row[i] = next[i];
+  }
 }
 
 // Groups the pairs by expert, in ascending token order, and cuts every expert's pairs into
-// runs of up to P.  Each expert has a bit mask of the tokens that chose it: its count is
+// runs of up to P (and, for the second kernel, of up to P2 into `out`, where given).  Each expert has a bit mask of the tokens that chose it: its count is
 // the mask's population, a pair's place in its group the population below its token, and
 // one scan over the experts (thread e holds expert e) places groups and runs.  Given
 // routing may name an expert twice in one token, which a mask cannot hold: then every
@@ -181,7 +199,7 @@ __device__ __forceinline__ void dl_route(DlPlan& s, float* w, const DecodeLayerA
 static_assert(kDlThreads >= 1024 && kDlMaxPairs <= kDlThreads && kDecodeLayerMaxT <= 64, "thread e holds expert e");
 
 __device__ __forceinline__ int dl_plan(DlPlan& s, const int32_t* slots, uint64_t* mask, uint32_t* part,
-                                       const DecodeLayerArgs& a, int P) {
+                                       const DecodeLayerArgs& a, int P, int P2, DlShared* out) {
   const int n = a.T * a.k, p = threadIdx.x, wv = p >> 6, t = p / a.k;
   int e = -1;
   if (p < n) {
@@ -195,7 +213,8 @@ __device__ __forceinline__ int dl_plan(DlPlan& s, const int32_t* slots, uint64_t
     twice = (atomicOr(reinterpret_cast<unsigned long long*>(mask + e), bit) & bit) != 0;
   }
   twice = __syncthreads_or(twice);
-  // thread e: pairs of expert e in the low half word, its runs in the high one
+  // thread e: pairs of expert e, its runs, and its runs for the second kernel, 10 bits each
+  // (sums of at most 512)
   uint32_t count = 0;
   if (p < a.E) {
     if (!twice) {
@@ -205,8 +224,8 @@ __device__ __forceinline__ int dl_plan(DlPlan& s, const int32_t* slots, uint64_t
       for (int q = 0; q < n; ++q) count += s.key[q] == p;
     }
   }
-  const uint32_t runs_here = (count + P - 1) / P;
-  const uint32_t packed = count | runs_here << 16, scan = wave_scan(packed);
+  const uint32_t runs1 = (count + P - 1) / P, runs2 = (count + P2 - 1) / P2;
+  const uint32_t packed = count | runs1 << 10 | runs2 << 20, scan = wave_scan(packed);
   if ((p & 63) == 63) part[wv] = scan;
   __syncthreads();
   uint32_t base = 0, total = 0;
@@ -217,15 +236,20 @@ __device__ __forceinline__ int dl_plan(DlPlan& s, const int32_t* slots, uint64_t
     total += v;
   }
   base += scan - packed;
-  const int sh_runs = a.shared_w ? (a.T + P - 1) / P : 0;
-  if (p < sh_runs) s.run[p] = DlRun{reinterpret_cast<uint64_t>(a.shared_w), p * P, min(P, a.T - p * P)};
+  const int sh1 = a.shared_w ? (a.T + P - 1) / P : 0, sh2 = a.shared_w ? (a.T + P2 - 1) / P2 : 0;
+  const uint64_t shared_w = reinterpret_cast<uint64_t>(a.shared_w);
+  if (p < sh1) s.run[p] = DlRun{shared_w, p * P, min(P, a.T - p * P)};
+  if (out && p < sh2) out->run[p] = DlRun{shared_w, p * P2, min(P2, a.T - p * P2)};
   if (count > 0) {
     const uint64_t w = reinterpret_cast<uint64_t>(a.slot_pool) + (uint64_t)slots[p] * a.slot_stride;
-    const int at = base & 0xffff, r = sh_runs + (base >> 16);
+    const int at = base & 0x3ff, r1 = sh1 + (base >> 10 & 0x3ff), r2 = sh2 + (base >> 20);
 #pragma unroll 1
-    for (int i = 0; i < (int)runs_here; ++i) s.run[r + i] = DlRun{w, at + i * P, min(P, (int)count - i * P)};
+    for (int i = 0; i < (int)runs1; ++i) s.run[r1 + i] = DlRun{w, at + i * P, min(P, (int)count - i * P)};
+#pragma unroll 1
+    for (int i = 0; out && i < (int)runs2; ++i) out->run[r2 + i] = DlRun{w, at + i * P2, min(P2, (int)count - i * P2)};
   }
-  if (p < a.E) s.group[p] = base & 0xffff;
+  if (out && p == 0) out->runs = sh2 + (total >> 20);
+  if (p < a.E) s.group[p] = base & 0x3ff;
   __syncthreads();
   if (e >= 0) {
     int before = 0;
@@ -238,7 +262,7 @@ __device__ __forceinline__ int dl_plan(DlPlan& s, const int32_t* slots, uint64_t
     s.sorted[s.group[e] + before] = (uint16_t)p;
   }
   __syncthreads();
-  return sh_runs + (total >> 16);
+  return sh1 + (total >> 10 & 0x3ff);
 }
 
 struct RunRef {
@@ -280,8 +304,9 @@ __device__ __forceinline__ void copy_rows(uint8_t* rows, int row_bytes, const ui
 // ---------------------------------------------------------------------------
 // Gate/up.  The row tiles of W13 of all runs form one list, cut into equal contiguous
 // ranges, one per block (one block of 16 waves per CU), so a block meets few runs and
-// copies each run's token rows into LDS once.  The 16 waves split K (wave w takes column
-// steps w, w + 16, ...) and stream their part of the range through kBufs register buffers
+// copies each run's token rows into LDS once.  The 16 waves split K (bf16: wave w takes
+// column steps w, w + 16, ...; MXFP4: an even number of consecutive steps, so that one
+// scale word serves two) and stream their part of the range through kBufs register buffers
 // of kUnits weight fragments: loads run across tiles and runs, up to 8 KB in flight per
 // wave, and nothing but weights goes through vector memory.  At the end of a tile the
 // block adds the 16 parts in LDS (two buffers, one barrier per tile that does not wait
@@ -323,12 +348,13 @@ struct ExpertShape {
 template <int WT, int U>
 struct GuBuf {
   u32x4 w[U];
-  uint32_t sc[U];
+  uint32_t sc[U / 2];
 };
+static_assert(GuTune<W_MXFP4>::units % 2 == 0, "scale words serve pairs of steps");
 
 // resident: all T token rows fit the LDS rows and are copied there once, beside the top-k.
 template <int WT>
-__global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, int P, int row_bytes, bool resident) {
+__global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, int P, int P2, int row_bytes, bool resident) {
   constexpr int U = GuTune<WT>::units, B = GuTune<WT>::bufs;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   DlPlan& s = *reinterpret_cast<DlPlan*>(lds);
@@ -366,15 +392,12 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
       a.w[p] = w[p];
     }
   }
-  const int runs = uniform(dl_plan(s, slots, masks, reinterpret_cast<uint32_t*>(slots + 1024 + kDlMaxPairs), a, P));
-  if (blockIdx.x == 0) {
-    DlShared* out = static_cast<DlShared*>(a.plan);
-    if (p == 0) out->runs = runs;
-    if (p < runs) out->run[p] = s.run[p];
-    if (p < n) {
-      out->sorted[p] = s.sorted[p];
-      out->valid[p] = s.key[p] >= 0;
-    }
+  DlShared* out = blockIdx.x == 0 ? static_cast<DlShared*>(a.plan) : nullptr;
+  const int runs =
+      uniform(dl_plan(s, slots, masks, reinterpret_cast<uint32_t*>(slots + 1024 + kDlMaxPairs), a, P, P2, out));
+  if (out && p < n) {
+    out->sorted[p] = s.sorted[p];
+    out->valid[p] = s.key[p] >= 0;
   }
   const int sh_runs = a.shared_w ? (a.T + P - 1) / P : 0;
   const int sh_tiles = a.I_shared / 8, rt_tiles = a.I / 8;
@@ -383,6 +406,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
   if (lo >= hi) return;
   const ExpertShape<WT> rt(a.H, a.I), sh(a.H, a.I_shared);
   const int nk = rt.n13, nu = (nk + kDlWaves - 1) / kDlWaves, nc = (nu + U - 1) / U;  // steps, units, chunks of a tile
+  const int step0 = WT == W_MXFP4 ? kp * nc * U : kp, step_by = WT == W_MXFP4 ? 1 : kDlWaves;
   const int run0 = lo < sh_total ? lo / max(sh_tiles, 1) : sh_runs + (lo - sh_total) / rt_tiles;
   const int tile0 = lo < sh_total ? lo - run0 * sh_tiles : lo - sh_total - (run0 - sh_runs) * rt_tiles;
 
@@ -402,13 +426,14 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
   auto issue = [&](GuBuf<WT, U>& b) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int step = (ic * U + u) * kDlWaves + kp;
+      const int step = step0 + (ic * U + u) * step_by;
       const bool live = iq < hi && step < nk;
       const __amdgpu_buffer_rsrc_t buf = make_rsrc(iw, live ? ibytes : 0);
       b.w[u] = bld16(buf, lane * 16, live ? (itile * nk + step) * 1024 : 0);
-      if constexpr (WT == W_MXFP4)
-        b.sc[u] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-            buf, lane * 16, live ? isc + (itile * ((nk + 15) / 16) + step / 16) * 1024 + step % 16 / 4 * 4 : 0, 0);
+      if constexpr (WT == W_MXFP4)  // steps in pairs from an even one: one word
+        if (u % 2 == 0)
+          b.sc[u / 2] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+              buf, lane * 16, live ? isc + (itile * ((nk + 15) / 16) + step / 16) * 1024 + step % 16 / 4 * 4 : 0, 0);
     }
     if (++ic == nc) {
       ic = 0;
@@ -449,12 +474,12 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
     for (int b = 0; b < B; ++b) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int step = (cc * U + u) * kDlWaves + kp;
+        const int step = step0 + (cc * U + u) * step_by;
         if (step < nk) {
           if constexpr (WT == W_BF16) {
             acc = mfma16(*reinterpret_cast<const u32x4*>(my_row + step * 64 + 16 * g), as_bf16x8(buf[b].w[u]), acc);
           } else {
-            const float sc = scale_of_word(buf[b].sc[u], step);
+            const float sc = scale_of_word(buf[b].sc[u / 2], step);
 #pragma unroll
             for (int f = 0; f < 4; ++f)
               acc = mfma16(*reinterpret_cast<const u32x4*>(my_row + step * 256 + 64 * g + 16 * f),
@@ -504,21 +529,41 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
 // w / parts, w / parts + 16 / parts, ... and streams them (weights, and the run's h
 // fragments, which come from L2) without meeting the others; the parts of all pairs
 // collect in LDS, and the block adds the parts, then each token's pairs in ascending j.
+//
+// The vector memory pipe, not HBM, is what a 4-bit stream runs into here (an h fragment
+// for every 256 bytes of codes: with four fragment loads and a scale load beside each code
+// load the MXFP4 kernel took 86 us at 64 tokens, 28 us of them its codes).  Runs are
+// therefore short, 4 VN tokens, and one load brings four fragments: in a quad of lanes,
+// which would hold the same token four times (VN = 1) or two tokens twice (VN = 2), each
+// lane loads another fragment, and quad permutes hand them to the products.
 // ---------------------------------------------------------------------------
-template <int WT>
+template <int WT, int VN>
 struct DnTune {
-  static constexpr int units = WT == W_BF16 ? 4 : 2;
+  static constexpr int units = WT == W_BF16 ? 4 : 2;  // steps of a chunk
+  static constexpr int groups = WT == W_BF16 ? 1 : 2;  // of four fragments: bf16 one per step, MXFP4 four
+  static constexpr int bufs = VN == 1 ? 4 : 3;
 };
 
-template <int WT, int U>
+template <int WT, int VN>
 struct DnBuf {
-  u32x4 w[U], h[U][StepFrags<WT>::value];
-  uint32_t sc[U];
+  u32x4 w[DnTune<WT, VN>::units], h[DnTune<WT, VN>::groups][VN];
+  uint32_t sc;
 };
 
-template <int WT, bool BF16OUT>
-__global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int P, int log_parts) {
-  constexpr int U = DnTune<WT>::units, NB = StepFrags<WT>::value;
+// Fragment f of a group for every row of the operand, from the quads' loads.
+template <int VN, int F>
+__device__ __forceinline__ u32x4 quad_fragment(const u32x4 (&h)[VN]) {
+  constexpr int a = VN == 1 ? F : 2 * (F & 1), b = VN == 1 ? F : a + 1;
+  const u32x4 v = h[VN == 1 ? 0 : F / 2];
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], a | b << 2 | a << 4 | b << 6, 0xf, 0xf, true);
+  return o;
+}
+
+template <int WT, int VN, bool BF16OUT>
+__global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int log_parts) {
+  constexpr int U = DnTune<WT, VN>::units, NG = DnTune<WT, VN>::groups, B = DnTune<WT, VN>::bufs, P = 4 * VN;
   __shared__ DlShared s;
   __shared__ float w[kDlMaxPairs];
   extern __shared__ float val[];  // [part][pair, then shared token][16]
@@ -544,9 +589,15 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
   const int hbytes = nrows * a.h_ld * 2;
   const ExpertShape<WT> rt(a.H, a.I), sh(a.H, a.I_shared);
   const int parts = 1 << log_parts, part = wv & (parts - 1), stride = kDlWaves >> log_parts;
+  // a part is whole chunks of U steps
+  auto part_steps = [&](int nk, int& from, int& to) {
+    const int chunks = (nk + U - 1) / U;
+    from = (part * chunks >> log_parts) * U;
+    to = min(((part + 1) * chunks >> log_parts) * U, nk);
+  };
 
   // Issue side: run ir, steps is .. ie-1 of it.
-  int ir = (wv >> log_parts) - stride, is = 0, ie = 0, i_off = 0, i_w2 = 0, i_sc = 0;
+  int ir = (wv >> log_parts) - stride, is = 0, ie = 0, i_off[VN], i_w2 = 0, i_sc = 0;
   const uint8_t* iw = nullptr;
   int ibytes = 0;
   auto issue_run = [&]() {
@@ -559,12 +610,17 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
     ibytes = shared ? sh.bytes : rt.bytes;
     i_w2 = (shared ? sh.c13 : rt.c13) + tile * nk * 1024;
     i_sc = (shared ? sh.c13 + sh.c2 + sh.s13 : rt.c13 + rt.c2 + rt.s13) + tile * ((nk + 15) / 16) * 1024;
-    is = part * nk >> log_parts;
-    ie = (part + 1) * nk >> log_parts;
-    const int i = min(a_token(lane), r.m - 1);
-    i_off = (shared ? n + r.at + i : s.sorted[r.at + i]) * a.h_ld * 2 + (WT == W_MXFP4 ? 64 : 16) * g;
+    part_steps(nk, is, ie);
+    // this lane's load l: token `tok`, fragment f (bf16: 64 bytes a step; MXFP4: blocks of 64 bytes)
+    const int j = lane & 3, tok = ((lane & 15) >> 2) + (VN == 2 ? 4 * (j & 1) : 0), i = min(tok, r.m - 1);
+    const int row = (shared ? n + r.at + i : s.sorted[r.at + i]) * a.h_ld * 2;
+#pragma unroll
+    for (int l = 0; l < VN; ++l) {
+      const int f = VN == 1 ? j : 2 * l + (j >> 1);
+      i_off[l] = row + (WT == W_MXFP4 ? 64 * g + 16 * f : 16 * g + 64 * f);
+    }
   };
-  auto issue = [&](DnBuf<WT, U>& b) {
+  auto issue = [&](DnBuf<WT, VN>& b) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int step = is + u;
@@ -572,10 +628,13 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
       const __amdgpu_buffer_rsrc_t wbuf = make_rsrc(iw, live ? ibytes : 0), hbuf = make_rsrc(a.h, live ? hbytes : 0);
       b.w[u] = bld16(wbuf, lane * 16, live ? i_w2 + step * 1024 : 0);
       if constexpr (WT == W_MXFP4)
-        b.sc[u] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-            wbuf, lane * 16, live ? i_sc + step / 16 * 1024 + step % 16 / 4 * 4 : 0, 0);
+        if (u == 0)
+          b.sc = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+              wbuf, lane * 16, live ? i_sc + step / 16 * 1024 + step % 16 / 4 * 4 : 0, 0);
+      if (u < NG) {
 #pragma unroll
-      for (int f = 0; f < NB; ++f) b.h[u][f] = bld16(hbuf, i_off + 16 * f, live ? step * (WT == W_MXFP4 ? 256 : 64) : 0);
+        for (int l = 0; l < VN; ++l) b.h[u][l] = bld16(hbuf, i_off[l], live ? step * (WT == W_MXFP4 ? 256 : 64) : 0);
+      }
     }
     is += U;
     if (is >= ie && ir < runs) issue_run();
@@ -586,28 +645,33 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
       const RunRef r = read_run(s.run + cr);
       at = r.at;
       m = r.m;
-      const int nk = cr < sh_runs ? sh.n2 : rt.n2;
-      cs = part * nk >> log_parts;
-      ce = (part + 1) * nk >> log_parts;
+      part_steps(cr < sh_runs ? sh.n2 : rt.n2, cs, ce);
     };
-    DnBuf<WT, U> buf[2];
+    DnBuf<WT, VN> buf[B];
     issue_run();
-    issue(buf[0]);
-    issue(buf[1]);
+#pragma unroll
+    for (int b = 0; b < B; ++b) issue(buf[b]);
     enter_run();
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     for (bool more = true; more;) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < B; ++b) {
+        if constexpr (WT == W_BF16) {
+          const DnBuf<WT, VN>& c = buf[b];
+          acc = mfma16(quad_fragment<VN, 0>(c.h[0]), as_bf16x8(c.w[0]), acc);
+          if (cs + 1 < ce) acc = mfma16(quad_fragment<VN, 1>(c.h[0]), as_bf16x8(c.w[1]), acc);
+          if (cs + 2 < ce) acc = mfma16(quad_fragment<VN, 2>(c.h[0]), as_bf16x8(c.w[2]), acc);
+          if (cs + 3 < ce) acc = mfma16(quad_fragment<VN, 3>(c.h[0]), as_bf16x8(c.w[3]), acc);
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (cs + u < ce) {
-            if constexpr (WT == W_BF16) {
-              acc = mfma16(buf[b].h[u][0], as_bf16x8(buf[b].w[u]), acc);
-            } else {
-              const float sc = scale_of_word(buf[b].sc[u], cs + u);
-#pragma unroll
-              for (int f = 0; f < 4; ++f) acc = mfma16(buf[b].h[u][f], fp4x8_to_bf16x8(buf[b].w[u][f], sc), acc);
+          for (int u = 0; u < U; ++u) {
+            if (cs + u < ce) {
+              const DnBuf<WT, VN>& c = buf[b];
+              const float sc = scale_of_word(c.sc, cs + u);
+              acc = mfma16(quad_fragment<VN, 0>(c.h[u]), fp4x8_to_bf16x8(c.w[u][0], sc), acc);
+              acc = mfma16(quad_fragment<VN, 1>(c.h[u]), fp4x8_to_bf16x8(c.w[u][1], sc), acc);
+              acc = mfma16(quad_fragment<VN, 2>(c.h[u]), fp4x8_to_bf16x8(c.w[u][2], sc), acc);
+              acc = mfma16(quad_fragment<VN, 3>(c.h[u]), fp4x8_to_bf16x8(c.w[u][3], sc), acc);
             }
           }
         }
@@ -615,7 +679,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
         cs += U;
         if (cs < ce) continue;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
+        for (int v = 0; v < VN; ++v) {
           const int i = g + 4 * v;
           if (i < m) {
             const int row = cr < sh_runs ? n + at + i : s.sorted[at + i];
@@ -667,6 +731,25 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
   }
 }
 
+template <int WT, int VN>
+static hipError_t launch_down(const DecodeLayerArgs& a, bool bf16_out, hipStream_t st) {
+  // K parts of the down product: enough (run, part) tasks for the waves when every pair is
+  // a run of its own, each part at least one chunk of steps long, and LDS for the parts
+  const int nrows = a.T * a.k + (a.shared_w ? a.T : 0);
+  const int ks = (WT == W_MXFP4 ? 128 : 32) * DnTune<WT, VN>::units;
+  int chunks = (a.I + ks - 1) / ks;
+  if (a.shared_w && (a.I_shared + ks - 1) / ks < chunks) chunks = (a.I_shared + ks - 1) / ks;
+  int lp = 0;
+  while (lp < 4 && 2 << lp <= chunks && nrows << lp < 64 && (size_t)(nrows << lp) * 128 <= 65536) ++lp;
+  const size_t lds = (size_t)(nrows << lp) * 64;
+  const dim3 grid(a.H / 16), block(kDlThreads);
+  if (bf16_out)
+    hipLaunchKernelGGL((decode_down<WT, VN, true>), grid, block, lds, st, a, lp);
+  else
+    hipLaunchKernelGGL((decode_down<WT, VN, false>), grid, block, lds, st, a, lp);
+  return hipGetLastError();
+}
+
 template <int WT>
 static hipError_t launch_t(const DecodeLayerArgs& a, bool bf16_out, hipStream_t st) {
   const int n = a.T * a.k;
@@ -678,24 +761,11 @@ static hipError_t launch_t(const DecodeLayerArgs& a, bool bf16_out, hipStream_t 
   const size_t lds = sizeof(DlPlan) + gu_red_bytes(P) + kDlRouting + (size_t)P * rb;
   const int64_t bound = (a.shared_w ? (int64_t)(a.T + P - 1) / P * (a.I_shared / 8) : 0) + (int64_t)n * (a.I / 8);
   const unsigned grid = (unsigned)(bound < 256 ? bound : 256);
-  hipLaunchKernelGGL(decode_gate_up<WT>, dim3(grid), dim3(kDlThreads), lds, st, a, P, rb, resident);
-  hipError_t e = hipGetLastError();
+  const int vn = a.T <= kDlOneQuadT ? 1 : 2;
+  hipLaunchKernelGGL(decode_gate_up<WT>, dim3(grid), dim3(kDlThreads), lds, st, a, P, 4 * vn, rb, resident);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // K parts of the down product: enough (run, part) tasks for the waves when every pair is
-  // a run of its own, each part at least one chunk of steps long, and LDS for the parts
-  const int nrows = n + (a.shared_w ? a.T : 0);
-  const int ks = WT == W_MXFP4 ? 128 : 32;
-  int nk = (a.I + ks - 1) / ks;
-  if (a.shared_w && (a.I_shared + ks - 1) / ks < nk) nk = (a.I_shared + ks - 1) / ks;
-  int lp = 0;
-  while (lp < 4 && (2 << lp) * DnTune<WT>::units <= nk && (nrows << lp) < 64 && (size_t)(2 << lp) * nrows * 64 <= 65536) ++lp;
-  const size_t lds2 = (size_t)(nrows << lp) * 64;
-  const dim3 g2(a.H / 16), b2(kDlThreads);
-  if (bf16_out)
-    hipLaunchKernelGGL((decode_down<WT, true>), g2, b2, lds2, st, a, P, lp);
-  else
-    hipLaunchKernelGGL((decode_down<WT, false>), g2, b2, lds2, st, a, P, lp);
-  return hipGetLastError();
+  return vn == 1 ? launch_down<WT, 1>(a, bf16_out, st) : launch_down<WT, 2>(a, bf16_out, st);
 }
 
 hipError_t launch_decode_layer(int wtype, const DecodeLayerArgs& a, bool bf16_out, hipStream_t st) {
