@@ -20,12 +20,14 @@
 // gives q exactly, two per instruction.
 //   sum_k x W = sum over groups s * (sum_k x q - z sum_k x)
 // and sum_k x over the same 32 columns is one more MFMA with an all-ones operand.
+#include <type_traits>
+
 #include "kernels.hpp"
 #include "stream_tile.hpp"
 
 namespace moe {
 
-constexpr int kW4Waves = 8;
+constexpr int kW4WideTiles = 1024;  // row tiles from which 17 or more tokens take the wide kernel
 
 size_t w4_code_bytes(int N, int K) { return (size_t)((N + 15) / 16) * ((K + 127) / 128) * 1024; }
 
@@ -125,8 +127,7 @@ hipError_t launch_w4_pack(int fmt, const uint8_t* codes, const void* scales, con
 }
 
 // ---------------------------------------------------------------------------
-// Product.  A block owns one row tile for up to 16 tokens; its waves split K and the
-// block adds their parts in LDS in ascending order.
+// Product.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ bf16x8 int4x8_to_bf16x8(uint32_t w) {
   const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
@@ -141,85 +142,407 @@ __device__ __forceinline__ bf16x8 int4x8_to_bf16x8(uint32_t w) {
 __device__ __forceinline__ float f16_lo(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)w); }
 __device__ __forceinline__ float f16_hi(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16)); }
 
-template <int FMT, int G, bool BF16OUT>
-__global__ __launch_bounds__(64 * kW4Waves) void w4_linear_kernel(W4Args a) {
-  __shared__ float red[kW4Waves][256];
-  const int lane = threadIdx.x & 63, kp = uniform(threadIdx.x >> 6), g = lane >> 4, r = lane & 15;
-  const int tile = blockIdx.x;
-  const int t0 = blockIdx.y * 16, m = min(16, a.T - t0);
-  const int nk = (a.K + 127) / 128, s0 = kp * nk / kW4Waves, s1 = (kp + 1) * nk / kW4Waves;
-  const size_t rt = (a.N + 15) / 16;
-  const uint8_t* scales = a.w + rt * nk * 1024;
-  const __amdgpu_buffer_rsrc_t xbuf = make_rsrc(a.x + (size_t)t0 * a.x_ld, ((size_t)(m - 1) * a.x_ld + a.K) * 2);
-  const int row_off = min(a_token(lane), m - 1) * (int)a.x_ld * 2;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+
+// Parameters of two consecutive column steps (the first one even): words of 32 bits per
+// lane, this lane's weight row.  MXFP4: one word of E8M0 bytes.  INT4: 128 / G words a step.
+template <int FMT, int G>
+struct W4Params {
+  static constexpr int words = FMT == kW4Mxfp4 ? 1 : 256 / G;
+  uint32_t v[words];
+};
+
+// Byte offsets of a row tile's codes and parameters, per tile.
+struct W4Shape {
+  int nk, code_tile, par_tile;
+  size_t par_at;
+  __device__ __forceinline__ W4Shape(int fmt, int N, int K, int G) {
+    nk = (K + 127) / 128;
+    code_tile = nk * 1024;
+    par_at = (size_t)((N + 15) / 16) * code_tile;
+    par_tile = fmt == kW4Mxfp4 ? (nk + 15) / 16 * 1024 : ((K + G - 1) / G + 3) / 4 * 256;
+  }
+};
+
+// Loads the parameters of steps `step`, `step` + 1 of a tile whose parameters are `buf`.
+template <int FMT, int G>
+__device__ __forceinline__ void load_params(W4Params<FMT, G>& p, __amdgpu_buffer_rsrc_t buf, int step, bool live) {
+  const int lane = threadIdx.x & 63;
   if constexpr (FMT == kW4Mxfp4) {
-    Mat w;
-    w.nK = nk;
-    w.nKs = (nk + 15) / 16;
-    w.K = a.K;
-    w.codes = make_rsrc(a.w + (size_t)tile * nk * 1024, (size_t)nk * 1024);
-    w.scales = make_rsrc(scales + (size_t)tile * w.nKs * 1024, (size_t)w.nKs * 1024);
-    stream_tile<W_MXFP4>(w, 0, s0, s1, xbuf, row_off, acc);
+    p.v[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(buf, lane * 16, live ? step / 16 * 1024 + step % 16 / 4 * 4 : 0, 0);
   } else {
-    const int groups = (a.K + G - 1) / G, nb = (groups + 3) / 4;
-    const __amdgpu_buffer_rsrc_t codes = make_rsrc(a.w + (size_t)tile * nk * 1024, (size_t)nk * 1024);
-    const uint32_t* par = reinterpret_cast<const uint32_t*>(scales + (size_t)tile * nb * 256) + r * 4;
-    const u32x4 one4 = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-    constexpr int B = G / 32;  // MFMAs per group
-    for (int s = s0; s < s1; ++s) {
-      const u32x4 q = bld16(codes, lane * 16, s * 1024);
-      f32x4 d = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
+    // word (group % 4) of block group / 4, 16 bytes a row
+    const int vo = (lane & 15) * 16;
+    if constexpr (G == 128) {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                                                    buf, vo, live ? step / 4 * 256 + step % 4 * 4 : 0, 0));
+      p.v[0] = v[0];
+      p.v[1] = v[1];
+    } else {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int o = frag_offset<W_INT4>(s, b, g, a.K);
-        const u32x4 x = bld16(xbuf, o == kPastEnd ? kPastEnd : row_off + o, 0);
-        d = mfma16(x, int4x8_to_bf16x8(q[b]), d);
-        xs = mfma16(x, as_bf16x8(one4), xs);
-        if (b % B == B - 1) {
-          const int grp = min((s * 128 + b * 32) / G, groups - 1);
-          const uint32_t p = par[grp / 4 * 64 + grp % 4];
-          const float sc = f16_lo(p), z = f16_hi(p);
+      for (int i = 0; i < W4Params<FMT, G>::words / 4; ++i) {
+        const u32x4 v = bld16(buf, vo, live ? (step * (128 / G) / 4 + i) * 256 : 0);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[v] = fmaf(sc, fmaf(-z, xs[v], d[v]), acc[v]);
-          d = xs = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < 4; ++j) p.v[4 * i + j] = v[j];
+      }
+    }
+  }
+}
+
+// acc[r][nt] += x . W^T over step u (0 or 1) of a pair of steps, for R row tiles (codes
+// w[r], parameters p[r]) and NT token tiles; frag(nt, m) is the token fragment m of the
+// step.  INT4: a group's products and activation sums are formed first (d, xs), then
+// scale (d - zero xs) is added to the f32 accumulator; VN of a tile's elements hold tokens.
+template <int FMT, int G, int R, int NT, int VN, typename Frag>
+__device__ __forceinline__ void w4_step(f32x4 (&acc)[R][NT], const u32x4 (&w)[R],
+                                        const W4Params<FMT, G> (&p)[R], int u, int step, const Frag& frag) {
+  if constexpr (FMT == kW4Mxfp4) {
+    float sc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) sc[r] = scale_of_word(p[r].v[0], step);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      u32x4 x[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[nt] = frag(nt, m);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bf16x8 b = fp4x8_to_bf16x8(w[r][m], sc[r]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[r][nt] = mfma16(x[nt], b, acc[r][nt]);
+      }
+    }
+  } else {
+    constexpr int B = G / 32;  // products per group
+    const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    f32x4 d[R][NT], xs[NT];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      u32x4 x[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        x[nt] = frag(nt, m);
+        xs[nt] = mfma16(x[nt], as_bf16x8(ones), m % B ? xs[nt] : zero);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bf16x8 b = int4x8_to_bf16x8(w[r][m]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) d[r][nt] = mfma16(x[nt], b, m % B ? d[r][nt] : zero);
+      }
+      if (m % B == B - 1) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t pw = p[r].v[(4 * u + m) / B];
+          const float sc = f16_lo(pw), z = f16_hi(pw);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int v = 0; v < VN; ++v) acc[r][nt][v] = fmaf(sc, fmaf(-z, xs[nt][v], d[r][nt][v]), acc[r][nt][v]);
         }
       }
     }
   }
-#pragma unroll
-  for (int v = 0; v < 4; ++v) red[kp][64 * v + lane] = acc[v];
-  __syncthreads();
-  const int o = threadIdx.x, t = o >> 4;
-  if (o >= 256 || t >= m) return;
-  const int64_t col = (int64_t)tile * 16 + (o & 15);
-  if (col >= a.N) return;
-  float y = 0.f;
-#pragma unroll
-  for (int q = 0; q < kW4Waves; ++q) y += red[q][o];
+}
+
+template <bool BF16OUT>
+__device__ __forceinline__ void store_y(const W4Args& a, int64_t row, int64_t col, float y) {
   if (a.bias) y += a.bias[col];
-  const size_t at = (size_t)(t0 + t) * a.y_ld + col;
   if (BF16OUT)
-    static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_rne(y);
+    static_cast<uint16_t*>(a.y)[row * a.y_ld + col] = f32_to_bf16_rne(y);
   else
-    static_cast<float*>(a.y)[at] = y;
+    static_cast<float*>(a.y)[row * a.y_ld + col] = y;
+}
+
+// Up to 16 tokens.  The waves of a block split K in pairs of column steps, so a wave's token
+// fragments are the same for every row tile: it keeps them in registers (NC pairs of steps;
+// NC = 0: K too long, they are read again for every tile) and streams the codes of the
+// block's contiguous range of row tiles through a few buffers of two steps.  At the end
+// of a tile the block adds the waves' parts in LDS, in ascending order (two buffers, one
+// barrier per tile, which waits for no load).  Up to 4 VN tokens, in a quad of lanes the
+// same token would be held 4 / VN times: there each lane loads another fragment, and quad
+// permutes hand them to the products (VN = 4: every lane its own).
+template <int VN, int NC>
+struct W4Bufs {  // as many as the registers of 16 waves hold
+  static constexpr int value = NC == 0 || (NC == 2 && VN == 4) ? 2 : VN == 4 ? 3 : 4;
+};
+
+template <int VN>
+__device__ __forceinline__ u32x4 quad_pick(const u32x4 (&x)[VN], int m) {
+  if constexpr (VN == 4) return x[m];
+  const int lo = VN == 1 ? m : 2 * (m & 1), hi = VN == 1 ? m : lo + 1;
+  const u32x4 v = x[VN == 1 ? 0 : m / 2];
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // the permute is an immediate of the instruction
+    switch (lo * 4 + hi) {
+      case 0: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0x00, 0xf, 0xf, true); break;
+      case 5: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0x55, 0xf, 0xf, true); break;
+      case 10: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0xaa, 0xf, 0xf, true); break;
+      case 15: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0xff, 0xf, 0xf, true); break;
+      case 1: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0x44, 0xf, 0xf, true); break;
+      default: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0xee, 0xf, 0xf, true); break;
+    }
+  }
+  return o;
+}
+
+template <int FMT, int G, int VN, int NC, bool BF16OUT>
+__global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
+  constexpr int NX = NC ? NC : 1, B = W4Bufs<VN, NC>::value;
+  extern __shared__ float red[];  // [buffer][element v][part][lane]
+  const int lane = threadIdx.x & 63, g = lane >> 4, kp = uniform(threadIdx.x >> 6), waves = uniform(blockDim.x >> 6);
+  const int t0 = blockIdx.y * 16, m = min(16, a.T - t0), j = lane & 3, q4 = (lane & 15) >> 2;
+  const W4Shape sh(FMT, a.N, a.K, G);
+  const int tiles = (a.N + 15) / 16;
+  const int lo = (int)((int64_t)blockIdx.x * tiles / gridDim.x), hi = (int)((int64_t)(blockIdx.x + 1) * tiles / gridDim.x);
+  const int step0 = kp * nc * 2;
+
+  // Token fragments: load l of a step holds fragment f of token tok for this lane.
+  const int tok = min(q4 + 4 * (VN == 1 ? 0 : VN == 2 ? (j & 1) : j), m - 1);
+  const __amdgpu_buffer_rsrc_t xbuf = make_rsrc(a.x + (size_t)t0 * a.x_ld, ((size_t)(m - 1) * a.x_ld + a.K) * 2);
+  const int x_row = tok * (int)a.x_ld * 2;
+  auto load_x = [&](u32x4(&x)[VN], int step) {
+#pragma unroll
+    for (int l = 0; l < VN; ++l) {
+      const int f = VN == 1 ? j : VN == 2 ? 2 * l + (j >> 1) : l;
+      const int o = frag_offset<FMT>(step, f, g, a.K);
+      x[l] = bld16(xbuf, o == kPastEnd ? kPastEnd : x_row + o, 0);
+    }
+  };
+  u32x4 xr[NX][2][VN];
+  if constexpr (NC > 0) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) load_x(xr[c][u], step0 + 2 * c + u);
+  }
+
+  struct Buf {
+    u32x4 w[2][1];
+    W4Params<FMT, G> p[1];
+    u32x4 x[NC ? 1 : 2][VN];
+  };
+  Buf buf[B];
+  int iq = lo, ic = 0;
+  auto issue = [&](Buf& b) {
+    const int step = step0 + 2 * ic;
+    const uint8_t* codes = a.w + (size_t)iq * sh.code_tile;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool live = iq < hi && step + u < sh.nk;
+      b.w[u][0] = bld16(make_rsrc(codes, live ? sh.code_tile : 0), lane * 16, live ? (step + u) * 1024 : 0);
+    }
+    const bool live = iq < hi && step < sh.nk;
+    load_params<FMT, G>(b.p[0], make_rsrc(a.w + sh.par_at + (size_t)iq * sh.par_tile, live ? sh.par_tile : 0), step, live);
+    if constexpr (NC == 0) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) load_x(b.x[u], step + u);
+    }
+    if (++ic == nc) {
+      ic = 0;
+      ++iq;
+    }
+  };
+#pragma unroll
+  for (int b = 0; b < B; ++b) issue(buf[b]);
+  f32x4 acc[1][1];
+  acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int q = lo, half = 0;
+  const int red_tile = VN * waves * 64;
+  auto compute = [&](const Buf& b, int c, const u32x4(&x0)[VN], const u32x4(&x1)[VN]) {
+    const int step = step0 + 2 * c;
+    if (step < sh.nk) w4_step<FMT, G, 1, 1, VN>(acc, b.w[0], b.p, 0, step, [&](int, int f) { return quad_pick<VN>(x0, f); });
+    if (step + 1 < sh.nk)
+      w4_step<FMT, G, 1, 1, VN>(acc, b.w[1], b.p, 1, step + 1, [&](int, int f) { return quad_pick<VN>(x1, f); });
+  };
+  auto tile_end = [&]() {  // returns whether a tile is left
+    float* part = red + half * red_tile;
+#pragma unroll
+    for (int v = 0; v < VN; ++v) part[(v * waves + kp) * 64 + lane] = acc[0][0][v];
+    acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    lds_barrier();
+    // element v by wave (q VN + v) % waves: lane = (token % 4, row)
+    for (int v = 0; v < VN; ++v) {
+      if ((q * VN + v) % waves != kp) continue;
+      float y = 0.f;
+      for (int w = 0; w < waves; ++w) y += part[(v * waves + w) * 64 + lane];
+      const int64_t col = (int64_t)q * 16 + (lane & 15);
+      if (g + 4 * v < m && col < a.N) store_y<BF16OUT>(a, t0 + g + 4 * v, col, y);
+    }
+    half ^= 1;
+    return ++q < hi;
+  };
+  if constexpr (NC > 0) {
+    // buffer b holds chunk b % NC of its tile
+    static_assert(B % NX == 0 && B <= 4, "a tile's chunks stay on fixed buffers");
+    auto turn = [&](auto bi) {
+      constexpr int b = decltype(bi)::value;
+      if constexpr (b < B) {
+        compute(buf[b], b % NX, xr[b % NX][0], xr[b % NX][1]);
+        issue(buf[b]);
+        if constexpr (b % NX == NX - 1) return tile_end();
+      }
+      return true;
+    };
+    while (turn(std::integral_constant<int, 0>()) && turn(std::integral_constant<int, 1>()) &&
+           turn(std::integral_constant<int, 2>()) && turn(std::integral_constant<int, 3>())) {
+    }
+  } else {
+    int c = 0;
+    auto turn = [&](Buf& b) {
+      compute(b, c, b.x[0], b.x[1]);
+      issue(b);
+      if (++c < nc) return true;
+      c = 0;
+      return tile_end();
+    };
+    while (turn(buf[0]) && turn(buf[1])) {
+    }
+  }
+}
+
+// 17 to 64 tokens and many rows.  A wave owns R row tiles over the whole of K, a block of 8
+// waves 128 R rows; the tokens pass through LDS in slices of two column steps shared by the
+// waves (two buffers: the next slice travels to registers while this one is multiplied,
+// one barrier per slice), each fragment read from LDS serving R products.  The codes of
+// the next two slices are in flight in registers.
+constexpr int kWideR = 2, kWideWaves = 8;
+
+template <int FMT, int G, int NT, bool BF16OUT>
+__global__ __launch_bounds__(64 * kWideWaves) void w4_wide(W4Args a) {
+  constexpr int R = kWideR, ROWS = 16 * NT, LD = 512 + 16;
+  constexpr int PIECES = ROWS * 32 / (64 * kWideWaves);  // 16-byte pieces of a slice per thread
+  __shared__ __attribute__((aligned(16))) uint8_t xs[2][ROWS * LD];
+  const int lane = threadIdx.x & 63, g = lane >> 4, wv = uniform(threadIdx.x >> 6);
+  const int t0 = blockIdx.y * 64, m = min(ROWS, a.T - t0);
+  const W4Shape sh(FMT, a.N, a.K, G);
+  const int tiles = (a.N + 15) / 16;
+  const int tile0 = (blockIdx.x * kWideWaves + wv) * R;
+  const int slices = (sh.nk + 1) / 2;
+  const __amdgpu_buffer_rsrc_t xbuf = make_rsrc(a.x + (size_t)t0 * a.x_ld, ((size_t)(m - 1) * a.x_ld + a.K) * 2);
+  int x_off[PIECES], x_lds[PIECES], x_col[PIECES];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int c = threadIdx.x + i * 64 * kWideWaves, row = c >> 5, pc = c & 31;
+    x_off[i] = min(row, m - 1) * (int)a.x_ld * 2 + pc * 16;
+    x_lds[i] = row * LD + pc * 16;
+    x_col[i] = pc * 8;
+  }
+  u32x4 xv[PIECES];
+  auto load_slice = [&](int s) {  // columns past K become zeros
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) xv[i] = bld16(xbuf, s * 256 + x_col[i] < a.K ? x_off[i] + s * 512 : kPastEnd, 0);
+  };
+  auto store_slice = [&](int half) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) *reinterpret_cast<u32x4*>(xs[half] + x_lds[i]) = xv[i];
+  };
+  struct Buf {
+    u32x4 w[2][R];
+    W4Params<FMT, G> p[R];
+  };
+  Buf buf[2];
+  auto issue = [&](Buf& b, int s) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool tile = tile0 + r < tiles;
+      const uint8_t* codes = a.w + (size_t)(tile0 + r) * sh.code_tile;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool live = tile && 2 * s + u < sh.nk;
+        b.w[u][r] = bld16(make_rsrc(codes, live ? sh.code_tile : 0), lane * 16, live ? (2 * s + u) * 1024 : 0);
+      }
+      const bool live = tile && s < slices;
+      load_params<FMT, G>(b.p[r], make_rsrc(a.w + sh.par_at + (size_t)(tile0 + r) * sh.par_tile, live ? sh.par_tile : 0),
+                          2 * s, live);
+    }
+  };
+  f32x4 acc[R][NT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[r][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  load_slice(0);
+  issue(buf[0], 0);
+  issue(buf[1], 1);
+  store_slice(0);
+  lds_barrier();
+  const int row = a_token(lane) * LD;
+  for (int s = 0; s < slices; s += 2) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (s + b >= slices) break;
+      load_slice(s + b + 1);  // past the last slice: nothing is read
+      const uint8_t* x = xs[b] + row;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (2 * (s + b) + u < sh.nk)
+          w4_step<FMT, G, R, NT, 4>(acc, buf[b].w[u], buf[b].p, u, 2 * (s + b) + u, [&](int nt, int f) {
+            return *reinterpret_cast<const u32x4*>(x + nt * 16 * LD + u * 256 + (FMT == kW4Mxfp4 ? 64 * g + 16 * f : 64 * f + 16 * g));
+          });
+      issue(buf[b], s + b + 2);
+      store_slice(b ^ 1);
+      lds_barrier();
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t col = (int64_t)(tile0 + r) * 16 + (lane & 15);
+    if (col >= a.N) continue;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int t = nt * 16 + g + 4 * v;
+        if (t < m) store_y<BF16OUT>(a, t0 + t, col, acc[r][nt][v]);
+      }
+  }
+}
+
+template <int FMT, int G, bool BF16OUT>
+static void launch_t(const W4Args& a, hipStream_t st) {
+  const int tiles = (a.N + 15) / 16, pairs = ((a.K + 127) / 128 + 1) / 2;
+  if (a.T > 16 && tiles >= kW4WideTiles) {
+    const dim3 grid((unsigned)((tiles + kWideR * kWideWaves - 1) / (kWideR * kWideWaves)), (unsigned)((a.T + 63) / 64));
+    const dim3 block(64 * kWideWaves);
+    if (a.T <= 32) hipLaunchKernelGGL((w4_wide<FMT, G, 2, BF16OUT>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((w4_wide<FMT, G, 4, BF16OUT>), grid, block, 0, st, a);
+    return;
+  }
+  const int nc = (pairs + 15) / 16, waves = (pairs + nc - 1) / nc;
+  const int vn = a.T <= 4 ? 1 : a.T <= 8 ? 2 : 4;
+  const int per_cu = 16 / waves, fit = 256 * (per_cu > 4 ? 4 : per_cu);
+  const dim3 grid((unsigned)(tiles < fit ? tiles : fit), (unsigned)((a.T + 15) / 16)), block(64 * waves);
+  const size_t lds = (size_t)2 * vn * waves * 256;
+#define MOE_W4_FEW(VN, NC) hipLaunchKernelGGL((w4_few<FMT, G, VN, NC, BF16OUT>), grid, block, lds, st, a, nc)
+#define MOE_W4_VN(NC)                \
+  do {                               \
+    if (vn == 1) MOE_W4_FEW(1, NC);  \
+    else if (vn == 2) MOE_W4_FEW(2, NC); \
+    else MOE_W4_FEW(4, NC);          \
+  } while (0)
+  if (nc == 1) MOE_W4_VN(1);
+  else if (nc == 2) MOE_W4_VN(2);
+  else MOE_W4_VN(0);
+#undef MOE_W4_VN
+#undef MOE_W4_FEW
 }
 
 template <int FMT, int G>
-static void launch_t(const W4Args& a, bool bf16_out, hipStream_t st) {
-  const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.T + 15) / 16)), block(64 * kW4Waves);
-  if (bf16_out)
-    hipLaunchKernelGGL((w4_linear_kernel<FMT, G, true>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((w4_linear_kernel<FMT, G, false>), grid, block, 0, st, a);
+static void launch_out(const W4Args& a, bool bf16_out, hipStream_t st) {
+  if (bf16_out) launch_t<FMT, G, true>(a, st);
+  else launch_t<FMT, G, false>(a, st);
 }
 
 hipError_t launch_w4_linear(int fmt, const W4Args& a, bool bf16_out, hipStream_t st) {
   if (a.T == 0) return hipSuccess;
-  if (fmt == kW4Mxfp4) launch_t<kW4Mxfp4, 32>(a, bf16_out, st);
-  else if (a.group == 32) launch_t<kW4Int4, 32>(a, bf16_out, st);
-  else if (a.group == 64) launch_t<kW4Int4, 64>(a, bf16_out, st);
-  else launch_t<kW4Int4, 128>(a, bf16_out, st);
+  if (fmt == kW4Mxfp4) launch_out<kW4Mxfp4, 32>(a, bf16_out, st);
+  else if (a.group == 32) launch_out<kW4Int4, 32>(a, bf16_out, st);
+  else if (a.group == 64) launch_out<kW4Int4, 64>(a, bf16_out, st);
+  else launch_out<kW4Int4, 128>(a, bf16_out, st);
   return hipGetLastError();
 }
 
