@@ -26,6 +26,7 @@ namespace moe {
 constexpr int kDlMaxPairs = kDecodeLayerMaxPairs;
 constexpr int kDlWaves = 16;  // waves of a block, one block per CU
 constexpr int kDlThreads = 64 * kDlWaves;
+constexpr int kDlTeams = 4;  // gate/up: teams of a block, a tile each
 constexpr int kDlOneQuadT = 8;  // batches whose down runs hold up to 4 pairs, larger ones up to 8
 
 // A run: pairs of one expert (or tokens of the shared expert) that one matrix tile serves.
@@ -304,14 +305,14 @@ __device__ __forceinline__ void copy_rows(uint8_t* rows, int row_bytes, const ui
 // ---------------------------------------------------------------------------
 // Gate/up.  The row tiles of W13 of all runs form one list, cut into equal contiguous
 // ranges, one per block (one block of 16 waves per CU), so a block meets few runs and
-// copies each run's token rows into LDS once.  The 16 waves split K (bf16: wave w takes
-// column steps w, w + 16, ...; MXFP4: an even number of consecutive steps, so that one
-// scale word serves two) and stream their part of the range through kBufs register buffers
-// of kUnits weight fragments: loads run across tiles and runs, up to 8 KB in flight per
-// wave, and nothing but weights goes through vector memory.  At the end of a tile the
-// block adds the 16 parts in LDS (two buffers, one barrier per tile that does not wait
-// for loads), applies SwiGLU and writes h.  A W13 row tile holds 8 gate rows and the 8
-// up rows beside them.
+// copies each run's token rows into LDS once.  The 16 waves are four teams with a tile
+// each; the waves of a team split K (bf16: wave w of 4 takes column steps w, w + 4, ...;
+// MXFP4: an even number of consecutive steps, so that one scale word serves two) and
+// stream their tiles through `bufs` register buffers of `units` weight fragments: loads run
+// across tiles and runs, up to 8 KB in flight per wave, and nothing but weights goes
+// through vector memory.  At the end of a turn (a tile per team) the block adds the parts
+// in LDS (two buffers, one barrier per turn, which waits for no load), applies SwiGLU and
+// writes h.  A W13 row tile holds 8 gate rows and the 8 up rows beside them.
 //
 // Two things shape the loops.  Every issue requests its loads, past the end from an empty
 // buffer, which reads nothing: were they conditional, the wait for a fragment could not count
@@ -399,19 +400,23 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
     out->sorted[p] = s.sorted[p];
     out->valid[p] = s.key[p] >= 0;
   }
+  constexpr int teams = kDlTeams, parts = kDlWaves / teams;
+  const int team = kp / parts, part = kp % parts;
   const int sh_runs = a.shared_w ? (a.T + P - 1) / P : 0;
   const int sh_tiles = a.I_shared / 8, rt_tiles = a.I / 8;
-  const int sh_total = sh_runs * sh_tiles, total = sh_total + (runs - sh_runs) * rt_tiles;
+  const int sh_turns = (sh_tiles + teams - 1) / teams, rt_turns = (rt_tiles + teams - 1) / teams;
+  const int sh_total = sh_runs * sh_turns, total = sh_total + (runs - sh_runs) * rt_turns;
   const int lo = (int)((int64_t)blockIdx.x * total / gridDim.x), hi = (int)((int64_t)(blockIdx.x + 1) * total / gridDim.x);
   if (lo >= hi) return;
   const ExpertShape<WT> rt(a.H, a.I), sh(a.H, a.I_shared);
-  const int nk = rt.n13, nu = (nk + kDlWaves - 1) / kDlWaves, nc = (nu + U - 1) / U;  // steps, units, chunks of a tile
-  const int step0 = WT == W_MXFP4 ? kp * nc * U : kp, step_by = WT == W_MXFP4 ? 1 : kDlWaves;
-  const int run0 = lo < sh_total ? lo / max(sh_tiles, 1) : sh_runs + (lo - sh_total) / rt_tiles;
-  const int tile0 = lo < sh_total ? lo - run0 * sh_tiles : lo - sh_total - (run0 - sh_runs) * rt_tiles;
+  // column steps, units and chunks of units of a wave's tile
+  const int nk = rt.n13, nu = (nk + parts - 1) / parts, nc = (nu + U - 1) / U;
+  const int step0 = WT == W_MXFP4 ? part * nc * U : part, step_by = WT == W_MXFP4 ? 1 : parts;
+  const int run0 = lo < sh_total ? lo / max(sh_turns, 1) : sh_runs + (lo - sh_total) / rt_turns;
+  const int turn0 = lo < sh_total ? lo - run0 * sh_turns : lo - sh_total - (run0 - sh_runs) * rt_turns;
 
   // Issue side: the next chunk to request.
-  int iq = lo, ic = 0, irun = run0 - 1, itile = tile0, iper = 0, isc = 0;
+  int iq = lo, ic = 0, irun = run0 - 1, itile = turn0 * teams + team, iper = 0, isc = 0;
   const uint8_t* iw = nullptr;
   int ibytes = 0;
   auto issue_run = [&]() {
@@ -427,7 +432,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int step = step0 + (ic * U + u) * step_by;
-      const bool live = iq < hi && step < nk;
+      const bool live = iq < hi && step < nk && itile < iper;
       const __amdgpu_buffer_rsrc_t buf = make_rsrc(iw, live ? ibytes : 0);
       b.w[u] = bld16(buf, lane * 16, live ? (itile * nk + step) * 1024 : 0);
       if constexpr (WT == W_MXFP4)  // steps in pairs from an even one: one word
@@ -438,8 +443,9 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
     if (++ic == nc) {
       ic = 0;
       ++iq;
-      if (++itile == iper && iq < hi) {
-        itile = 0;
+      itile += teams;
+      if (itile - team >= iper && iq < hi) {
+        itile = team;
         issue_run();
       }
     }
@@ -449,7 +455,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
   for (int b = 0; b < B; ++b) issue(buf[b]);
 
   // Compute side.
-  int q = lo, cc = 0, run = run0 - 1, tile = tile0, per = 0, at = 0, m = 0, half = 0;
+  int q = lo, cc = 0, run = run0 - 1, tile = turn0 * teams + team, per = 0, at = 0, m = 0, half = 0;
   const uint8_t* my_row = rows;
   auto enter_run = [&]() {  // the token rows of the next run into LDS
     ++run;
@@ -475,7 +481,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int step = step0 + (cc * U + u) * step_by;
-        if (step < nk) {
+        if (step < nk) {  // a team without a tile multiplies zeros
           if constexpr (WT == W_BF16) {
             acc = mfma16(*reinterpret_cast<const u32x4*>(my_row + step * 64 + 16 * g), as_bf16x8(buf[b].w[u]), acc);
           } else {
@@ -490,33 +496,37 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
       issue(buf[b]);
       if (++cc < nc) continue;
       cc = 0;
-      float* part = red + half * red_tile;
+      float* sums = red + half * red_tile;
       const int nv = (m + 3) / 4;
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        if (v < nv) part[(v * kDlWaves + kp) * 64 + lane] = acc[v];
+        if (v < nv) sums[(v * kDlWaves + kp) * 64 + lane] = acc[v];
       acc = f32x4{0.f, 0.f, 0.f, 0.f};
       lds_barrier();
-      // element v of tile q by wave (q nv + v) % 16: lane = (token % 4, stored row)
-      const int v = (kp - q * nv) & (kDlWaves - 1);
-      if (v < nv) {
+      // element v of a team's tile by wave v + nv (team + teams q) of the 16: lane =
+      // (token % 4, stored row)
+      const int unit = (kp - q * nv * teams) & (kDlWaves - 1);
+      if (unit < nv * teams) {
+        const int tm = unit / nv, v = unit - tm * nv, tl = tile - team + tm;
+        const float* src = sums + (v * kDlWaves + tm * parts) * 64 + lane;
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kDlWaves; ++w) sum += part[(v * kDlWaves + w) * 64 + lane];
+        for (int w = 0; w < parts; ++w) sum += src[w * 64];
         const float up = __shfl_xor(sum, 8, 64);
         const int i = g + 4 * v;
-        if (i < m && (lane & 8) == 0) {
+        if (i < m && (lane & 8) == 0 && tl < per) {
           const int row = run < sh_runs ? n + at + i : s.sorted[at + i];
           uint16_t* h = a.h + (size_t)row * a.h_ld;
-          h[tile * 8 + (lane & 7)] = f32_to_bf16_rne(silu_f32(sum) * up);
-          if (WT == W_MXFP4 && tile + 1 == per)  // zeros up to the next whole column step
+          h[tl * 8 + (lane & 7)] = f32_to_bf16_rne(silu_f32(sum) * up);
+          if (WT == W_MXFP4 && tl + 1 == per)  // zeros up to the next whole column step
             for (int z = per * 8; z % 128; z += 8) h[z + (lane & 7)] = 0;
         }
       }
       half ^= 1;
       if (++q >= hi) return;
-      if (++tile == per) {
-        tile = 0;
+      tile += teams;
+      if (tile - team >= per) {
+        tile = team;
         enter_run();
       }
     }
@@ -759,7 +769,8 @@ static hipError_t launch_t(const DecodeLayerArgs& a, bool bf16_out, hipStream_t 
   const bool resident = a.T <= P;
   if (P > a.T) P = a.T;  // a token routes to an expert once, unless the caller's routing repeats it
   const size_t lds = sizeof(DlPlan) + gu_red_bytes(P) + kDlRouting + (size_t)P * rb;
-  const int64_t bound = (a.shared_w ? (int64_t)(a.T + P - 1) / P * (a.I_shared / 8) : 0) + (int64_t)n * (a.I / 8);
+  const int64_t sh_turns = (a.I_shared / 8 + kDlTeams - 1) / kDlTeams, rt_turns = (a.I / 8 + kDlTeams - 1) / kDlTeams;
+  const int64_t bound = (a.shared_w ? (a.T + P - 1) / P * sh_turns : 0) + n * rt_turns;  // every pair a run
   const unsigned grid = (unsigned)(bound < 256 ? bound : 256);
   const int vn = a.T <= kDlOneQuadT ? 1 : 2;
   hipLaunchKernelGGL(decode_gate_up<WT>, dim3(grid), dim3(kDlThreads), lds, st, a, P, 4 * vn, rb, resident);

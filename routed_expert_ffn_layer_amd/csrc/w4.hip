@@ -408,7 +408,7 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
 // waves 128 R rows; the tokens pass through LDS in slices of two column steps shared by the
 // waves (two buffers: the next slice travels to registers while this one is multiplied,
 // one barrier per slice), each fragment read from LDS serving R products.  The codes of
-// the next two slices are in flight in registers.
+// up to three slices are in flight in registers.
 constexpr int kWideR = 2, kWideWaves = 8;
 
 template <int FMT, int G, int NT, bool BF16OUT>
@@ -444,7 +444,7 @@ __global__ __launch_bounds__(64 * kWideWaves) void w4_wide(W4Args a) {
     u32x4 w[2][R];
     W4Params<FMT, G> p[R];
   };
-  Buf buf[2];
+  Buf buf[3];
   auto issue = [&](Buf& b, int s) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -465,28 +465,32 @@ __global__ __launch_bounds__(64 * kWideWaves) void w4_wide(W4Args a) {
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[r][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // Loads return in order, so a slice of tokens is requested ahead of the codes that are
+  // needed after it: waiting for slice s + 1 leaves the codes of s + 2 in flight.
   load_slice(0);
   issue(buf[0], 0);
   issue(buf[1], 1);
   store_slice(0);
+  load_slice(1);
+  issue(buf[2], 2);
   lds_barrier();
   const int row = a_token(lane) * LD;
-  for (int s = 0; s < slices; s += 2) {
+  int s = 0;
+  auto turn = [&](Buf& b) {
+    const uint8_t* x = xs[s & 1] + row;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      if (s + b >= slices) break;
-      load_slice(s + b + 1);  // past the last slice: nothing is read
-      const uint8_t* x = xs[b] + row;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (2 * (s + b) + u < sh.nk)
-          w4_step<FMT, G, R, NT, 4>(acc, buf[b].w[u], buf[b].p, u, 2 * (s + b) + u, [&](int nt, int f) {
-            return *reinterpret_cast<const u32x4*>(x + nt * 16 * LD + u * 256 + (FMT == kW4Mxfp4 ? 64 * g + 16 * f : 64 * f + 16 * g));
-          });
-      issue(buf[b], s + b + 2);
-      store_slice(b ^ 1);
-      lds_barrier();
-    }
+    for (int u = 0; u < 2; ++u)
+      if (2 * s + u < sh.nk)
+        w4_step<FMT, G, R, NT, 4>(acc, b.w[u], b.p, u, 2 * s + u, [&](int nt, int f) {
+          return *reinterpret_cast<const u32x4*>(x + nt * 16 * LD + u * 256 + (FMT == kW4Mxfp4 ? 64 * g + 16 * f : 64 * f + 16 * g));
+        });
+    store_slice((s + 1) & 1);
+    load_slice(s + 2);  // past the last slice: nothing is read
+    issue(b, s + 3);
+    lds_barrier();
+    return ++s < slices;
+  };
+  while (turn(buf[0]) && turn(buf[1]) && turn(buf[2])) {
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
