@@ -27,6 +27,7 @@ constexpr int kDlMaxPairs = kDecodeLayerMaxPairs;
 constexpr int kDlWaves = 16;  // waves of a block, one block per CU
 constexpr int kDlThreads = 64 * kDlWaves;
 constexpr int kDlTeams = 4;  // gate/up: teams of a block, a tile each
+constexpr int kDlHalfTiles = 256;  // row tiles of W2 below which the down kernel's blocks own half a tile
 constexpr int kDlOneQuadT = 8;  // batches whose down runs hold up to 4 pairs, larger ones up to 8
 
 // A run: pairs of one expert (or tokens of the shared expert) that one matrix tile serves.
@@ -193,7 +194,8 @@ __device__ __forceinline__ void dl_route(DlPlan& s, float* w, const DecodeLayerA
 // the mask's population, a pair's place in its group the population below its token, and
 // one scan over the experts (thread e holds expert e) places groups and runs.  Given
 // routing may name an expert twice in one token, which a mask cannot hold: then every
-// pair counts the pairs before it of the same expert instead (n compares each).
+// pair counts the pairs before it of the same expert instead (n compares each).  Up to 64
+// pairs take one wave and one barrier instead (four: 1.6 us of a 21 us layer at one token).
 // slots: the slot table; mask: E 64-bit words; part: 2 * kDlWaves words (all LDS).
 // Returns the number of runs, the shared expert's included (the same in every thread); ends
 // with a barrier.
@@ -202,11 +204,49 @@ static_assert(kDlThreads >= 1024 && kDlMaxPairs <= kDlThreads && kDecodeLayerMax
 __device__ __forceinline__ int dl_plan(DlPlan& s, const int32_t* slots, uint64_t* mask, uint32_t* part,
                                        const DecodeLayerArgs& a, int P, int P2, DlShared* out) {
   const int n = a.T * a.k, p = threadIdx.x, wv = p >> 6, t = p / a.k;
+  const int sh1 = a.shared_w ? (a.T + P - 1) / P : 0, sh2 = a.shared_w ? (a.T + P2 - 1) / P2 : 0;
+  const uint64_t shared_w = reinterpret_cast<uint64_t>(a.shared_w);
+  if (p < sh1) s.run[p] = DlRun{shared_w, p * P, min(P, a.T - p * P)};
+  if (out && p < sh2) out->run[p] = DlRun{shared_w, p * P2, min(P2, a.T - p * P2)};
   int e = -1;
   if (p < n) {
     const int id = s.id[p];
     e = id >= 0 && id < a.E && slots[id] >= 0 ? id : -1;
     s.key[p] = e;
+  }
+  if (n <= 64) {
+    // One wave, in registers, groups in order of their first pair: a pair counts its equals
+    // (all, and before it), a scan over the groups' first pairs places groups and runs.
+    if (wv == 0) {
+      int count = 0, before = 0, first = 64;
+#pragma unroll 1
+      for (int q = 0; q < n; ++q) {
+        const bool same = __builtin_amdgcn_readlane(e, q) == e;
+        count += same;
+        before += same && q < p;
+        first = same ? min(first, q) : first;
+      }
+      const bool head = e >= 0 && before == 0;
+      const uint32_t runs1 = head ? (count + P - 1) / P : 0, runs2 = head ? (count + P2 - 1) / P2 : 0;
+      const uint32_t packed = (head ? count : 0) | runs1 << 10 | runs2 << 20, scan = wave_scan(packed);
+      const uint32_t base = scan - packed;
+      if (head) {
+        const uint64_t w = reinterpret_cast<uint64_t>(a.slot_pool) + (uint64_t)slots[e] * a.slot_stride;
+        const int at = base & 0x3ff, r1 = sh1 + (base >> 10 & 0x3ff), r2 = sh2 + (base >> 20);
+#pragma unroll 1
+        for (int i = 0; i < (int)runs1; ++i) s.run[r1 + i] = DlRun{w, at + i * P, min(P, count - i * P)};
+#pragma unroll 1
+        for (int i = 0; out && i < (int)runs2; ++i) out->run[r2 + i] = DlRun{w, at + i * P2, min(P2, count - i * P2)};
+      }
+      const int group = __shfl((int)(base & 0x3ff), first & 63, 64);
+      if (e >= 0) s.sorted[group + before] = (uint16_t)p;
+      if (p == 63) {
+        part[0] = sh1 + (scan >> 10 & 0x3ff);
+        if (out) out->runs = sh2 + (scan >> 20);
+      }
+    }
+    __syncthreads();
+    return part[0];
   }
   bool twice = false;
   if (e >= 0) {
@@ -237,10 +277,6 @@ __device__ __forceinline__ int dl_plan(DlPlan& s, const int32_t* slots, uint64_t
     total += v;
   }
   base += scan - packed;
-  const int sh1 = a.shared_w ? (a.T + P - 1) / P : 0, sh2 = a.shared_w ? (a.T + P2 - 1) / P2 : 0;
-  const uint64_t shared_w = reinterpret_cast<uint64_t>(a.shared_w);
-  if (p < sh1) s.run[p] = DlRun{shared_w, p * P, min(P, a.T - p * P)};
-  if (out && p < sh2) out->run[p] = DlRun{shared_w, p * P2, min(P2, a.T - p * P2)};
   if (count > 0) {
     const uint64_t w = reinterpret_cast<uint64_t>(a.slot_pool) + (uint64_t)slots[p] * a.slot_stride;
     const int at = base & 0x3ff, r1 = sh1 + (base >> 10 & 0x3ff), r2 = sh2 + (base >> 20);
@@ -547,16 +583,27 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
 // which would hold the same token four times (VN = 1) or two tokens twice (VN = 2), each
 // lane loads another fragment, and quad permutes hand them to the products.
 // ---------------------------------------------------------------------------
-template <int WT, int VN>
+//
+// HALF: a block owns 8 columns of y, half a row tile (H / 8 blocks where H / 16 would leave
+// CUs idle; bf16 layer of 16 tokens at H = 2048: 139 -> DOWN_HALF us).  One 1 KB load then
+// holds the 8 rows at two steps, rows at the even step as operand columns 0-7 and at the odd
+// one as columns 8-15, and the quads of lanes hold two tokens at both steps: rows 4 i and
+// 4 i + 1 of the result are right in columns 0-7, rows 4 i + 2 and 4 i + 3 in columns 8-15
+// (the other products mean nothing), and the two halves add up.  An h load serves half as
+// many weights, so this is for blocks that would be too few otherwise.
+template <int WT, int VN, bool HALF>
 struct DnTune {
-  static constexpr int units = WT == W_BF16 ? 4 : 2;  // steps of a chunk
-  static constexpr int groups = WT == W_BF16 ? 1 : 2;  // of four fragments: bf16 one per step, MXFP4 four
+  static constexpr int units = WT == W_BF16 ? 4 : 2;                // steps of a chunk
+  static constexpr int wloads = HALF ? units / 2 : units;           // code loads of a chunk
+  static constexpr int groups = HALF || WT == W_BF16 ? 1 : 2;       // groups of h loads
+  static constexpr int hloads = HALF && WT == W_MXFP4 ? 4 : VN;     // h loads of a group
   static constexpr int bufs = VN == 1 ? 4 : 3;
 };
 
-template <int WT, int VN>
+template <int WT, int VN, bool HALF>
 struct DnBuf {
-  u32x4 w[DnTune<WT, VN>::units], h[DnTune<WT, VN>::groups][VN];
+  using Tune = DnTune<WT, VN, HALF>;
+  u32x4 w[Tune::wloads], h[Tune::groups][Tune::hloads];
   uint32_t sc;
 };
 
@@ -571,16 +618,19 @@ __device__ __forceinline__ u32x4 quad_fragment(const u32x4 (&h)[VN]) {
   return o;
 }
 
-template <int WT, int VN, bool BF16OUT>
+template <int WT, int VN, bool HALF, bool BF16OUT>
 __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int log_parts) {
-  constexpr int U = DnTune<WT, VN>::units, NG = DnTune<WT, VN>::groups, B = DnTune<WT, VN>::bufs, P = 4 * VN;
+  using Tune = DnTune<WT, VN, HALF>;
+  constexpr int U = Tune::units, NW = Tune::wloads, NG = Tune::groups, NH = Tune::hloads, B = Tune::bufs, P = 4 * VN;
+  constexpr int COLS = HALF ? 8 : 16;
+  static_assert(!HALF || VN == 2, "half tiles hold two tokens a quad");
   __shared__ DlShared s;
   __shared__ float w[kDlMaxPairs];
-  extern __shared__ float val[];  // [part][pair, then shared token][16]
-  const int lane = threadIdx.x & 63, g = lane >> 4, wv = uniform(threadIdx.x >> 6);
+  extern __shared__ float val[];  // [part][pair, then shared token][COLS]
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, wv = uniform(threadIdx.x >> 6);
   const int n = a.T * a.k, nrows = n + (a.shared_w ? a.T : 0), p = threadIdx.x;
   const int sh_runs = a.shared_w ? (a.T + P - 1) / P : 0;
-  const int tile = blockIdx.x;
+  const int tile = HALF ? blockIdx.x >> 1 : blockIdx.x;
   const DlShared* in = static_cast<const DlShared*>(a.plan);
   const int runs = in->runs;
   {
@@ -605,9 +655,13 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
     from = (part * chunks >> log_parts) * U;
     to = min(((part + 1) * chunks >> log_parts) * U, nk);
   };
+  // this lane's fragment of a tile, and (HALF) the step it takes of a pair
+  const int frag = HALF ? 16 * g + 8 * (blockIdx.x & 1) + (c & 7) : lane;
+  const int w_step = HALF ? c >> 3 : 0, j = lane & 3, h_step = HALF ? j >> 1 : 0;
+  const int w_off = frag * 16 + w_step * 1024;
 
   // Issue side: run ir, steps is .. ie-1 of it.
-  int ir = (wv >> log_parts) - stride, is = 0, ie = 0, i_off[VN], i_w2 = 0, i_sc = 0;
+  int ir = (wv >> log_parts) - stride, is = 0, ie = 0, i_row = 0, i_w2 = 0, i_sc = 0;
   const uint8_t* iw = nullptr;
   int ibytes = 0;
   auto issue_run = [&]() {
@@ -621,29 +675,34 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
     i_w2 = (shared ? sh.c13 : rt.c13) + tile * nk * 1024;
     i_sc = (shared ? sh.c13 + sh.c2 + sh.s13 : rt.c13 + rt.c2 + rt.s13) + tile * ((nk + 15) / 16) * 1024;
     part_steps(nk, is, ie);
-    // this lane's load l: token `tok`, fragment f (bf16: 64 bytes a step; MXFP4: blocks of 64 bytes)
-    const int j = lane & 3, tok = ((lane & 15) >> 2) + (VN == 2 ? 4 * (j & 1) : 0), i = min(tok, r.m - 1);
-    const int row = (shared ? n + r.at + i : s.sorted[r.at + i]) * a.h_ld * 2;
-#pragma unroll
-    for (int l = 0; l < VN; ++l) {
-      const int f = VN == 1 ? j : 2 * l + (j >> 1);
-      i_off[l] = row + (WT == W_MXFP4 ? 64 * g + 16 * f : 16 * g + 64 * f);
-    }
+    const int tok = (c >> 2) + (VN == 2 ? 4 * (j & 1) : 0), i = min(tok, r.m - 1);
+    i_row = (shared ? n + r.at + i : s.sorted[r.at + i]) * a.h_ld * 2 + (WT == W_MXFP4 ? 64 : 16) * g;
   };
-  auto issue = [&](DnBuf<WT, VN>& b) {
+  auto issue = [&](DnBuf<WT, VN, HALF>& b) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; u += HALF ? 2 : 1) {
       const int step = is + u;
       const bool live = ir < runs && step < ie;
       const __amdgpu_buffer_rsrc_t wbuf = make_rsrc(iw, live ? ibytes : 0), hbuf = make_rsrc(a.h, live ? hbytes : 0);
-      b.w[u] = bld16(wbuf, lane * 16, live ? i_w2 + step * 1024 : 0);
+      // HALF, an odd number of steps: the lanes of the missing one read nothing
+      const bool pair = !HALF || step + 1 < ie;
+      b.w[HALF ? u / 2 : u] = bld16(wbuf, pair || w_step == 0 ? w_off : kPastEnd, live ? i_w2 + step * 1024 : 0);
       if constexpr (WT == W_MXFP4)
         if (u == 0)
           b.sc = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-              wbuf, lane * 16, live ? i_sc + step / 16 * 1024 + step % 16 / 4 * 4 : 0, 0);
-      if (u < NG) {
+              wbuf, frag * 16, live ? i_sc + step / 16 * 1024 + step % 16 / 4 * 4 : 0, 0);
+      const int hs = live ? step * (WT == W_MXFP4 ? 256 : 64) : 0;
+      if constexpr (HALF && WT == W_BF16) {
+        b.h[0][u / 2] = bld16(hbuf, pair || h_step == 0 ? i_row + 64 * h_step : kPastEnd, hs);
+      } else if constexpr (HALF) {
 #pragma unroll
-        for (int l = 0; l < VN; ++l) b.h[u][l] = bld16(hbuf, i_off[l], live ? step * (WT == W_MXFP4 ? 256 : 64) : 0);
+        for (int f = 0; f < 4; ++f)
+          b.h[0][f] = bld16(hbuf, pair || h_step == 0 ? i_row + 256 * h_step + 16 * f : kPastEnd, hs);
+      } else if (u < NG) {
+        // load l: fragment f of this lane's token (bf16: 64 bytes a step; MXFP4: 16 bytes)
+#pragma unroll
+        for (int l = 0; l < NH; ++l)
+          b.h[u][l] = bld16(hbuf, i_row + (WT == W_MXFP4 ? 16 : 64) * (VN == 1 ? j : 2 * l + (j >> 1)), hs);
       }
     }
     is += U;
@@ -657,7 +716,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
       m = r.m;
       part_steps(cr < sh_runs ? sh.n2 : rt.n2, cs, ce);
     };
-    DnBuf<WT, VN> buf[B];
+    DnBuf<WT, VN, HALF> buf[B];
     issue_run();
 #pragma unroll
     for (int b = 0; b < B; ++b) issue(buf[b]);
@@ -666,22 +725,28 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
     for (bool more = true; more;) {
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        if constexpr (WT == W_BF16) {
-          const DnBuf<WT, VN>& c = buf[b];
-          acc = mfma16(quad_fragment<VN, 0>(c.h[0]), as_bf16x8(c.w[0]), acc);
-          if (cs + 1 < ce) acc = mfma16(quad_fragment<VN, 1>(c.h[0]), as_bf16x8(c.w[1]), acc);
-          if (cs + 2 < ce) acc = mfma16(quad_fragment<VN, 2>(c.h[0]), as_bf16x8(c.w[2]), acc);
-          if (cs + 3 < ce) acc = mfma16(quad_fragment<VN, 3>(c.h[0]), as_bf16x8(c.w[3]), acc);
+        const DnBuf<WT, VN, HALF>& k = buf[b];
+        if constexpr (HALF && WT == W_BF16) {
+          acc = mfma16(k.h[0][0], as_bf16x8(k.w[0]), acc);
+          if (cs + 2 < ce) acc = mfma16(k.h[0][1], as_bf16x8(k.w[1]), acc);
+        } else if constexpr (HALF) {
+          const float sc = e8m0_to_f32(k.sc >> (8 * ((cs & 3) + w_step)) & 0xffu);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) acc = mfma16(k.h[0][f], fp4x8_to_bf16x8(k.w[0][f], sc), acc);
+        } else if constexpr (WT == W_BF16) {
+          acc = mfma16(quad_fragment<VN, 0>(k.h[0]), as_bf16x8(k.w[0]), acc);
+          if (cs + 1 < ce) acc = mfma16(quad_fragment<VN, 1>(k.h[0]), as_bf16x8(k.w[1]), acc);
+          if (cs + 2 < ce) acc = mfma16(quad_fragment<VN, 2>(k.h[0]), as_bf16x8(k.w[2]), acc);
+          if (cs + 3 < ce) acc = mfma16(quad_fragment<VN, 3>(k.h[0]), as_bf16x8(k.w[3]), acc);
         } else {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             if (cs + u < ce) {
-              const DnBuf<WT, VN>& c = buf[b];
-              const float sc = scale_of_word(c.sc, cs + u);
-              acc = mfma16(quad_fragment<VN, 0>(c.h[u]), fp4x8_to_bf16x8(c.w[u][0], sc), acc);
-              acc = mfma16(quad_fragment<VN, 1>(c.h[u]), fp4x8_to_bf16x8(c.w[u][1], sc), acc);
-              acc = mfma16(quad_fragment<VN, 2>(c.h[u]), fp4x8_to_bf16x8(c.w[u][2], sc), acc);
-              acc = mfma16(quad_fragment<VN, 3>(c.h[u]), fp4x8_to_bf16x8(c.w[u][3], sc), acc);
+              const float sc = scale_of_word(k.sc, cs + u);
+              acc = mfma16(quad_fragment<VN, 0>(k.h[u]), fp4x8_to_bf16x8(k.w[u][0], sc), acc);
+              acc = mfma16(quad_fragment<VN, 1>(k.h[u]), fp4x8_to_bf16x8(k.w[u][1], sc), acc);
+              acc = mfma16(quad_fragment<VN, 2>(k.h[u]), fp4x8_to_bf16x8(k.w[u][2], sc), acc);
+              acc = mfma16(quad_fragment<VN, 3>(k.h[u]), fp4x8_to_bf16x8(k.w[u][3], sc), acc);
             }
           }
         }
@@ -690,10 +755,15 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
         if (cs < ce) continue;
 #pragma unroll
         for (int v = 0; v < VN; ++v) {
+          float d = acc[v];
+          if constexpr (HALF) {
+            if (c >= 8) d = acc[v + 2];
+            d += __shfl_xor(d, 8, 64);
+          }
           const int i = g + 4 * v;
-          if (i < m) {
+          if (i < m && c < COLS) {
             const int row = cr < sh_runs ? n + at + i : s.sorted[at + i];
-            val[(part * nrows + row) * 16 + (lane & 15)] = acc[v];
+            val[(part * nrows + row) * COLS + c] = d;
           }
         }
         acc = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -706,16 +776,16 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
   }
   __syncthreads();
   if (parts > 1) {
-    for (int o = threadIdx.x; o < nrows * 16; o += kDlThreads) {
+    for (int o = threadIdx.x; o < nrows * COLS; o += kDlThreads) {
       float d = val[o];
 #pragma unroll 4
-      for (int q = 1; q < parts; ++q) d += val[q * nrows * 16 + o];
+      for (int q = 1; q < parts; ++q) d += val[q * nrows * COLS + o];
       val[o] = d;
     }
     __syncthreads();
   }
-  for (int o = threadIdx.x; o < a.T * 16; o += kDlThreads) {
-    const int tk = o >> 4, c = o & 15;
+  for (int o = threadIdx.x; o < a.T * COLS; o += kDlThreads) {
+    const int tk = o / COLS, col = o % COLS;
     float y = 0.f;
 #pragma unroll 1
     for (int j0 = 0; j0 < a.k; j0 += 4) {  // four pairs' LDS reads at a time
@@ -726,14 +796,14 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
         const int pr = tk * a.k + min(j0 + j, a.k - 1);
         ok[j] = j0 + j < a.k ? s.valid[pr] : 0;
         wj[j] = w[pr];
-        d[j] = val[pr * 16 + c];
+        d[j] = val[pr * COLS + col];
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (ok[j]) y = fmaf(wj[j], d[j], y);
     }
-    if (a.shared_w) y += val[(n + tk) * 16 + c];
-    const size_t out = (size_t)tk * a.H + tile * 16 + c;
+    if (a.shared_w) y += val[(n + tk) * COLS + col];
+    const size_t out = (size_t)tk * a.H + blockIdx.x * COLS + col;
     if (BF16OUT)
       static_cast<uint16_t*>(a.y)[out] = f32_to_bf16_rne(y);
     else
@@ -741,22 +811,23 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
   }
 }
 
-template <int WT, int VN>
+template <int WT, int VN, bool HALF>
 static hipError_t launch_down(const DecodeLayerArgs& a, bool bf16_out, hipStream_t st) {
   // K parts of the down product: enough (run, part) tasks for the waves when every pair is
   // a run of its own, each part at least one chunk of steps long, and LDS for the parts
+  constexpr int COLS = HALF ? 8 : 16;
   const int nrows = a.T * a.k + (a.shared_w ? a.T : 0);
-  const int ks = (WT == W_MXFP4 ? 128 : 32) * DnTune<WT, VN>::units;
+  const int ks = (WT == W_MXFP4 ? 128 : 32) * DnTune<WT, VN, HALF>::units;
   int chunks = (a.I + ks - 1) / ks;
   if (a.shared_w && (a.I_shared + ks - 1) / ks < chunks) chunks = (a.I_shared + ks - 1) / ks;
   int lp = 0;
-  while (lp < 4 && 2 << lp <= chunks && nrows << lp < 64 && (size_t)(nrows << lp) * 128 <= 65536) ++lp;
-  const size_t lds = (size_t)(nrows << lp) * 64;
-  const dim3 grid(a.H / 16), block(kDlThreads);
+  while (lp < 4 && 2 << lp <= chunks && nrows << lp < 64 && (size_t)(nrows << lp) * COLS * 8 <= 65536) ++lp;
+  const size_t lds = (size_t)(nrows << lp) * COLS * 4;
+  const dim3 grid(a.H / COLS), block(kDlThreads);
   if (bf16_out)
-    hipLaunchKernelGGL((decode_down<WT, VN, true>), grid, block, lds, st, a, lp);
+    hipLaunchKernelGGL((decode_down<WT, VN, HALF, true>), grid, block, lds, st, a, lp);
   else
-    hipLaunchKernelGGL((decode_down<WT, VN, false>), grid, block, lds, st, a, lp);
+    hipLaunchKernelGGL((decode_down<WT, VN, HALF, false>), grid, block, lds, st, a, lp);
   return hipGetLastError();
 }
 
@@ -772,11 +843,13 @@ static hipError_t launch_t(const DecodeLayerArgs& a, bool bf16_out, hipStream_t 
   const int64_t sh_turns = (a.I_shared / 8 + kDlTeams - 1) / kDlTeams, rt_turns = (a.I / 8 + kDlTeams - 1) / kDlTeams;
   const int64_t bound = (a.shared_w ? (a.T + P - 1) / P * sh_turns : 0) + n * rt_turns;  // every pair a run
   const unsigned grid = (unsigned)(bound < 256 ? bound : 256);
-  const int vn = a.T <= kDlOneQuadT ? 1 : 2;
+  const bool half = a.H / 16 < kDlHalfTiles;
+  const int vn = a.T <= kDlOneQuadT && !half ? 1 : 2;
   hipLaunchKernelGGL(decode_gate_up<WT>, dim3(grid), dim3(kDlThreads), lds, st, a, P, 4 * vn, rb, resident);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return vn == 1 ? launch_down<WT, 1>(a, bf16_out, st) : launch_down<WT, 2>(a, bf16_out, st);
+  if (half) return launch_down<WT, 2, true>(a, bf16_out, st);
+  return vn == 1 ? launch_down<WT, 1, false>(a, bf16_out, st) : launch_down<WT, 2, false>(a, bf16_out, st);
 }
 
 hipError_t launch_decode_layer(int wtype, const DecodeLayerArgs& a, bool bf16_out, hipStream_t st) {
