@@ -579,9 +579,12 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
 // The vector memory pipe, not HBM, is what a 4-bit stream runs into here (an h fragment
 // for every 256 bytes of codes: with four fragment loads and a scale load beside each code
 // load the MXFP4 kernel took 86 us at 64 tokens, 28 us of them its codes).  Runs are
-// therefore short, 4 VN tokens, and one load brings four fragments: in a quad of lanes,
+// therefore short, 4 VN tokens, and one load brings several fragments: in a quad of lanes,
 // which would hold the same token four times (VN = 1) or two tokens twice (VN = 2), each
-// lane loads another fragment, and quad permutes hand them to the products.
+// lane loads another fragment.  Such an operand goes into the products of all its
+// fragments' weights as it is: of row 4 i + j of a product only the fragment that lane j
+// loaded means something, so fragment f adds up in accumulator f % (4 / VN), whose
+// elements from VN (f % (4 / VN)) on are the tokens' sums.
 // ---------------------------------------------------------------------------
 //
 // HALF: a block owns 8 columns of y, half a row tile (H / 8 blocks where H / 16 would leave
@@ -607,22 +610,11 @@ struct DnBuf {
   uint32_t sc;
 };
 
-// Fragment f of a group for every row of the operand, from the quads' loads.
-template <int VN, int F>
-__device__ __forceinline__ u32x4 quad_fragment(const u32x4 (&h)[VN]) {
-  constexpr int a = VN == 1 ? F : 2 * (F & 1), b = VN == 1 ? F : a + 1;
-  const u32x4 v = h[VN == 1 ? 0 : F / 2];
-  u32x4 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], a | b << 2 | a << 4 | b << 6, 0xf, 0xf, true);
-  return o;
-}
-
 template <int WT, int VN, bool HALF, bool BF16OUT>
 __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int log_parts) {
   using Tune = DnTune<WT, VN, HALF>;
-  constexpr int U = Tune::units, NW = Tune::wloads, NG = Tune::groups, NH = Tune::hloads, B = Tune::bufs, P = 4 * VN;
-  constexpr int COLS = HALF ? 8 : 16;
+  constexpr int U = Tune::units, NG = Tune::groups, NH = Tune::hloads, B = Tune::bufs, P = 4 * VN;
+  constexpr int COLS = HALF ? 8 : 16, NA = HALF ? 1 : 4 / VN;  // columns of y; accumulators
   static_assert(!HALF || VN == 2, "half tiles hold two tokens a quad");
   __shared__ DlShared s;
   __shared__ float w[kDlMaxPairs];
@@ -721,32 +713,35 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
 #pragma unroll
     for (int b = 0; b < B; ++b) issue(buf[b]);
     enter_run();
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[NA];
+    auto clear = [&]() {
+#pragma unroll
+      for (int f = 0; f < NA; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+    clear();
     for (bool more = true; more;) {
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         const DnBuf<WT, VN, HALF>& k = buf[b];
         if constexpr (HALF && WT == W_BF16) {
-          acc = mfma16(k.h[0][0], as_bf16x8(k.w[0]), acc);
-          if (cs + 2 < ce) acc = mfma16(k.h[0][1], as_bf16x8(k.w[1]), acc);
+          acc[0] = mfma16(k.h[0][0], as_bf16x8(k.w[0]), acc[0]);
+          if (cs + 2 < ce) acc[0] = mfma16(k.h[0][1], as_bf16x8(k.w[1]), acc[0]);
         } else if constexpr (HALF) {
           const float sc = e8m0_to_f32(k.sc >> (8 * ((cs & 3) + w_step)) & 0xffu);
 #pragma unroll
-          for (int f = 0; f < 4; ++f) acc = mfma16(k.h[0][f], fp4x8_to_bf16x8(k.w[0][f], sc), acc);
+          for (int f = 0; f < 4; ++f) acc[0] = mfma16(k.h[0][f], fp4x8_to_bf16x8(k.w[0][f], sc), acc[0]);
         } else if constexpr (WT == W_BF16) {
-          acc = mfma16(quad_fragment<VN, 0>(k.h[0]), as_bf16x8(k.w[0]), acc);
-          if (cs + 1 < ce) acc = mfma16(quad_fragment<VN, 1>(k.h[0]), as_bf16x8(k.w[1]), acc);
-          if (cs + 2 < ce) acc = mfma16(quad_fragment<VN, 2>(k.h[0]), as_bf16x8(k.w[2]), acc);
-          if (cs + 3 < ce) acc = mfma16(quad_fragment<VN, 3>(k.h[0]), as_bf16x8(k.w[3]), acc);
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            if (f == 0 || cs + f < ce) acc[f % NA] = mfma16(k.h[0][f / NA], as_bf16x8(k.w[f]), acc[f % NA]);
         } else {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             if (cs + u < ce) {
               const float sc = scale_of_word(k.sc, cs + u);
-              acc = mfma16(quad_fragment<VN, 0>(k.h[u]), fp4x8_to_bf16x8(k.w[u][0], sc), acc);
-              acc = mfma16(quad_fragment<VN, 1>(k.h[u]), fp4x8_to_bf16x8(k.w[u][1], sc), acc);
-              acc = mfma16(quad_fragment<VN, 2>(k.h[u]), fp4x8_to_bf16x8(k.w[u][2], sc), acc);
-              acc = mfma16(quad_fragment<VN, 3>(k.h[u]), fp4x8_to_bf16x8(k.w[u][3], sc), acc);
+#pragma unroll
+              for (int f = 0; f < 4; ++f)
+                acc[f % NA] = mfma16(k.h[u][f / NA], fp4x8_to_bf16x8(k.w[u][f], sc), acc[f % NA]);
             }
           }
         }
@@ -755,10 +750,14 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
         if (cs < ce) continue;
 #pragma unroll
         for (int v = 0; v < VN; ++v) {
-          float d = acc[v];
+          float d;
           if constexpr (HALF) {
-            if (c >= 8) d = acc[v + 2];
+            d = c < 8 ? acc[0][v] : acc[0][v + 2];
             d += __shfl_xor(d, 8, 64);
+          } else {
+            d = acc[0][v];
+#pragma unroll
+            for (int f = 1; f < NA; ++f) d += acc[f][v + VN * f];
           }
           const int i = g + 4 * v;
           if (i < m && c < COLS) {
@@ -766,7 +765,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
             val[(part * nrows + row) * COLS + c] = d;
           }
         }
-        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        clear();
         cr += stride;
         more = cr < runs;
         if (!more) break;

@@ -192,8 +192,8 @@ __device__ __forceinline__ void load_params(W4Params<FMT, G>& p, __amdgpu_buffer
 // acc[r][nt] += x . W^T over step u (0 or 1) of a pair of steps, for R row tiles (codes
 // w[r], parameters p[r]) and NT token tiles; frag(nt, m) is the token fragment m of the
 // step.  INT4: a group's products and activation sums are formed first (d, xs), then
-// scale (d - zero xs) is added to the f32 accumulator; VN of a tile's elements hold tokens.
-template <int FMT, int G, int R, int NT, int VN, typename Frag>
+// scale (d - zero xs) is added to the f32 accumulator.
+template <int FMT, int G, int R, int NT, typename Frag>
 __device__ __forceinline__ void w4_step(f32x4 (&acc)[R][NT], const u32x4 (&w)[R],
                                         const W4Params<FMT, G> (&p)[R], int u, int step, const Frag& frag) {
   if constexpr (FMT == kW4Mxfp4) {
@@ -239,7 +239,7 @@ __device__ __forceinline__ void w4_step(f32x4 (&acc)[R][NT], const u32x4 (&w)[R]
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int v = 0; v < VN; ++v) acc[r][nt][v] = fmaf(sc, fmaf(-z, xs[nt][v], d[r][nt][v]), acc[r][nt][v]);
+            for (int v = 0; v < 4; ++v) acc[r][nt][v] = fmaf(sc, fmaf(-z, xs[nt][v], d[r][nt][v]), acc[r][nt][v]);
         }
       }
     }
@@ -261,32 +261,52 @@ __device__ __forceinline__ void store_y(const W4Args& a, int64_t row, int64_t co
 // block's contiguous range of row tiles through a few buffers of two steps.  At the end
 // of a tile the block adds the waves' parts in LDS, in ascending order (two buffers, one
 // barrier per tile, which waits for no load).  Up to 4 VN tokens, in a quad of lanes the
-// same token would be held 4 / VN times: there each lane loads another fragment, and quad
-// permutes hand them to the products (VN = 4: every lane its own).
+// same token would be held 4 / VN times: there each lane loads another fragment (VN = 4:
+// every lane its own token).
 template <int VN, int NC>
 struct W4Bufs {  // as many as the registers of 16 waves hold
   static constexpr int value = NC == 0 || (NC == 2 && VN == 4) ? 2 : VN == 4 ? 3 : 4;
 };
 
-template <int VN>
-__device__ __forceinline__ u32x4 quad_pick(const u32x4 (&x)[VN], int m) {
-  if constexpr (VN == 4) return x[m];
-  const int lo = VN == 1 ? m : 2 * (m & 1), hi = VN == 1 ? m : lo + 1;
-  const u32x4 v = x[VN == 1 ? 0 : m / 2];
-  u32x4 o;
+
+// acc += x . W^T over one step of a row tile (codes w, parameters p), for up to 4 VN tokens
+// whose fragments are quad-loaded: x[l] holds fragments l * NA + f, f < NA = 4 / VN, fragment
+// f in the quads' lanes f VN .. f VN + VN - 1.  A product with fragment f's weights takes
+// x[l] as it is and is right in its elements from f VN on; pick() gathers them.
+template <int FMT, int G, int VN>
+__device__ __forceinline__ void w4_step_few(float (&acc)[VN], f32x4 (&part)[4 / VN], u32x4 w, const W4Params<FMT, G>& p,
+                                            int u, int step, const u32x4 (&x)[VN]) {
+  constexpr int NA = 4 / VN;
+  if constexpr (FMT == kW4Mxfp4) {
+    const float sc = scale_of_word(p.v[0], step);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // the permute is an immediate of the instruction
-    switch (lo * 4 + hi) {
-      case 0: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0x00, 0xf, 0xf, true); break;
-      case 5: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0x55, 0xf, 0xf, true); break;
-      case 10: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0xaa, 0xf, 0xf, true); break;
-      case 15: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0xff, 0xf, 0xf, true); break;
-      case 1: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0x44, 0xf, 0xf, true); break;
-      default: o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], 0xee, 0xf, 0xf, true); break;
+    for (int m = 0; m < 4; ++m) part[m % NA] = mfma16(x[m / NA], fp4x8_to_bf16x8(w[m], sc), part[m % NA]);
+  } else {
+    constexpr int B = G / 32;  // products per group
+    const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    f32x4 d[4], xs[VN];
+#pragma unroll
+    for (int l = 0; l < VN; ++l) xs[l] = mfma16(x[l], as_bf16x8(ones), zero);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) d[m] = mfma16(x[m / NA], int4x8_to_bf16x8(w[m]), zero);
+#pragma unroll
+    for (int m0 = 0; m0 < 4; m0 += B) {
+      const uint32_t pw = p.v[(4 * u + m0) / B];
+      const float sc = f16_lo(pw), z = f16_hi(pw);
+#pragma unroll
+      for (int v = 0; v < VN; ++v) {
+        float ds = 0.f, xsum = 0.f;
+#pragma unroll
+        for (int m = m0; m < m0 + B; ++m) {
+          const float dm = d[m][v + VN * (m % NA)], xm = xs[m / NA][v + VN * (m % NA)];
+          ds = m == m0 ? dm : ds + dm;
+          xsum = m == m0 ? xm : xsum + xm;
+        }
+        acc[v] = fmaf(sc, fmaf(-z, xsum, ds), acc[v]);
+      }
     }
   }
-  return o;
 }
 
 template <int FMT, int G, int VN, int NC, bool BF16OUT>
@@ -321,8 +341,8 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
   }
 
   struct Buf {
-    u32x4 w[2][1];
-    W4Params<FMT, G> p[1];
+    u32x4 w[2];
+    W4Params<FMT, G> p;
     u32x4 x[NC ? 1 : 2][VN];
   };
   Buf buf[B];
@@ -333,10 +353,10 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const bool live = iq < hi && step + u < sh.nk;
-      b.w[u][0] = bld16(make_rsrc(codes, live ? sh.code_tile : 0), lane * 16, live ? (step + u) * 1024 : 0);
+      b.w[u] = bld16(make_rsrc(codes, live ? sh.code_tile : 0), lane * 16, live ? (step + u) * 1024 : 0);
     }
     const bool live = iq < hi && step < sh.nk;
-    load_params<FMT, G>(b.p[0], make_rsrc(a.w + sh.par_at + (size_t)iq * sh.par_tile, live ? sh.par_tile : 0), step, live);
+    load_params<FMT, G>(b.p, make_rsrc(a.w + sh.par_at + (size_t)iq * sh.par_tile, live ? sh.par_tile : 0), step, live);
     if constexpr (NC == 0) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) load_x(b.x[u], step + u);
@@ -348,21 +368,49 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
   };
 #pragma unroll
   for (int b = 0; b < B; ++b) issue(buf[b]);
-  f32x4 acc[1][1];
-  acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // MXFP4, and 16 tokens, add up in the products' accumulators, INT4 in acc
+  constexpr int NA = 4 / VN;
+  float acc[VN];
+  f32x4 sums[NA];
+  auto clear = [&]() {
+#pragma unroll
+    for (int v = 0; v < VN; ++v) acc[v] = 0.f;
+#pragma unroll
+    for (int f = 0; f < NA; ++f) sums[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  clear();
   int q = lo, half = 0;
   const int red_tile = VN * waves * 64;
   auto compute = [&](const Buf& b, int c, const u32x4(&x0)[VN], const u32x4(&x1)[VN]) {
     const int step = step0 + 2 * c;
-    if (step < sh.nk) w4_step<FMT, G, 1, 1, VN>(acc, b.w[0], b.p, 0, step, [&](int, int f) { return quad_pick<VN>(x0, f); });
-    if (step + 1 < sh.nk)
-      w4_step<FMT, G, 1, 1, VN>(acc, b.w[1], b.p, 1, step + 1, [&](int, int f) { return quad_pick<VN>(x1, f); });
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (step + u >= sh.nk) continue;
+      const u32x4(&x)[VN] = u ? x1 : x0;
+      if constexpr (VN == 4) {  // every lane its own token: the products of a group chain
+        const u32x4 w[1] = {b.w[u]};
+        const W4Params<FMT, G> p[1] = {b.p};
+        f32x4 a1[1][1] = {{sums[0]}};
+        w4_step<FMT, G, 1, 1>(a1, w, p, u, step + u, [&](int, int f) { return x[f]; });
+        sums[0] = a1[0][0];
+      } else {
+        w4_step_few<FMT, G, VN>(acc, sums, b.w[u], b.p, u, step + u, x);
+      }
+    }
   };
   auto tile_end = [&]() {  // returns whether a tile is left
     float* part = red + half * red_tile;
 #pragma unroll
-    for (int v = 0; v < VN; ++v) part[(v * waves + kp) * 64 + lane] = acc[0][0][v];
-    acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int v = 0; v < VN; ++v) {
+      float d = acc[v];
+      if constexpr (FMT == kW4Mxfp4 || VN == 4) {
+        d = sums[0][v];
+#pragma unroll
+        for (int f = 1; f < NA; ++f) d += sums[f][v + VN * f];
+      }
+      part[(v * waves + kp) * 64 + lane] = d;
+    }
+    clear();
     lds_barrier();
     // element v by wave (q VN + v) % waves: lane = (token % 4, row)
     for (int v = 0; v < VN; ++v) {
@@ -481,7 +529,7 @@ __global__ __launch_bounds__(64 * kWideWaves) void w4_wide(W4Args a) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
       if (2 * s + u < sh.nk)
-        w4_step<FMT, G, R, NT, 4>(acc, b.w[u], b.p, u, 2 * s + u, [&](int nt, int f) {
+        w4_step<FMT, G, R, NT>(acc, b.w[u], b.p, u, 2 * s + u, [&](int nt, int f) {
           return *reinterpret_cast<const u32x4*>(x + nt * 16 * LD + u * 256 + (FMT == kW4Mxfp4 ? 64 * g + 16 * f : 64 * f + 16 * g));
         });
     store_slice((s + 1) & 1);
