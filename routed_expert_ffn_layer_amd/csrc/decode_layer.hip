@@ -579,12 +579,12 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
 // The vector memory pipe, not HBM, is what a 4-bit stream runs into here (an h fragment
 // for every 256 bytes of codes: with four fragment loads and a scale load beside each code
 // load the MXFP4 kernel took 86 us at 64 tokens, 28 us of them its codes).  Runs are
-// therefore short, 4 VN tokens, and one load brings several fragments: in a quad of lanes,
-// which would hold the same token four times (VN = 1) or two tokens twice (VN = 2), each
-// lane loads another fragment.  Such an operand goes into the products of all its
-// fragments' weights as it is: of row 4 i + j of a product only the fragment that lane j
-// loaded means something, so fragment f adds up in accumulator f % (4 / VN), whose
-// elements from VN (f % (4 / VN)) on are the tokens' sums.
+// therefore short, 4 VN tokens, and a load brings four fragments: lane j of a quad, where all
+// four would hold the same token, loads its fragment j, so that a load reads whole 64-byte
+// pieces (256 consecutive bytes of each of 4 tokens for MXFP4).  Such an operand goes into the
+// products of all its fragments' weights as it is: of row 4 i + j of a product only
+// fragment j means something, so fragment f adds up in an accumulator of its own, whose
+// element f is the token's sum.
 // ---------------------------------------------------------------------------
 //
 // HALF: a block owns 8 columns of y, half a row tile (H / 8 blocks where H / 16 would leave
@@ -600,7 +600,7 @@ struct DnTune {
   static constexpr int wloads = HALF ? units / 2 : units;           // code loads of a chunk
   static constexpr int groups = HALF || WT == W_BF16 ? 1 : 2;       // groups of h loads
   static constexpr int hloads = HALF && WT == W_MXFP4 ? 4 : VN;     // h loads of a group
-  static constexpr int bufs = VN == 1 ? 4 : 3;
+  static constexpr int bufs = VN == 1 ? 4 : HALF || WT == W_BF16 ? 3 : 2;
 };
 
 template <int WT, int VN, bool HALF>
@@ -614,7 +614,7 @@ template <int WT, int VN, bool HALF, bool BF16OUT>
 __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int log_parts) {
   using Tune = DnTune<WT, VN, HALF>;
   constexpr int U = Tune::units, NG = Tune::groups, NH = Tune::hloads, B = Tune::bufs, P = 4 * VN;
-  constexpr int COLS = HALF ? 8 : 16, NA = HALF ? 1 : 4 / VN;  // columns of y; accumulators
+  constexpr int COLS = HALF ? 8 : 16, NA = HALF ? 1 : 4, NR = HALF ? 1 : VN;  // columns of y; accumulators; quads' tokens
   static_assert(!HALF || VN == 2, "half tiles hold two tokens a quad");
   __shared__ DlShared s;
   __shared__ float w[kDlMaxPairs];
@@ -653,7 +653,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
   const int w_off = frag * 16 + w_step * 1024;
 
   // Issue side: run ir, steps is .. ie-1 of it.
-  int ir = (wv >> log_parts) - stride, is = 0, ie = 0, i_row = 0, i_w2 = 0, i_sc = 0;
+  int ir = (wv >> log_parts) - stride, is = 0, ie = 0, i_row[NR], i_w2 = 0, i_sc = 0;
   const uint8_t* iw = nullptr;
   int ibytes = 0;
   auto issue_run = [&]() {
@@ -667,8 +667,11 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
     i_w2 = (shared ? sh.c13 : rt.c13) + tile * nk * 1024;
     i_sc = (shared ? sh.c13 + sh.c2 + sh.s13 : rt.c13 + rt.c2 + rt.s13) + tile * ((nk + 15) / 16) * 1024;
     part_steps(nk, is, ie);
-    const int tok = (c >> 2) + (VN == 2 ? 4 * (j & 1) : 0), i = min(tok, r.m - 1);
-    i_row = (shared ? n + r.at + i : s.sorted[r.at + i]) * a.h_ld * 2 + (WT == W_MXFP4 ? 64 : 16) * g;
+    #pragma unroll
+    for (int l = 0; l < NR; ++l) {
+      const int i = min((c >> 2) + 4 * (HALF ? j & 1 : l), r.m - 1);
+      i_row[l] = (shared ? n + r.at + i : s.sorted[r.at + i]) * a.h_ld * 2 + (WT == W_MXFP4 ? 64 : 16) * g;
+    }
   };
   auto issue = [&](DnBuf<WT, VN, HALF>& b) {
 #pragma unroll
@@ -685,16 +688,15 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
               wbuf, frag * 16, live ? i_sc + step / 16 * 1024 + step % 16 / 4 * 4 : 0, 0);
       const int hs = live ? step * (WT == W_MXFP4 ? 256 : 64) : 0;
       if constexpr (HALF && WT == W_BF16) {
-        b.h[0][u / 2] = bld16(hbuf, pair || h_step == 0 ? i_row + 64 * h_step : kPastEnd, hs);
+        b.h[0][u / 2] = bld16(hbuf, pair || h_step == 0 ? i_row[0] + 64 * h_step : kPastEnd, hs);
       } else if constexpr (HALF) {
 #pragma unroll
         for (int f = 0; f < 4; ++f)
-          b.h[0][f] = bld16(hbuf, pair || h_step == 0 ? i_row + 256 * h_step + 16 * f : kPastEnd, hs);
+          b.h[0][f] = bld16(hbuf, pair || h_step == 0 ? i_row[0] + 256 * h_step + 16 * f : kPastEnd, hs);
       } else if (u < NG) {
-        // load l: fragment f of this lane's token (bf16: 64 bytes a step; MXFP4: 16 bytes)
+        // load l: tokens 4 l .. 4 l + 3, fragment j (bf16: 64 bytes a step; MXFP4: 16 bytes)
 #pragma unroll
-        for (int l = 0; l < NH; ++l)
-          b.h[u][l] = bld16(hbuf, i_row + (WT == W_MXFP4 ? 16 : 64) * (VN == 1 ? j : 2 * l + (j >> 1)), hs);
+        for (int l = 0; l < NH; ++l) b.h[u][l] = bld16(hbuf, i_row[l] + (WT == W_MXFP4 ? 16 : 64) * j, hs);
       }
     }
     is += U;
@@ -713,10 +715,12 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
 #pragma unroll
     for (int b = 0; b < B; ++b) issue(buf[b]);
     enter_run();
-    f32x4 acc[NA];
+    f32x4 acc[NR][NA];
     auto clear = [&]() {
 #pragma unroll
-      for (int f = 0; f < NA; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int l = 0; l < NR; ++l)
+#pragma unroll
+        for (int f = 0; f < NA; ++f) acc[l][f] = f32x4{0.f, 0.f, 0.f, 0.f};
     };
     clear();
     for (bool more = true; more;) {
@@ -724,24 +728,29 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
       for (int b = 0; b < B; ++b) {
         const DnBuf<WT, VN, HALF>& k = buf[b];
         if constexpr (HALF && WT == W_BF16) {
-          acc[0] = mfma16(k.h[0][0], as_bf16x8(k.w[0]), acc[0]);
-          if (cs + 2 < ce) acc[0] = mfma16(k.h[0][1], as_bf16x8(k.w[1]), acc[0]);
+          acc[0][0] = mfma16(k.h[0][0], as_bf16x8(k.w[0]), acc[0][0]);
+          if (cs + 2 < ce) acc[0][0] = mfma16(k.h[0][1], as_bf16x8(k.w[1]), acc[0][0]);
         } else if constexpr (HALF) {
           const float sc = e8m0_to_f32(k.sc >> (8 * ((cs & 3) + w_step)) & 0xffu);
 #pragma unroll
-          for (int f = 0; f < 4; ++f) acc[0] = mfma16(k.h[0][f], fp4x8_to_bf16x8(k.w[0][f], sc), acc[0]);
+          for (int f = 0; f < 4; ++f) acc[0][0] = mfma16(k.h[0][f], fp4x8_to_bf16x8(k.w[0][f], sc), acc[0][0]);
         } else if constexpr (WT == W_BF16) {
 #pragma unroll
           for (int f = 0; f < 4; ++f)
-            if (f == 0 || cs + f < ce) acc[f % NA] = mfma16(k.h[0][f / NA], as_bf16x8(k.w[f]), acc[f % NA]);
+            if (f == 0 || cs + f < ce)
+#pragma unroll
+              for (int l = 0; l < NR; ++l) acc[l][f] = mfma16(k.h[0][l], as_bf16x8(k.w[f]), acc[l][f]);
         } else {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             if (cs + u < ce) {
               const float sc = scale_of_word(k.sc, cs + u);
 #pragma unroll
-              for (int f = 0; f < 4; ++f)
-                acc[f % NA] = mfma16(k.h[u][f / NA], fp4x8_to_bf16x8(k.w[u][f], sc), acc[f % NA]);
+              for (int f = 0; f < 4; ++f) {
+                const bf16x8 wf = fp4x8_to_bf16x8(k.w[u][f], sc);
+#pragma unroll
+                for (int l = 0; l < NR; ++l) acc[l][f] = mfma16(k.h[u][l], wf, acc[l][f]);
+              }
             }
           }
         }
@@ -752,12 +761,12 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
         for (int v = 0; v < VN; ++v) {
           float d;
           if constexpr (HALF) {
-            d = c < 8 ? acc[0][v] : acc[0][v + 2];
+            d = c < 8 ? acc[0][0][v] : acc[0][0][v + 2];
             d += __shfl_xor(d, 8, 64);
           } else {
-            d = acc[0][v];
+            d = acc[v][0][0];
 #pragma unroll
-            for (int f = 1; f < NA; ++f) d += acc[f][v + VN * f];
+            for (int f = 1; f < NA; ++f) d += acc[v][f][f];
           }
           const int i = g + 4 * v;
           if (i < m && c < COLS) {
