@@ -138,7 +138,7 @@ def _torch():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
@@ -149,6 +149,18 @@ def _stream(stream):
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _stream_of(stream, *tensors):
+    """_stream for a call on these tensors: they have to be on the current device, whose
+    stream the kernels run on."""
+    dev = _torch().cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise MoeError(MOE_EINVAL, f"tensor on {t.device}, the current device is cuda:{dev}")
+    if stream is None:
+        return _torch_mod._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def moe_abi_version():
@@ -257,9 +269,10 @@ def moe_layer_decode_workspace(T, k, E, H, I, I_shared, wdt):
 def moe_layer_decode(wdt, slot_pool, slot_stride, slot_of_expert, shared_w, I_shared, x, logits, T, k, E, H, I,
                      topk_ids, topk_w, y, ydt, workspace, stream=None):
     """logits None: topk_ids and topk_w are read instead of written."""
+    st = _stream_of(stream, slot_pool, slot_of_expert, shared_w, x, logits, topk_ids, topk_w, y, workspace)
     _check(lib().moe_layer_decode(wdt, _ptr(slot_pool), slot_stride, _ptr(slot_of_expert), _ptr(shared_w), I_shared,
                                   _ptr(x), _ptr(logits), T, k, E, H, I, _ptr(topk_ids), _ptr(topk_w), _ptr(y), ydt,
-                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+                                  _ptr(workspace), workspace.numel() * workspace.element_size(), st))
 
 
 def moe_w4_bytes(fmt, N, K, group):
@@ -267,18 +280,24 @@ def moe_w4_bytes(fmt, N, K, group):
 
 
 def moe_w4_pack(fmt, codes, scales, zeros, N, K, group, w, stream=None):
-    _check(lib().moe_w4_pack(fmt, _ptr(codes), _ptr(scales), _ptr(zeros), N, K, group, _ptr(w), _stream(stream)))
+    if w.numel() * w.element_size() < moe_w4_bytes(fmt, N, K, group):
+        raise MoeError(MOE_ECAPACITY, f"w holds {w.numel() * w.element_size()} bytes of "
+                       f"{moe_w4_bytes(fmt, N, K, group)}")
+    st = _stream_of(stream, codes, scales, zeros, w)
+    _check(lib().moe_w4_pack(fmt, _ptr(codes), _ptr(scales), _ptr(zeros), N, K, group, _ptr(w), st))
 
 
 def moe_w4_linear(fmt, w, N, K, group, x, bias, y, stream=None):
-    """x [T][K] bf16 and y [T][N] (f32 or bf16) with unit stride along their rows."""
-    import torch
-    ydt = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(y.dtype, -1)
+    """x [T][K] bf16 and y [T][N] (f32 or bf16), each with unit stride along its rows."""
     T = x.shape[0]
+    if x.shape[1] != K or tuple(y.shape) != (T, N) or (T and (x.stride(1) != 1 and K > 1 or y.stride(1) != 1 and N > 1)):
+        raise MoeError(MOE_EINVAL, f"x {tuple(x.shape)}, y {tuple(y.shape)} for a product of [T][{K}] to [T][{N}] "
+                       "with unit stride along the rows")
+    ydt = MOE_F32 if y.dtype is _torch().float32 else MOE_BF16 if y.dtype is _torch_mod.bfloat16 else -1
     # the stride of a single row's dimension means nothing
     x_ld, y_ld = (x.stride(0), y.stride(0)) if T > 1 else (K, N)
-    _check(lib().moe_w4_linear(fmt, _ptr(w), N, K, group, _ptr(x), x_ld, T, _ptr(bias), _ptr(y), y_ld, ydt,
-                               _stream(stream)))
+    st = _stream_of(stream, w, x, bias, y)
+    _check(lib().moe_w4_linear(fmt, _ptr(w), N, K, group, _ptr(x), x_ld, T, _ptr(bias), _ptr(y), y_ld, ydt, st))
 
 
 class MoeCache:

@@ -240,6 +240,24 @@ def test_replays_and_streams(fmt, group, T):
     assert torch.equal(a, refs[1]) and torch.equal(b, refs[2])
 
 
+def test_refusals_of_the_binding():
+    """Shapes, strides and devices that the C entry cannot see."""
+    N, K = 32, 64
+    w = torch.zeros(moe.moe_w4_bytes(moe.MOE_INT4, N, K, 64), dtype=torch.uint8, device=dev())
+    x, y = torch.zeros((3, K), dtype=torch.bfloat16, device=dev()), torch.zeros((3, N), device=dev())
+    call = lambda x, y, w=w: moe.moe_w4_linear(moe.MOE_INT4, w, N, K, 64, x, None, y)
+    call(x, y)
+    for bx, by, bw in ((x[:, :32], y, w), (x, y[:2], w), (x, y[:, :16], w), (x, y.double(), w), (x.cpu(), y, w), (x, y, w.cpu()),
+                       (torch.zeros((K, 3), dtype=torch.bfloat16, device=dev()).t(), y, w),
+                       (x, torch.zeros((N, 3), device=dev()).t(), w)):
+        with pytest.raises(moe.MoeError) as e:
+            call(bx, by, bw)
+        assert e.value.status == moe.MOE_EINVAL
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_w4_pack(moe.MOE_INT4, w, w, None, N, K, 64, w[:-1])
+    assert e.value.status == moe.MOE_ECAPACITY
+
+
 @pytest.mark.parametrize("fmt,group", [(moe.MOE_MXFP4, 32), (moe.MOE_INT4, 128)])
 def test_a_decode_step_together(ora, fmt, group):
     """Projection with 4-bit weights, router logits with 4-bit weights, the layer on them, and
