@@ -27,7 +27,7 @@ constexpr int kDlMaxPairs = kDecodeLayerMaxPairs;
 constexpr int kDlWaves = 16;  // waves of a block, one block per CU
 constexpr int kDlThreads = 64 * kDlWaves;
 constexpr int kDlTeams = 4;  // gate/up: teams of a block, a tile each
-constexpr int kDlHalfTiles = 256;  // row tiles of W2 below which the down kernel's blocks own half a tile
+constexpr int kDlHalfTiles = 128;  // row tiles of W2 up to which the down kernel's blocks own half a tile
 constexpr int kDlOneQuadT = 8;  // batches whose down runs hold up to 4 pairs, larger ones up to 8
 
 // A run: pairs of one expert (or tokens of the shared expert) that one matrix tile serves.
@@ -851,7 +851,7 @@ static hipError_t launch_t(const DecodeLayerArgs& a, bool bf16_out, hipStream_t 
   const int64_t sh_turns = (a.I_shared / 8 + kDlTeams - 1) / kDlTeams, rt_turns = (a.I / 8 + kDlTeams - 1) / kDlTeams;
   const int64_t bound = (a.shared_w ? (a.T + P - 1) / P * sh_turns : 0) + n * rt_turns;  // every pair a run
   const unsigned grid = (unsigned)(bound < 256 ? bound : 256);
-  const bool half = a.H / 16 < kDlHalfTiles;
+  const bool half = a.H / 16 <= kDlHalfTiles;
   const int vn = a.T <= kDlOneQuadT && !half ? 1 : 2;
   hipLaunchKernelGGL(decode_gate_up<WT>, dim3(grid), dim3(kDlThreads), lds, st, a, P, 4 * vn, rb, resident);
   const hipError_t e = hipGetLastError();

@@ -289,15 +289,16 @@ def moe_w4_pack(fmt, codes, scales, zeros, N, K, group, w, stream=None):
 
 def moe_w4_linear(fmt, w, N, K, group, x, bias, y, stream=None):
     """x [T][K] bf16 and y [T][N] (f32 or bf16), each with unit stride along its rows."""
-    T = x.shape[0]
-    if x.shape[1] != K or tuple(y.shape) != (T, N) or (T and (x.stride(1) != 1 and K > 1 or y.stride(1) != 1 and N > 1)):
+    T, (x_ld, x_unit), (y_ld, y_unit) = x.shape[0], x.stride(), y.stride()
+    if x.shape != (T, K) or y.shape != (T, N) or x_unit != 1 or (y_unit != 1 and N > 1):
         raise MoeError(MOE_EINVAL, f"x {tuple(x.shape)}, y {tuple(y.shape)} for a product of [T][{K}] to [T][{N}] "
                        "with unit stride along the rows")
     ydt = MOE_F32 if y.dtype is _torch().float32 else MOE_BF16 if y.dtype is _torch_mod.bfloat16 else -1
-    # the stride of a single row's dimension means nothing
-    x_ld, y_ld = (x.stride(0), y.stride(0)) if T > 1 else (K, N)
+    if T <= 1:  # the stride of a single row's dimension means nothing
+        x_ld, y_ld = K, N
     st = _stream_of(stream, w, x, bias, y)
-    _check(lib().moe_w4_linear(fmt, _ptr(w), N, K, group, _ptr(x), x_ld, T, _ptr(bias), _ptr(y), y_ld, ydt, st))
+    _check(lib().moe_w4_linear(fmt, w.data_ptr(), N, K, group, x.data_ptr(), x_ld, T, _ptr(bias), y.data_ptr(), y_ld, ydt,
+                               st))
 
 
 class MoeCache:
