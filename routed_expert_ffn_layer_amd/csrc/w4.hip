@@ -27,7 +27,12 @@
 
 namespace moe {
 
-constexpr int kW4WideTiles = 1024;  // row tiles from which 17 or more tokens take the wide kernel
+// More than 16 tokens: w4_few reads the codes once per 16 tokens, w4_wide once per 64 with blocks
+// of 4 row tiles (4 waves of one) or 16 (8 waves of two, which read a token from LDS half as
+// often).  Measured at K = 4096: 64 tokens, N = 2048: w4_few 14 us, w4_wide 25; N = 4096: 26 and 22;
+// N = 12288: 39 and 27; N = 32768: 4-tile blocks 42, 16-tile blocks 48; N = 65536: 83 and 59.
+constexpr int kW4WideWork = 1024;   // row tiles x passes of 16 tokens from which w4_wide is taken
+constexpr int kW4WideTiles = 2800;  // row tiles from which its blocks have 16
 
 size_t w4_code_bytes(int N, int K) { return (size_t)((N + 15) / 16) * ((K + 127) / 128) * 1024; }
 
@@ -452,29 +457,27 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
   }
 }
 
-// 17 to 64 tokens and many rows.  A wave owns R row tiles over the whole of K, a block of 8
-// waves 128 R rows; the tokens pass through LDS in slices of two column steps shared by the
+// 17 to 64 tokens a block.  A wave owns R row tiles over the whole of K, a block of W waves
+// 16 R W rows; the tokens pass through LDS in slices of two column steps shared by the
 // waves (two buffers: the next slice travels to registers while this one is multiplied,
 // one barrier per slice), each fragment read from LDS serving R products.  The codes of
 // up to three slices are in flight in registers.
-constexpr int kWideR = 2, kWideWaves = 8;
-
-template <int FMT, int G, int NT, bool BF16OUT>
-__global__ __launch_bounds__(64 * kWideWaves) void w4_wide(W4Args a) {
-  constexpr int R = kWideR, ROWS = 16 * NT, LD = 512 + 16;
-  constexpr int PIECES = ROWS * 32 / (64 * kWideWaves);  // 16-byte pieces of a slice per thread
+template <int FMT, int G, int R, int W, int NT, bool BF16OUT>
+__global__ __launch_bounds__(64 * W) void w4_wide(W4Args a) {
+  constexpr int ROWS = 16 * NT, LD = 512 + 16;
+  constexpr int PIECES = ROWS * 32 / (64 * W);  // 16-byte pieces of a slice per thread
   __shared__ __attribute__((aligned(16))) uint8_t xs[2][ROWS * LD];
   const int lane = threadIdx.x & 63, g = lane >> 4, wv = uniform(threadIdx.x >> 6);
   const int t0 = blockIdx.y * 64, m = min(ROWS, a.T - t0);
   const W4Shape sh(FMT, a.N, a.K, G);
   const int tiles = (a.N + 15) / 16;
-  const int tile0 = (blockIdx.x * kWideWaves + wv) * R;
+  const int tile0 = (blockIdx.x * W + wv) * R;
   const int slices = (sh.nk + 1) / 2;
   const __amdgpu_buffer_rsrc_t xbuf = make_rsrc(a.x + (size_t)t0 * a.x_ld, ((size_t)(m - 1) * a.x_ld + a.K) * 2);
   int x_off[PIECES], x_lds[PIECES], x_col[PIECES];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
-    const int c = threadIdx.x + i * 64 * kWideWaves, row = c >> 5, pc = c & 31;
+    const int c = threadIdx.x + i * 64 * W, row = c >> 5, pc = c & 31;
     x_off[i] = min(row, m - 1) * (int)a.x_ld * 2 + pc * 16;
     x_lds[i] = row * LD + pc * 16;
     x_col[i] = pc * 8;
@@ -557,11 +560,14 @@ __global__ __launch_bounds__(64 * kWideWaves) void w4_wide(W4Args a) {
 template <int FMT, int G, bool BF16OUT>
 static void launch_t(const W4Args& a, hipStream_t st) {
   const int tiles = (a.N + 15) / 16, pairs = ((a.K + 127) / 128 + 1) / 2;
-  if (a.T > 16 && tiles >= kW4WideTiles) {
-    const dim3 grid((unsigned)((tiles + kWideR * kWideWaves - 1) / (kWideR * kWideWaves)), (unsigned)((a.T + 63) / 64));
-    const dim3 block(64 * kWideWaves);
-    if (a.T <= 32) hipLaunchKernelGGL((w4_wide<FMT, G, 2, BF16OUT>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((w4_wide<FMT, G, 4, BF16OUT>), grid, block, 0, st, a);
+  if (a.T > 16 && (int64_t)tiles * ((a.T + 15) / 16) >= kW4WideWork) {
+    const bool wide = tiles >= kW4WideTiles;
+    const int rows = wide ? 16 : 4;  // row tiles of a block
+    const dim3 grid((unsigned)((tiles + rows - 1) / rows), (unsigned)((a.T + 63) / 64));
+    if (wide && a.T <= 32) hipLaunchKernelGGL((w4_wide<FMT, G, 2, 8, 2, BF16OUT>), grid, dim3(512), 0, st, a);
+    else if (wide) hipLaunchKernelGGL((w4_wide<FMT, G, 2, 8, 4, BF16OUT>), grid, dim3(512), 0, st, a);
+    else if (a.T <= 32) hipLaunchKernelGGL((w4_wide<FMT, G, 1, 4, 2, BF16OUT>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((w4_wide<FMT, G, 1, 4, 4, BF16OUT>), grid, dim3(256), 0, st, a);
     return;
   }
   const int nc = (pairs + 15) / 16, waves = (pairs + nc - 1) / nc;
