@@ -92,7 +92,16 @@ SHAPES = [
     (130, 31, 288, True, False),
     (1, 20000, 512, False, True),
     (7, 9000, 8192, False, False),
-    (64, 5000, 4096, False, False),
+    (64, 5000, 4096, False, False),   # blocks of 4 row tiles
+    (20, 9000, 416, True, True),
+    (20, 45003, 256, False, False),   # blocks of 16
+    (64, 45003, 160, True, True),
+    (70, 45000, 288, False, False),   # and a second pass of 6 tokens
+    (1, 200, 8192, False, False),     # two chunks of steps per wave
+    (16, 100, 6112, False, True),
+    (3, 64, 9024, True, False),       # more than two
+    (6, 40, 9024, False, False),
+    (12, 33, 16384, False, False),
 ]
 
 
