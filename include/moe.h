@@ -382,7 +382,7 @@ int moe_combine(const float* out_rows, const float* topk_w, const int32_t* inv_r
  *   workspace >= moe_layer_decode_workspace() bytes, written by the call (two calls that
  *             may overlap need one each)
  * bf16 or MXFP4 weights (MOE_EUNSUPPORTED otherwise), T <= MOE_LAYER_DECODE_MAX_T,
- * T*k <= MOE_LAYER_DECODE_MAX_PAIRS, H <= 65536 and experts under 2 GiB
+ * T*k <= MOE_LAYER_DECODE_MAX_PAIRS, H <= 65536, experts and intermediate under 2 GiB
  * (MOE_EUNSUPPORTED beyond: use the separate calls).
  * Asynchronous, allocates nothing, may be captured into a graph. */
 #define MOE_LAYER_DECODE_MAX_T 64
@@ -401,8 +401,8 @@ int moe_layer_decode(int wdt, const void* slot_pool, size_t slot_stride, const i
  *   MOE_MXFP4: W = E2M1(code) * 2^(scale - 127), blocks of 32 along k (OCP MX v1.0)
  *   MOE_INT4:  W = s * (q - z), q the code 0..15, s (f16) and z (0..255) one per row
  *              and group of `group` = 32, 64 or 128 consecutive k
- * N >= 1, K a positive multiple of 32 and at most 2^20 (the last group may be partial,
- * group must be 32 for MOE_MXFP4), N * K < 2^40.
+ * 1 <= N <= 2^30, K a positive multiple of 32 and at most 2^20 (the last group may be
+ * partial, group must be 32 for MOE_MXFP4), N * K < 2^40.
  *
  * moe_w4_pack lays the weights out once for the products:
  *   codes   [N][K/2], element 2i of a row in the low nibble of byte i
@@ -411,9 +411,10 @@ int moe_layer_decode(int wdt, const void* slot_pool, size_t slot_stride, const i
  *   w       moe_w4_bytes() bytes (0 for invalid shapes)
  *
  * moe_w4_linear: x rows of K bf16, x_ld elements apart (x_ld >= K, a multiple of 8, at
- * most 2^22); y rows of N elements of ydt (MOE_F32 or MOE_BF16), y_ld >= N apart; bias [N] f32 or
- * NULL.  Any T >= 0: the weights stream once per 64 tokens.  Products are exact, sums are in
- * f32 in a fixed order, one rounding to ydt.  Asynchronous, no workspace. */
+ * most 2^22); y rows of N elements of ydt (MOE_F32 or MOE_BF16), y_ld >= N apart, not
+ * overlapping x; bias [N] f32 or NULL.  0 <= T <= 2^19: the weights are read once for up to 16
+ * tokens, or (many rows) 64, and again for every such batch.  Products are exact, sums
+ * are in f32 in a fixed order, one rounding to ydt.  Asynchronous, no workspace. */
 enum { MOE_INT4 = 4 };
 size_t moe_w4_bytes(int fmt, int N, int K, int group);
 int moe_w4_pack(int fmt, const uint8_t* codes, const void* scales, const uint8_t* zeros, int N, int K, int group,

@@ -259,6 +259,8 @@ int moe_layer_decode(int wdt, const void* slot_pool, size_t slot_stride, const i
     return fail(MOE_EUNSUPPORTED, "moe_layer_decode: experts of 2 GiB or more");
   if (H > moe::kDecodeLayerMaxH)
     return fail(MOE_EUNSUPPORTED, "moe_layer_decode: H=%d beyond %d", H, moe::kDecodeLayerMaxH);
+  if (decode_plan_offset(T, k, I, I_shared, wdt) >= (size_t)1 << 31)
+    return fail(MOE_EUNSUPPORTED, "moe_layer_decode: an intermediate of 2 GiB or more");
   const size_t plan_at = decode_plan_offset(T, k, I, I_shared, wdt);
   const size_t need = plan_at + moe::decode_layer_plan_bytes();
   if (ws_bytes < need) return fail(MOE_ECAPACITY, "workspace %zu bytes < %zu needed", ws_bytes, need);
@@ -290,8 +292,8 @@ namespace {
 
 int check_w4(int fmt, int N, int K, int group, const char* what) {
   if (fmt != MOE_MXFP4 && fmt != MOE_INT4) return fail(MOE_EINVAL, "%s: unknown 4-bit format %d", what, fmt);
-  if (N < 1 || K < 32 || K % 32 || K > 1 << 20 || (int64_t)N * K >= (int64_t)1 << 40)
-    return fail(MOE_EINVAL, "%s: N=%d must be >= 1, K=%d a multiple of 32 up to 2^20, N*K < 2^40", what, N, K);
+  if (N < 1 || N > 1 << 30 || K < 32 || K % 32 || K > 1 << 20 || (int64_t)N * K >= (int64_t)1 << 40)
+    return fail(MOE_EINVAL, "%s: N=%d must be in [1, 2^30], K=%d a multiple of 32 up to 2^20, N*K < 2^40", what, N, K);
   if (fmt == MOE_MXFP4 ? group != 32 : (group != 32 && group != 64 && group != 128))
     return fail(MOE_EINVAL, "%s: group=%d (MXFP4: 32; INT4: 32, 64 or 128)", what, group);
   return MOE_OK;
@@ -320,7 +322,7 @@ int moe_w4_linear(int fmt, const void* w, int N, int K, int group, const void* x
                   const float* bias, void* y, int64_t y_ld, int ydt, hipStream_t stream) {
   const CallRange range_(__func__);
   if (int rc = check_w4(fmt, N, K, group, "moe_w4_linear")) return rc;
-  REQUIRE(T >= 0 && T <= 1 << 20, "moe_w4_linear: T=%d must be in [0, 2^20]", T);
+  REQUIRE(T >= 0 && T <= 1 << 19, "moe_w4_linear: T=%d must be in [0, 2^19]", T);
   REQUIRE(ydt == MOE_F32 || ydt == MOE_BF16, "moe_w4_linear: ydt must be MOE_F32 or MOE_BF16");
   REQUIRE(x_ld >= K && x_ld % 8 == 0 && x_ld <= 1 << 22, "moe_w4_linear: x_ld=%lld (>= K, a multiple of 8, <= 2^22)",
           (long long)x_ld);

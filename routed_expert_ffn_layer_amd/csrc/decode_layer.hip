@@ -28,7 +28,9 @@ constexpr int kDlWaves = 16;  // waves of a block, one block per CU
 constexpr int kDlThreads = 64 * kDlWaves;
 constexpr int kDlTeams = 4;  // gate/up: teams of a block, a tile each
 constexpr int kDlHalfTiles = 128;  // row tiles of W2 up to which the down kernel's blocks own half a tile
-constexpr int kDlOneQuadT = 8;  // batches whose down runs hold up to 4 pairs, larger ones up to 8
+// Batches whose down runs hold up to 4 pairs; larger ones up to 8 (MXFP4, 4 or 8 pairs: 8 tokens
+// 66.8 and 67.4 us, 64 tokens 177 and 169).
+constexpr int kDlOneQuadT = 8;
 
 // A run: pairs of one expert (or tokens of the shared expert) that one matrix tile serves.
 struct __align__(16) DlRun {
@@ -57,8 +59,8 @@ struct __align__(16) DlPlan {
   uint16_t sorted[kDlMaxPairs];  // by position: the pair
 };
 
-// Largest of v over the wave, in a scalar register: five in-register steps (shifts
-// by 1, 2, 4, 8 inside a row of 16 lanes, then two broadcasts of a row's last lane).
+// Largest of v over the wave, in a scalar register, by six in-register steps (shifts by 1, 2,
+// 4, 8 inside a row of 16 lanes, then two broadcasts of a row's last lane).
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 #define MOE_DPP_MAX(ctrl, rows) \
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false))
@@ -190,13 +192,14 @@ __device__ __forceinline__ void dl_route(DlPlan& s, float* w, const DecodeLayerA
 }
 
 // Groups the pairs by expert, in ascending token order, and cuts every expert's pairs into
-// runs of up to P (and, for the second kernel, of up to P2 into `out`, where given).  Each expert has a bit mask of the tokens that chose it: its count is
-// the mask's population, a pair's place in its group the population below its token, and
-// one scan over the experts (thread e holds expert e) places groups and runs.  Given
-// routing may name an expert twice in one token, which a mask cannot hold: then every
-// pair counts the pairs before it of the same expert instead (n compares each).  Up to 64
-// pairs take one wave and one barrier instead (four: 1.6 us of a 21 us layer at one token).
-// slots: the slot table; mask: E 64-bit words; part: 2 * kDlWaves words (all LDS).
+// runs of up to P (and, for the second kernel, of up to P2 into `out`, where given).  Each
+// expert has a bit mask of the tokens that chose it: its count is the mask's population, a
+// pair's place in its group the population below its token, and one scan over the experts
+// (thread e holds expert e) places groups and runs.  Given routing may name an expert twice
+// in one token, which a mask cannot hold: then every pair counts the pairs before it of the
+// same expert instead (n compares each).  Up to 64 pairs take one wave and one barrier
+// instead (four barriers: 1.6 us of a 21 us layer at one token).
+// slots: the slot table; mask: E 64-bit words; part: kDlWaves words (all LDS).
 // Returns the number of runs, the shared expert's included (the same in every thread); ends
 // with a barrier.
 static_assert(kDlThreads >= 1024 && kDlMaxPairs <= kDlThreads && kDecodeLayerMaxT <= 64, "thread e holds expert e");
@@ -365,7 +368,8 @@ struct GuTune {
 // ranks, and the token rows.
 constexpr int kDlRouting = (1024 + kDlMaxPairs + kDlWaves) * 4;
 static int gu_row_bytes(int wtype, int H) { return (wtype == W_MXFP4 ? (H + 127) / 128 * 128 : H) * 2 + 16; }
-static constexpr size_t kGuLds = 160 * 1024;
+static constexpr size_t kGuLds = 159 * 1024;  // of 160 KB: the workgroup vote takes a few bytes
+static_assert(sizeof(DlPlan) + 2 * kDlWaves * 256 + kDlRouting + kDecodeLayerMaxH * 2 + 16 <= kGuLds, "one token row fits");
 static size_t gu_red_bytes(int P) { return (size_t)2 * kDlWaves * 256 * ((P + 3) / 4); }
 
 // Byte offsets and size of one expert's matrices (the slot layout of include/moe.h).
@@ -578,7 +582,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
 //
 // The vector memory pipe, not HBM, is what a 4-bit stream runs into here (an h fragment
 // for every 256 bytes of codes: with four fragment loads and a scale load beside each code
-// load the MXFP4 kernel took 86 us at 64 tokens, 28 us of them its codes).  Runs are
+// load the MXFP4 kernel took 86 us at 64 tokens, without them 28; now 62).  Runs are
 // therefore short, 4 VN tokens, and a load brings four fragments: lane j of a quad, where all
 // four would hold the same token, loads its fragment j, so that a load reads whole 64-byte
 // pieces (256 consecutive bytes of each of 4 tokens for MXFP4).  Such an operand goes into the
@@ -588,8 +592,9 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
 // ---------------------------------------------------------------------------
 //
 // HALF: a block owns 8 columns of y, half a row tile (H / 8 blocks where H / 16 would leave
-// CUs idle; bf16 layer of 16 tokens at H = 2048: 139 -> DOWN_HALF us).  One 1 KB load then
-// holds the 8 rows at two steps, rows at the even step as operand columns 0-7 and at the odd
+// CUs idle, as long as the half tiles are one round of blocks: bf16 layer of 16 tokens at
+// H = 2048 140 -> 130 us, but MXFP4 layer of 53 tokens at H = 2592 55 -> 70 us).  One 1 KB load
+// then holds the 8 rows at two steps, rows at the even step as operand columns 0-7 and at the odd
 // one as columns 8-15, and the quads of lanes hold two tokens at both steps: rows 4 i and
 // 4 i + 1 of the result are right in columns 0-7, rows 4 i + 2 and 4 i + 3 in columns 8-15
 // (the other products mean nothing), and the two halves add up.  An h load serves half as

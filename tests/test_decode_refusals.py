@@ -31,6 +31,7 @@ def _layer(**kw):
     (dict(nws=4 * 2 * 32 * 2 + 13327), moe.MOE_ECAPACITY),
     (dict(shared=P, ish=64, nws=12 * 64 * 2 + 13327), moe.MOE_ECAPACITY),
     (dict(H=65568, stride=1 << 24), moe.MOE_EUNSUPPORTED),
+    (dict(T=64, k=8, H=32, I=1 << 21, stride=1 << 30, nws=1 << 40), moe.MOE_EUNSUPPORTED),  # 512 rows of 4 MiB
     (dict(wdt=moe.MOE_BF16, H=32768, I=16384, stride=1 << 40, nws=1 << 30), moe.MOE_EUNSUPPORTED),  # experts of 3 GiB
 ] + [({n: v}, moe.MOE_EINVAL) for n in ("pool", "slots", "x", "ids", "w", "y", "ws") for v in (None, BAD)]
   + [(dict(logits=BAD), moe.MOE_EINVAL)])
@@ -61,13 +62,13 @@ def _linear(**kw):
                                    a["y"], a["y_ld"], a["ydt"], None)
 
 
-SHAPES = [dict(fmt=1), dict(fmt=3), dict(N=0), dict(N=-5), dict(K=0), dict(K=48), dict(K=-32), dict(K=(1 << 20) + 32, x_ld=1 << 22),
+SHAPES = [dict(fmt=1), dict(fmt=3), dict(N=0), dict(N=-5), dict(N=(1 << 30) + 1, K=32, x_ld=32, y_ld=1 << 31), dict(K=0), dict(K=48), dict(K=-32), dict(K=(1 << 20) + 32, x_ld=1 << 22),
           dict(group=16), dict(group=256), dict(group=0), dict(fmt=moe.MOE_MXFP4, group=64),
           dict(N=1 << 30, K=1 << 20, x_ld=1 << 20, y_ld=1 << 30)]
 
 
 @pytest.mark.parametrize("kw", SHAPES + [
-    dict(T=-1), dict(T=(1 << 20) + 1), dict(ydt=2), dict(ydt=-1), dict(x_ld=248), dict(x_ld=260), dict(x_ld=(1 << 22) + 8),
+    dict(T=-1), dict(T=(1 << 19) + 1), dict(ydt=2), dict(ydt=-1), dict(x_ld=248), dict(x_ld=260), dict(x_ld=(1 << 22) + 8),
     dict(y_ld=39), dict(w=None), dict(w=BAD), dict(x=None), dict(x=BAD), dict(y=None), dict(y=BAD), dict(bias=BAD)])
 def test_linear_refusals(kw):
     assert _linear(**kw) == moe.MOE_EINVAL
