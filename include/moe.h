@@ -369,9 +369,10 @@ int moe_combine(const float* out_rows, const float* topk_w, const int32_t* inv_r
  * layer, "The gap it targets"; at that size the launches and round trips between
  * the layer's steps cost as much as the weights).
  *     y[t] = sum_j topk_w[t][j] * FFN_e(x[t]),  e = topk_ids[t][j]  (+ FFN_shared(x[t]))
- * with FFN, weight layouts and roundings of moe_grouped_ffn and the order of sums of
- * moe_combine; the K order inside a product differs from moe_grouped_ffn's, so the two
- * agree within rounding, not bit for bit.
+ * with FFN and weight layouts of moe_grouped_ffn and the order of sums of moe_combine.
+ * Up to 8 tokens the SwiGLU intermediate keeps 16 significant bits (a bf16 and a bf16
+ * remainder), above it is rounded to bf16 as in moe_grouped_ffn; the K order inside a
+ * product differs from moe_grouped_ffn's, so the two agree within rounding, not bit for bit.
  *   logits    [T][E] f32: routed as moe_route_topk does, topk_ids and topk_w [T][k] are
  *             written; NULL: topk_ids and topk_w are read as given (routing of the
  *             caller's own, or of an earlier moe_route)

@@ -207,7 +207,7 @@ int decode_h_ld(int I, int I_shared, int wdt) {
 
 size_t decode_plan_offset(int T, int k, int I, int I_shared, int wdt) {
   const size_t rows = (size_t)T * k + (I_shared > 0 ? T : 0);
-  return (rows * decode_h_ld(I, I_shared, wdt) * 2 + 255) / 256 * 256;
+  return (rows * decode_h_ld(I, I_shared, wdt) * 4 + 255) / 256 * 256;  // two bf16 rows each
 }
 
 }  // namespace

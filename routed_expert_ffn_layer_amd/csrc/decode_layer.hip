@@ -2,7 +2,7 @@
 // gate/up products, and the down products with the weighted sum.
 //
 //   ids, w = top-k of the logits and their softmax (or given by the caller)
-//   h[p]   = SiLU(Wgate[e] x[t]) * (Wup[e] x[t])          p = t*k + j, e = ids[p]
+//   h[p]   = SiLU(Wgate[e] x[t]) * (Wup[e] x[t])          p = t*k + j, e = ids[p]; bf16, or two of them
 //   y[t]   = sum_j w[p] * (W2[e] h[p])  (+ the shared expert)
 //
 // What bounds it: the active experts' weights are read once (HBM) and, for one token,
@@ -28,9 +28,13 @@ constexpr int kDlWaves = 16;  // waves of a block, one block per CU
 constexpr int kDlThreads = 64 * kDlWaves;
 constexpr int kDlTeams = 4;  // gate/up: teams of a block, a tile each
 constexpr int kDlHalfTiles = 128;  // row tiles of W2 up to which the down kernel's blocks own half a tile
-// Batches whose down runs hold up to 4 pairs; larger ones up to 8 (MXFP4, 4 or 8 pairs: 8 tokens
-// 66.8 and 67.4 us, 64 tokens 177 and 169).
-constexpr int kDlOneQuadT = 8;
+// Up to this many tokens h is kept as two bf16, h and the remainder of its rounding (16
+// significant bits), larger batches round it to bf16.  One rounding of h costs y as much
+// as y's own rounding to bf16 (an RMS error of 0.0024 instead of 0.0017); the remainder rides in
+// operand rows that a few tokens leave empty, but doubles the h loads that bound the down
+// products of many (MXFP4, h in one and in two parts: 28.2 and 28.9 us a layer at one token,
+// 65 and 70 at 8).
+constexpr int kDlSplitT = 8;
 
 // A run: pairs of one expert (or tokens of the shared expert) that one matrix tile serves.
 struct __align__(16) DlRun {
@@ -395,7 +399,7 @@ static_assert(GuTune<W_MXFP4>::units % 2 == 0, "scale words serve pairs of steps
 
 // resident: all T token rows fit the LDS rows and are copied there once, beside the top-k.
 template <int WT>
-__global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, int P, int P2, int row_bytes, bool resident) {
+__global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, int P, int P2, int row_bytes, bool resident, bool split) {
   constexpr int U = GuTune<WT>::units, B = GuTune<WT>::bufs;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   DlPlan& s = *reinterpret_cast<DlPlan*>(lds);
@@ -556,10 +560,19 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
         const int i = g + 4 * v;
         if (i < m && (lane & 8) == 0 && tl < per) {
           const int row = run < sh_runs ? n + at + i : s.sorted[at + i];
-          uint16_t* h = a.h + (size_t)row * a.h_ld;
-          h[tl * 8 + (lane & 7)] = f32_to_bf16_rne(silu_f32(sum) * up);
+          uint16_t* h = a.h + (size_t)row * (a.h_ld << split) + (lane & 7);
+          const float hv = silu_f32(sum) * up;
+          const uint16_t hi = f32_to_bf16_rne(hv);
+          h[tl * 8] = hi;
+          if (split) {  // an infinite or NaN h has no remainder
+            const float rest = hv - bf16_bits_to_f32(hi);
+            h[a.h_ld + tl * 8] = fabsf(rest) < INFINITY ? f32_to_bf16_rne(rest) : 0;
+          }
           if (WT == W_MXFP4 && tl + 1 == per)  // zeros up to the next whole column step
-            for (int z = per * 8; z % 128; z += 8) h[z + (lane & 7)] = 0;
+            for (int z = per * 8; z % 128; z += 8) {
+              h[z] = 0;
+              if (split) h[a.h_ld + z] = 0;
+            }
         }
       }
       half ^= 1;
@@ -583,44 +596,44 @@ __global__ __launch_bounds__(kDlThreads) void decode_gate_up(DecodeLayerArgs a, 
 // The vector memory pipe, not HBM, is what a 4-bit stream runs into here (an h fragment
 // for every 256 bytes of codes: with four fragment loads and a scale load beside each code
 // load the MXFP4 kernel took 86 us at 64 tokens, without them 28; now 62).  Runs are
-// therefore short, 4 VN tokens, and a load brings four fragments: lane j of a quad, where all
-// four would hold the same token, loads its fragment j, so that a load reads whole 64-byte
-// pieces (256 consecutive bytes of each of 4 tokens for MXFP4).  Such an operand goes into the
-// products of all its fragments' weights as it is: of row 4 i + j of a product only
-// fragment j means something, so fragment f adds up in an accumulator of its own, whose
-// element f is the token's sum.
-// ---------------------------------------------------------------------------
+// therefore short, and a load brings four fragments of 4 rows of h: lane j of a quad, where all
+// four would hold the same row, loads its fragment j, so that a load reads whole 64-byte
+// pieces (256 consecutive bytes of a row for MXFP4).  Such an operand goes into the products
+// of all its fragments' weights as it is: of row 4 i + j of a product only fragment j means
+// something, so fragment f adds up in an accumulator of its own, whose element f is the
+// row's sum.  A run has 8 rows: 8 tokens, or (SPLIT) 4 tokens and the remainders of their h,
+// which add to the same accumulators.
 //
 // HALF: a block owns 8 columns of y, half a row tile (H / 8 blocks where H / 16 would leave
 // CUs idle, as long as the half tiles are one round of blocks: bf16 layer of 16 tokens at
 // H = 2048 140 -> 130 us, but MXFP4 layer of 53 tokens at H = 2592 55 -> 70 us).  One 1 KB load
 // then holds the 8 rows at two steps, rows at the even step as operand columns 0-7 and at the odd
-// one as columns 8-15, and the quads of lanes hold two tokens at both steps: rows 4 i and
+// one as columns 8-15, and the quads of lanes hold two rows of h at both steps: rows 4 i and
 // 4 i + 1 of the result are right in columns 0-7, rows 4 i + 2 and 4 i + 3 in columns 8-15
 // (the other products mean nothing), and the two halves add up.  An h load serves half as
 // many weights, so this is for blocks that would be too few otherwise.
-template <int WT, int VN, bool HALF>
+template <int WT, bool HALF, bool SPLIT>
 struct DnTune {
   static constexpr int units = WT == W_BF16 ? 4 : 2;                // steps of a chunk
   static constexpr int wloads = HALF ? units / 2 : units;           // code loads of a chunk
   static constexpr int groups = HALF || WT == W_BF16 ? 1 : 2;       // groups of h loads
-  static constexpr int hloads = HALF && WT == W_MXFP4 ? 4 : VN;     // h loads of a group
-  static constexpr int bufs = VN == 1 ? 4 : HALF || WT == W_BF16 ? 3 : 2;
+  static constexpr int hloads = HALF && WT == W_MXFP4 ? 4 : 2;      // h loads of a group
+  static constexpr int bufs = HALF || SPLIT || WT == W_BF16 ? 3 : 2;  // what the registers of 16 waves hold
 };
 
-template <int WT, int VN, bool HALF>
+template <int WT, bool HALF, bool SPLIT>
 struct DnBuf {
-  using Tune = DnTune<WT, VN, HALF>;
+  using Tune = DnTune<WT, HALF, SPLIT>;
   u32x4 w[Tune::wloads], h[Tune::groups][Tune::hloads];
   uint32_t sc;
 };
 
-template <int WT, int VN, bool HALF, bool BF16OUT>
+template <int WT, bool HALF, bool SPLIT, bool BF16OUT>
 __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int log_parts) {
-  using Tune = DnTune<WT, VN, HALF>;
-  constexpr int U = Tune::units, NG = Tune::groups, NH = Tune::hloads, B = Tune::bufs, P = 4 * VN;
-  constexpr int COLS = HALF ? 8 : 16, NA = HALF ? 1 : 4, NR = HALF ? 1 : VN;  // columns of y; accumulators; quads' tokens
-  static_assert(!HALF || VN == 2, "half tiles hold two tokens a quad");
+  using Tune = DnTune<WT, HALF, SPLIT>;
+  constexpr int U = Tune::units, NG = Tune::groups, NH = Tune::hloads, B = Tune::bufs, P = SPLIT ? 4 : 8;
+  constexpr int COLS = HALF ? 8 : 16, NA = HALF ? 1 : 4;           // columns of y; fragments' accumulators
+  constexpr int NR = HALF ? 1 : 2, NS = HALF || SPLIT ? 1 : 2;     // rows a lane reads; sets of accumulators
   __shared__ DlShared s;
   __shared__ float w[kDlMaxPairs];
   extern __shared__ float val[];  // [part][pair, then shared token][COLS]
@@ -643,7 +656,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
     }
   }
   __syncthreads();
-  const int hbytes = nrows * a.h_ld * 2;
+  const int h_row = (a.h_ld << SPLIT) * 2, hbytes = nrows * h_row;
   const ExpertShape<WT> rt(a.H, a.I), sh(a.H, a.I_shared);
   const int parts = 1 << log_parts, part = wv & (parts - 1), stride = kDlWaves >> log_parts;
   // a part is whole chunks of U steps
@@ -674,11 +687,13 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
     part_steps(nk, is, ie);
     #pragma unroll
     for (int l = 0; l < NR; ++l) {
-      const int i = min((c >> 2) + 4 * (HALF ? j & 1 : l), r.m - 1);
-      i_row[l] = (shared ? n + r.at + i : s.sorted[r.at + i]) * a.h_ld * 2 + (WT == W_MXFP4 ? 64 : 16) * g;
+      // tokens 0-3, and tokens 4-7 (SPLIT: the remainders of the first)
+      const int second = HALF ? j & 1 : l, i = min((c >> 2) + (SPLIT ? 0 : 4 * second), r.m - 1);
+      i_row[l] = (shared ? n + r.at + i : s.sorted[r.at + i]) * h_row + (SPLIT ? second * a.h_ld * 2 : 0) +
+                 (WT == W_MXFP4 ? 64 : 16) * g;
     }
   };
-  auto issue = [&](DnBuf<WT, VN, HALF>& b) {
+  auto issue = [&](DnBuf<WT, HALF, SPLIT>& b) {
 #pragma unroll
     for (int u = 0; u < U; u += HALF ? 2 : 1) {
       const int step = is + u;
@@ -699,7 +714,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
         for (int f = 0; f < 4; ++f)
           b.h[0][f] = bld16(hbuf, pair || h_step == 0 ? i_row[0] + 256 * h_step + 16 * f : kPastEnd, hs);
       } else if (u < NG) {
-        // load l: tokens 4 l .. 4 l + 3, fragment j (bf16: 64 bytes a step; MXFP4: 16 bytes)
+        // fragment j (bf16: 64 bytes a step; MXFP4: 16 bytes)
 #pragma unroll
         for (int l = 0; l < NH; ++l) b.h[u][l] = bld16(hbuf, i_row[l] + (WT == W_MXFP4 ? 16 : 64) * j, hs);
       }
@@ -715,15 +730,15 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
       m = r.m;
       part_steps(cr < sh_runs ? sh.n2 : rt.n2, cs, ce);
     };
-    DnBuf<WT, VN, HALF> buf[B];
+    DnBuf<WT, HALF, SPLIT> buf[B];
     issue_run();
 #pragma unroll
     for (int b = 0; b < B; ++b) issue(buf[b]);
     enter_run();
-    f32x4 acc[NR][NA];
+    f32x4 acc[NS][NA];
     auto clear = [&]() {
 #pragma unroll
-      for (int l = 0; l < NR; ++l)
+      for (int l = 0; l < NS; ++l)
 #pragma unroll
         for (int f = 0; f < NA; ++f) acc[l][f] = f32x4{0.f, 0.f, 0.f, 0.f};
     };
@@ -731,7 +746,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
     for (bool more = true; more;) {
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const DnBuf<WT, VN, HALF>& k = buf[b];
+        const DnBuf<WT, HALF, SPLIT>& k = buf[b];
         if constexpr (HALF && WT == W_BF16) {
           acc[0][0] = mfma16(k.h[0][0], as_bf16x8(k.w[0]), acc[0][0]);
           if (cs + 2 < ce) acc[0][0] = mfma16(k.h[0][1], as_bf16x8(k.w[1]), acc[0][0]);
@@ -744,7 +759,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
           for (int f = 0; f < 4; ++f)
             if (f == 0 || cs + f < ce)
 #pragma unroll
-              for (int l = 0; l < NR; ++l) acc[l][f] = mfma16(k.h[0][l], as_bf16x8(k.w[f]), acc[l][f]);
+              for (int l = 0; l < NR; ++l) acc[l % NS][f] = mfma16(k.h[0][l], as_bf16x8(k.w[f]), acc[l % NS][f]);
         } else {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
@@ -754,7 +769,7 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
               for (int f = 0; f < 4; ++f) {
                 const bf16x8 wf = fp4x8_to_bf16x8(k.w[u][f], sc);
 #pragma unroll
-                for (int l = 0; l < NR; ++l) acc[l][f] = mfma16(k.h[u][l], wf, acc[l][f]);
+                for (int l = 0; l < NR; ++l) acc[l % NS][f] = mfma16(k.h[u][l], wf, acc[l % NS][f]);
               }
             }
           }
@@ -763,15 +778,16 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
         cs += U;
         if (cs < ce) continue;
 #pragma unroll
-        for (int v = 0; v < VN; ++v) {
+        for (int v = 0; v < (SPLIT ? 1 : 2); ++v) {
           float d;
           if constexpr (HALF) {
             d = c < 8 ? acc[0][0][v] : acc[0][0][v + 2];
+            if constexpr (SPLIT) d += c < 8 ? acc[0][0][1] : acc[0][0][3];
             d += __shfl_xor(d, 8, 64);
           } else {
-            d = acc[v][0][0];
+            d = acc[v % NS][0][0];
 #pragma unroll
-            for (int f = 1; f < NA; ++f) d += acc[v][f][f];
+            for (int f = 1; f < NA; ++f) d += acc[v % NS][f][f];
           }
           const int i = g + 4 * v;
           if (i < m && c < COLS) {
@@ -824,13 +840,13 @@ __global__ __launch_bounds__(kDlThreads) void decode_down(DecodeLayerArgs a, int
   }
 }
 
-template <int WT, int VN, bool HALF>
+template <int WT, bool HALF, bool SPLIT>
 static hipError_t launch_down(const DecodeLayerArgs& a, bool bf16_out, hipStream_t st) {
   // K parts of the down product: enough (run, part) tasks for the waves when every pair is
   // a run of its own, each part at least one chunk of steps long, and LDS for the parts
   constexpr int COLS = HALF ? 8 : 16;
   const int nrows = a.T * a.k + (a.shared_w ? a.T : 0);
-  const int ks = (WT == W_MXFP4 ? 128 : 32) * DnTune<WT, VN, HALF>::units;
+  const int ks = (WT == W_MXFP4 ? 128 : 32) * DnTune<WT, HALF, SPLIT>::units;
   int chunks = (a.I + ks - 1) / ks;
   if (a.shared_w && (a.I_shared + ks - 1) / ks < chunks) chunks = (a.I_shared + ks - 1) / ks;
   int lp = 0;
@@ -838,9 +854,9 @@ static hipError_t launch_down(const DecodeLayerArgs& a, bool bf16_out, hipStream
   const size_t lds = (size_t)(nrows << lp) * COLS * 4;
   const dim3 grid(a.H / COLS), block(kDlThreads);
   if (bf16_out)
-    hipLaunchKernelGGL((decode_down<WT, VN, HALF, true>), grid, block, lds, st, a, lp);
+    hipLaunchKernelGGL((decode_down<WT, HALF, SPLIT, true>), grid, block, lds, st, a, lp);
   else
-    hipLaunchKernelGGL((decode_down<WT, VN, HALF, false>), grid, block, lds, st, a, lp);
+    hipLaunchKernelGGL((decode_down<WT, HALF, SPLIT, false>), grid, block, lds, st, a, lp);
   return hipGetLastError();
 }
 
@@ -857,12 +873,12 @@ static hipError_t launch_t(const DecodeLayerArgs& a, bool bf16_out, hipStream_t 
   const int64_t bound = (a.shared_w ? (a.T + P - 1) / P * sh_turns : 0) + n * rt_turns;  // every pair a run
   const unsigned grid = (unsigned)(bound < 256 ? bound : 256);
   const bool half = a.H / 16 <= kDlHalfTiles;
-  const int vn = a.T <= kDlOneQuadT && !half ? 1 : 2;
-  hipLaunchKernelGGL(decode_gate_up<WT>, dim3(grid), dim3(kDlThreads), lds, st, a, P, 4 * vn, rb, resident);
+  const bool split = a.T <= kDlSplitT;
+  hipLaunchKernelGGL(decode_gate_up<WT>, dim3(grid), dim3(kDlThreads), lds, st, a, P, split ? 4 : 8, rb, resident, split);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (half) return launch_down<WT, 2, true>(a, bf16_out, st);
-  return vn == 1 ? launch_down<WT, 1, false>(a, bf16_out, st) : launch_down<WT, 2, false>(a, bf16_out, st);
+  if (half) return split ? launch_down<WT, true, true>(a, bf16_out, st) : launch_down<WT, true, false>(a, bf16_out, st);
+  return split ? launch_down<WT, false, true>(a, bf16_out, st) : launch_down<WT, false, false>(a, bf16_out, st);
 }
 
 hipError_t launch_decode_layer(int wtype, const DecodeLayerArgs& a, bool bf16_out, hipStream_t st) {

@@ -69,7 +69,7 @@ struct DecodeLayerArgs {
   const float* logits;            // [T][E], or null: ids and w are given
   int32_t* ids;                   // [T][k]
   float* w;                       // [T][k]
-  uint16_t* h;                    // workspace: [T*k + T][h_ld] bf16
+  uint16_t* h;                    // workspace: [T*k + T][2][h_ld] bf16 (h and the remainder of its rounding)
   void* plan;                     // workspace: decode_layer_plan_bytes()
   void* y;                        // [T][H]
   int T, k, E, H, I, I_shared, h_ld;

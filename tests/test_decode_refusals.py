@@ -28,10 +28,10 @@ def _layer(**kw):
     (dict(T=65, k=1), moe.MOE_EUNSUPPORTED), (dict(T=64, k=9, E=16), moe.MOE_EUNSUPPORTED),
     (dict(ydt=2), moe.MOE_EINVAL), (dict(stride=EB - 16), moe.MOE_EINVAL), (dict(stride=EB + 8), moe.MOE_EINVAL),
     (dict(shared=P, ish=16), moe.MOE_EINVAL), (dict(shared=P, ish=0), moe.MOE_EINVAL), (dict(shared=BAD, ish=32), moe.MOE_EINVAL),
-    (dict(nws=4 * 2 * 32 * 2 + 13327), moe.MOE_ECAPACITY),
-    (dict(shared=P, ish=64, nws=12 * 64 * 2 + 13327), moe.MOE_ECAPACITY),
+    (dict(nws=4 * 2 * 32 * 4 + 13327), moe.MOE_ECAPACITY),
+    (dict(shared=P, ish=64, nws=12 * 64 * 4 + 13327), moe.MOE_ECAPACITY),
     (dict(H=65568, stride=1 << 24), moe.MOE_EUNSUPPORTED),
-    (dict(T=64, k=8, H=32, I=1 << 21, stride=1 << 30, nws=1 << 40), moe.MOE_EUNSUPPORTED),  # 512 rows of 4 MiB
+    (dict(T=64, k=8, H=32, I=1 << 20, stride=1 << 30, nws=1 << 40), moe.MOE_EUNSUPPORTED),  # 512 rows of 4 MiB
     (dict(wdt=moe.MOE_BF16, H=32768, I=16384, stride=1 << 40, nws=1 << 30), moe.MOE_EUNSUPPORTED),  # experts of 3 GiB
 ] + [({n: v}, moe.MOE_EINVAL) for n in ("pool", "slots", "x", "ids", "w", "y", "ws") for v in (None, BAD)]
   + [(dict(logits=BAD), moe.MOE_EINVAL)])
@@ -46,11 +46,11 @@ def test_layer_without_tokens_needs_no_buffers():
 
 def test_layer_workspace():
     ws = moe.moe_layer_decode_workspace
-    # the intermediate in whole 256 bytes, then the routing: 16 bytes, 16 per run, two integers per pair
+    # two bf16 per element of the intermediate, in whole 256 bytes, then the routing: 16 bytes, 16 per run, two integers per pair
     plan = 16 + 16 * (moe.MOE_LAYER_DECODE_MAX_PAIRS + 64) + 2 * 4 * moe.MOE_LAYER_DECODE_MAX_PAIRS
-    assert ws(4, 2, 8, 64, 32, 0, moe.MOE_BF16) == 4 * 2 * 32 * 2 + plan
-    assert ws(4, 2, 8, 64, 32, 64, moe.MOE_BF16) == (8 + 4) * 64 * 2 + plan
-    assert ws(4, 2, 8, 64, 32, 64, moe.MOE_MXFP4) == (8 + 4) * 128 * 2 + plan  # rows of whole 128 columns
+    assert ws(4, 2, 8, 64, 32, 0, moe.MOE_BF16) == 4 * 2 * 32 * 4 + plan
+    assert ws(4, 2, 8, 64, 32, 64, moe.MOE_BF16) == (8 + 4) * 64 * 4 + plan
+    assert ws(4, 2, 8, 64, 32, 64, moe.MOE_MXFP4) == (8 + 4) * 128 * 4 + plan  # rows of whole 128 columns
     assert ws(1, 1, 8, 64, 32, 0, moe.MOE_BF16) == 256 + plan
     assert ws(4, 2, 8, 64, 32, 0, moe.MOE_F32) == 0 and ws(-1, 2, 8, 64, 32, 0, moe.MOE_BF16) == 0
 

@@ -7,9 +7,9 @@ exact products of bf16 operands, a K-term sum in f32 in any order is off by at m
 instruction's internal sum need not round to nearest).  So, with |W||x| the sums of
 magnitudes,
     dg <= 2 (H + 64) u |Wg||x|,  du <= 2 (H + 64) u |Wu||x|
-    dh <= 1.1 dg |up| + |silu| du + |h| (2^-8 + (8 + |g|) 2^-23)
-(|silu'| <= 1.1; the intermediate is rounded to bf16, half a step 2^-8 relative; the
-hardware exponential and reciprocal), and through the down product and the weights
+    dh <= 1.1 dg |up| + |silu| du + |h| (2^-8 or 2^-16 + (8 + |g|) 2^-23)
+(|silu'| <= 1.1; the intermediate is rounded to bf16, half a step 2^-8 relative, or up to 8
+tokens to two bf16, 2^-16; the hardware exponential and reciprocal), and through the down product and the weights
     dy <= sum_j w_j ( |W2| dh + 2 (I + 64) u |W2||h| ) + (2^-18 + (k + 2) u) sum_j w_j |row_j|
 (gate weights good to 2e-6 < 2^-18).  Second order terms are covered by a factor 1.02; a
 bf16 output adds 2^-8 |y| (1.02 of it as well).
@@ -31,30 +31,31 @@ def _silu(z):
     return z / (1.0 + np.exp(-z))
 
 
-def _expert_rows(ora, dtype, slot, H, I, x):
+def _expert_rows(ora, dtype, slot, H, I, x, half_step):
     """Rows FFN(x) [n][H] and their error bound."""
     wg, wu, wd = ora.decode_expert(dtype, slot, H, I)
     g, u = x @ wg.T, x @ wu.T
     dg, du = (2 * (H + 64) * U * (np.abs(x) @ np.abs(w).T) for w in (wg, wu))
     h = _silu(g) * u
-    dh = 1.1 * dg * np.abs(u) + np.abs(_silu(g)) * du + np.abs(h) * (2.0 ** -8 + (8 + np.abs(g)) * 2.0 ** -23)
+    dh = 1.1 * dg * np.abs(u) + np.abs(_silu(g)) * du + np.abs(h) * (half_step + (8 + np.abs(g)) * 2.0 ** -23)
     return h @ wd.T, (dh + 2 * (I + 64) * U * np.abs(h)) @ np.abs(wd).T
 
 
 def _reference(ora, lay, ids, w, have=None):
     """y [T][H] and its bound for the routing ids, w (pairs outside `have` left out)."""
     dtype, T, H, I, E, k = (lay[n] for n in ("dtype", "T", "H", "I", "E", "k"))
+    half_step = 2.0 ** -16 if T <= 8 else 2.0 ** -8
     x = ora.decode_x(dtype, lay["x"], T, H)
     y, b = np.zeros((T, H)), np.zeros((T, H))
     for e in np.unique(ids):
         if e < 0 or e >= E or (have is not None and not have[e]):
             continue
         for t, j in zip(*np.nonzero(ids == e)):
-            row, d = _expert_rows(ora, dtype, lay["experts"][e], H, I, x[t:t + 1])
+            row, d = _expert_rows(ora, dtype, lay["experts"][e], H, I, x[t:t + 1], half_step)
             y[t] += w[t, j] * row[0]
             b[t] += np.abs(w[t, j]) * (d[0] + (2.0 ** -18 + (k + 2) * U) * np.abs(row[0]))
     if lay["shared"] is not None:
-        row, d = _expert_rows(ora, dtype, lay["shared"], H, lay["I_shared"], x)
+        row, d = _expert_rows(ora, dtype, lay["shared"], H, lay["I_shared"], x, half_step)
         y += row
         b += d + (k + 2) * U * np.abs(row)
     return y, 1.02 * b
