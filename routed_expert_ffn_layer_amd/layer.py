@@ -26,8 +26,9 @@ class LayerBuffers:
         self.inv_rows = torch.empty(n, dtype=i32, device=dev)
         self.out_rows = torch.empty((n, H), dtype=f32, device=dev)
         self.shared_out = torch.empty((max(T, 1), H), dtype=f32, device=dev) if I_shared else None
-        ws = max(moe.moe_grouped_ffn_workspace(T, k, E, H, I, I_shared, wdt),
-                 moe.moe_layer_decode_workspace(T, k, E, H, I, I_shared, wdt))
+        ws = moe.moe_grouped_ffn_workspace(T, k, E, H, I, I_shared, wdt)
+        if T <= moe.MOE_LAYER_DECODE_MAX_T and T * k <= moe.MOE_LAYER_DECODE_MAX_PAIRS:
+            ws = max(ws, moe.moe_layer_decode_workspace(T, k, E, H, I, I_shared, wdt))
         self.workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=dev)
         self.ydt = moe.MOE_F32 if wdt == moe.MOE_F32 else moe.MOE_BF16
         self.y = torch.empty((T, H), dtype=f32 if self.ydt == moe.MOE_F32 else torch.bfloat16, device=dev)
