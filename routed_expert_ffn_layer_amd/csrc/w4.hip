@@ -34,10 +34,15 @@ namespace moe {
 
 // More than 16 tokens: w4_few reads the codes once per 16 tokens, w4_wide once per 64 with blocks
 // of 4 row tiles (4 waves of one) or 16 (8 waves of two, which read a token from LDS half as
-// often).  Measured at K = 4096: 64 tokens, N = 2048: w4_few 14 us, w4_wide 25; N = 4096: 26 and 22;
-// N = 12288: 39 and 27; N = 32768: 4-tile blocks 42, 16-tile blocks 48; N = 65536: 83 and 59.
-constexpr int kW4WideWork = 1024;   // row tiles x passes of 16 tokens from which w4_wide is taken
-constexpr int kW4WideTiles = 2800;  // row tiles from which its blocks have 16
+// often).  Measured at K = 4096, INT4 in groups of 128: 64 tokens, N = 2048: w4_few 14 us,
+// w4_wide 23; N = 4096: 27 and 24; 24 tokens, N = 6000: 16.0 and 15.4, N = 4096: 13 and 15.
+// Above 32 tokens a CU holds two blocks of 4 row tiles, so 2048 tiles are one round of them: N =
+// 24576: 4-tile blocks 39, 16-tile blocks 47 (MXFP4 29 and 33, groups of 64 55 and 51); N = 36000: 57
+// and 49 (44 and 36, 79 and 51); N = 65536: 84 and 63.  Up to 32 it holds four: N = 36000: 30 and 31,
+// N = 65536: 48 and 41.
+constexpr int kW4WideWork = 1024;    // row tiles x passes of 16 tokens from which w4_wide is taken
+constexpr int kW4WideTiles = 2049;   // row tiles from which its blocks have 16
+constexpr int kW4WideTiles32 = 2800; // the same up to 32 tokens
 
 size_t w4_code_bytes(int N, int K) { return (size_t)((N + 15) / 16) * ((K + 127) / 128) * 1024; }
 
@@ -469,6 +474,13 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
 // up to three slices are in flight in registers.
 template <int FMT, int G, int R, int W, int NT, bool BF16OUT>
 __global__ __launch_bounds__(64 * W) void w4_wide(W4Args a) {
+  // Both steps of a slice are multiplied, also where the last has one: the missing one's codes,
+  // parameters and tokens are zeros, and without a branch between them the compiler runs the
+  // second's loads and products into the first's (N = 12288, K = 4096, 24 tokens: INT4 in
+  // groups of 64 19.8 -> 17.4 us, MXFP4 14.5 -> 13.6).  Blocks of 16 row tiles gain nothing
+  // or run out of registers (INT4 in groups of 128, N = 65536, 64 tokens: 67 -> 73 us), and so
+  // does INT4 in groups of 32 with 64 tokens (39 -> 142).
+  constexpr bool BOTH = R == 1 && !(FMT == kW4Int4 && G == 32 && NT > 2);
   constexpr int ROWS = 16 * NT, LD = 512 + 16;
   constexpr int PIECES = ROWS * 32 / (64 * W);  // 16-byte pieces of a slice per thread
   __shared__ __attribute__((aligned(16))) uint8_t xs[2][ROWS * LD];
@@ -536,7 +548,7 @@ __global__ __launch_bounds__(64 * W) void w4_wide(W4Args a) {
     const uint8_t* x = xs[s & 1] + row;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      if (2 * s + u < sh.nk)
+      if (BOTH || 2 * s + u < sh.nk)
         w4_step<FMT, G, R, NT>(acc, b.w[u], b.p, u, 2 * s + u, [&](int nt, int f) {
           return *reinterpret_cast<const u32x4*>(x + nt * 16 * LD + u * 256 + (FMT == kW4Mxfp4 ? 64 * g + 16 * f : 64 * f + 16 * g));
         });
@@ -566,7 +578,7 @@ template <int FMT, int G, bool BF16OUT>
 static void launch_t(const W4Args& a, hipStream_t st) {
   const int tiles = (a.N + 15) / 16, pairs = ((a.K + 127) / 128 + 1) / 2;
   if (a.T > 16 && (int64_t)tiles * ((a.T + 15) / 16) >= kW4WideWork) {
-    const bool wide = tiles >= kW4WideTiles;
+    const bool wide = tiles >= (a.T <= 32 ? kW4WideTiles32 : kW4WideTiles);
     const int rows = wide ? 16 : 4;  // row tiles of a block
     const dim3 grid((unsigned)((tiles + rows - 1) / rows), (unsigned)((a.T + 63) / 64));
     if (wide && a.T <= 32) hipLaunchKernelGGL((w4_wide<FMT, G, 2, 8, 2, BF16OUT>), grid, dim3(512), 0, st, a);

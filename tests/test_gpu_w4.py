@@ -179,6 +179,25 @@ def test_extreme_scales_and_zeros():
     assert np.all(np.abs(y.double().cpu().numpy()[:, keep] - ref) <= lim)
 
 
+@pytest.mark.parametrize("fmt,group", FORMATS, ids=["mxfp4", "int4_32", "int4_64", "int4_128"])
+@pytest.mark.parametrize("T,N", [(20, 9000), (64, 5000), (40, 33000)])
+@pytest.mark.parametrize("K", [32, 288])
+def test_an_odd_number_of_column_steps(T, N, K, fmt, group):
+    """Blocks of 4 and 16 row tiles whose last pair of column steps has one: close to the formula, and a
+    token with infinities and NaN in that step stays its own."""
+    codes, scales, zeros = _weights(fmt, N, K, group, seed=61)
+    w = _pack(fmt, codes, scales, zeros, K, group)
+    xb = _x(T, K, 62)
+    x = to_dev(xb).view(torch.bfloat16)
+    y, y2 = torch.empty((T, N), device=dev()), torch.empty((T, N), device=dev())
+    moe.moe_w4_linear(fmt, w, N, K, group, x, None, y)
+    _check(y, *_dequant(fmt, codes, scales, zeros, K, group), xb, None, False, f"{fmt} {group} {T} {N} {K}")
+    x[3, K - 1], x[T - 1, K - 2] = float("inf"), float("nan")
+    moe.moe_w4_linear(fmt, w, N, K, group, x, None, y2)
+    keep = [t for t in range(T) if t not in (3, T - 1)]
+    assert torch.equal(y[keep], y2[keep]) and bool(torch.isnan(y2[T - 1]).all())
+
+
 def test_a_bad_token_stays_its_own():
     for fmt, group in FORMATS:
         N, K = 40, 512
