@@ -19,7 +19,10 @@
 // subnormals and the first binade are one linear run), so the scaled convert by 2^9
 // gives q exactly, two per instruction.
 //   sum_k x W = sum over groups s * (sum_k x q - z sum_k x)
-// and sum_k x over the same 32 columns is one more MFMA with an all-ones operand.
+// and sum_k x over the same 32 columns is one more MFMA with an all-ones operand.  That identity
+// holds while nothing overflows: an infinite x makes both sums infinite and their difference NaN,
+// and finite ones may pass the f32 range before the scale brings them back.  Either leaves the
+// output infinite or NaN, so an output that is gets formed again from W itself (int4_redo).
 //
 // Up to 16 tokens the codes bound the product (MXFP4, 65536 x 4096, 16 tokens: 33 us,
 // 4.4 TB/s); small matrices are bound by one launch and one round trip to memory (2048 x 2048:
@@ -270,6 +273,48 @@ __device__ __forceinline__ void store_y(const W4Args& a, int64_t row, int64_t co
     static_cast<float*>(a.y)[row * a.y_ld + col] = y;
 }
 
+// An INT4 output that came out infinite or NaN, again from the definition: s (q - z) is exact in
+// f32 (f16 times an integer of 9 bits), its products with x are added in ascending k with one
+// rounding each.  Runs when a wave's last output is written, with nothing else in registers, so that
+// the ordinary path pays a comparison per output (within 1% at 1 to 64 tokens).  It is bound by a
+// single lane's unpacking: a batch with one infinite token 785 us instead of 35 (65536 x 4096, 16 tokens),
+// 270 instead of 60 (64 tokens); outputs that are NaN end with the first NaN.
+template <int G, bool BF16OUT>
+__device__ __forceinline__ void int4_redo(const W4Args& a, const W4Shape& sh, int64_t t, int64_t col) {
+  if (BF16OUT) {
+    if (isfinite(bf16_bits_to_f32(static_cast<const uint16_t*>(a.y)[t * a.y_ld + col]))) return;
+  } else {
+    if (isfinite(static_cast<const float*>(a.y)[t * a.y_ld + col])) return;
+  }
+  const int64_t tile = col >> 4;
+  const int row = (int)(col & 15);
+  const uint8_t* codes = a.w + (size_t)tile * sh.code_tile + row * 16;
+  const uint8_t* par = a.w + sh.par_at + (size_t)tile * sh.par_tile + row * 16;
+  const uint16_t* x = a.x + t * a.x_ld;
+  float y = 0.f;
+#pragma unroll 1
+  for (int k0 = 0; k0 < a.K && y == y; k0 += 32) {  // NaN stays NaN
+    const uint32_t pw = *reinterpret_cast<const uint32_t*>(par + k0 / G / 4 * 256 + k0 / G % 4 * 4);
+    const float sc = f16_lo(pw), z = f16_hi(pw);
+    u32x4 xv[4];
+    uint32_t q[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      xv[g] = ldg16(x + k0 + 8 * g);
+      q[g] = *reinterpret_cast<const uint32_t*>(codes + (size_t)(k0 / 128) * 1024 + g * 256 + k0 % 128 / 32 * 4);
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // column j in nibble 2 j, column 4 + j in nibble 2 j + 1
+        const float code = (float)(q[g] >> (8 * (j & 3) + (j & 4)) & 15u);
+        const float xj = __uint_as_float(j & 1 ? xv[g][j / 2] & 0xffff0000u : xv[g][j / 2] << 16);
+        y = fmaf(sc * (code - z), xj, y);
+      }
+  }
+  store_y<BF16OUT>(a, t, col, y);
+}
+
 // Up to 16 tokens.  The waves of a block split K in pairs of column steps, so a wave's token
 // fragments are the same for every row tile: it keeps them in registers (NC pairs of steps;
 // NC = 0: K too long, they are read again for every tile) and streams the codes of the
@@ -395,6 +440,7 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
   };
   clear();
   int q = lo, half = 0;
+  uint64_t again = 0;  // INT4: lanes with an output to be formed again
   const int red_tile = VN * waves * 64;
   auto compute = [&](const Buf& b, int c, const u32x4(&x0)[VN], const u32x4(&x1)[VN]) {
     const int step = step0 + 2 * c;
@@ -433,7 +479,9 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
       float y = 0.f;
       for (int w = 0; w < waves; ++w) y += part[(v * waves + w) * 64 + lane];
       const int64_t col = (int64_t)q * 16 + (lane & 15);
-      if (g + 4 * v < m && col < a.N) store_y<BF16OUT>(a, t0 + g + 4 * v, col, y);
+      const bool mine = g + 4 * v < m && col < a.N;
+      if (mine) store_y<BF16OUT>(a, t0 + g + 4 * v, col, y);
+      if constexpr (FMT == kW4Int4) again |= __ballot(mine && !isfinite(y));
     }
     half ^= 1;
     return ++q < hi;
@@ -464,6 +512,19 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
     };
     while (turn(buf[0]) && turn(buf[1])) {
     }
+  }
+  if constexpr (FMT == kW4Int4) {
+    if (again == 0) return;
+    // the lane anew: kept until here it would take a register from the loop
+    const int l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+#pragma unroll 1
+    for (q = lo; q < hi; ++q)
+#pragma unroll 1
+      for (int v = 0; v < VN; ++v) {
+        const int64_t col = (int64_t)q * 16 + (l & 15);
+        const int t = (l >> 4) + 4 * v;
+        if ((q * VN + v) % waves == kp && t < m && col < a.N) int4_redo<G, BF16OUT>(a, sh, t0 + t, col);
+      }
   }
 }
 
@@ -560,6 +621,7 @@ __global__ __launch_bounds__(64 * W) void w4_wide(W4Args a) {
   };
   while (turn(buf[0]) && turn(buf[1]) && turn(buf[2])) {
   }
+  bool again = false;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int64_t col = (int64_t)(tile0 + r) * 16 + (lane & 15);
@@ -569,8 +631,20 @@ __global__ __launch_bounds__(64 * W) void w4_wide(W4Args a) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int t = nt * 16 + g + 4 * v;
-        if (t < m) store_y<BF16OUT>(a, t0 + t, col, acc[r][nt][v]);
+        if (t < m) {
+          store_y<BF16OUT>(a, t0 + t, col, acc[r][nt][v]);
+          again |= !isfinite(acc[r][nt][v]);
+        }
       }
+  }
+  if constexpr (FMT == kW4Int4) {
+    if (!again) return;
+#pragma unroll 1
+    for (int r = 0; r < R; ++r) {
+      const int64_t col = (int64_t)(tile0 + r) * 16 + (lane & 15);
+#pragma unroll 1
+      for (int t = g; t < m && col < a.N; t += 4) int4_redo<G, BF16OUT>(a, sh, t0 + t, col);
+    }
   }
 }
 

@@ -314,3 +314,43 @@ def test_a_decode_step_together(ora, fmt, group):
     ref, bound = _reference(ora, lay, ids, w64)
     check_layer(y, ref, bound, True, "layer")
     _check(out, *_dequant(fmt, *mats["head"], H, group), bits(y), None, False, "head")
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,N,K", [(1, 40, 512), (4, 33, 9024), (3, 50, 8192), (7, 40, 512), (8, 20, 6112), (6, 40, 9024),
+                                   (16, 40, 544), (12, 33, 6112), (9, 17, 16384), (17, 40, 512), (20, 9000, 416),
+                                   (64, 5000, 256), (40, 33000, 96), (30, 45003, 96), (70, 45000, 160)])
+def test_infinite_and_huge_activations(T, N, K, group):
+    """INT4 holds y = sum s (q - z) x over every x: an infinite x gives the infinity of its products'
+    sign, NaN only where q = z (or two infinities differ), and finite x whose sums with the codes alone would
+    pass the f32 range give the finite result.  The weights are small enough that no sum of whole products
+    does.  With K such products the bound of the module holds, its magnitudes included."""
+    codes, scales, zeros = _weights(moe.MOE_INT4, N, K, group, seed=81)
+    zeros[::3] = np.random.default_rng(82).integers(0, 256, zeros[::3].shape)
+    scales[scales == 0] = np.float16(0.001)
+    xb = synth.bf16_bits_to_f32(_x(T, K, 83))
+    xb[0, K // 2 + 1] = np.inf
+    if T > 1:
+        xb[T - 1, K - 1] = -np.inf
+    if T > 2:  # two in one group
+        xb[1] = 0
+        xb[1, K - 2], xb[1, K - 7] = 3e37, 2.9e37
+    if T > 3:
+        xb[2, 0], xb[2, 40] = np.inf, -np.inf
+    x = synth.bf16_bits(xb)
+    xf = synth.bf16_bits_to_f32(x).astype(np.float64)
+    y = torch.empty((T, N), device=dev())
+    moe.moe_w4_linear(moe.MOE_INT4, _pack(moe.MOE_INT4, codes, scales, zeros, K, group), N, K, group, to_dev(x), None, y)
+    got = y.double().cpu().numpy()
+    w, mag = _dequant(moe.MOE_INT4, codes, scales, zeros, K, group)
+    with np.errstate(invalid="ignore"):
+        for t in range(T):
+            far = ~np.isfinite(xf[t])
+            ref = np.where(far, 0.0, xf[t]) @ w.T
+            if far.any():
+                ref = ref + (w[:, far] * xf[t, far]).sum(1)
+            else:
+                lim = 2 * (2 * K + 64) * U * (mag @ np.abs(xf[t])) + 1e-37
+                assert np.isfinite(got[t]).all() and np.all(np.abs(got[t] - ref) <= lim), t
+            if far.any():
+                np.testing.assert_array_equal(got[t], ref, err_msg=str(t))
