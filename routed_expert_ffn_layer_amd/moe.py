@@ -6,6 +6,7 @@ torch is used for); the default stream is torch's current stream.  The library
 must be built (routed_expert_ffn_layer_amd/build.py); there is no fallback.
 """
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -132,9 +133,25 @@ def _torch():
     global _torch_mod
     if _torch_mod is None:
         import torch
-        torch.cuda.init()
         _torch_mod = torch
     return _torch_mod
+
+
+@functools.lru_cache(maxsize=None)
+def _dtypes(kind):
+    """Torch types that hold the named values: bf16 and f16 also as the 16-bit integers of their bits."""
+    t = _torch()
+    return {"bf16": (t.bfloat16, t.int16, t.uint16), "f32": (t.float32,)}[kind]
+
+
+def _want(t, name, kind, rows, width):
+    """Refuses t unless it holds `rows` rows of `width` elements of the kind one behind the
+    other (more rows may follow).  The library sees addresses only and would read other types,
+    strides or sizes as if they were these.  None is left to the library's own check."""
+    if t is not None and (t.dtype not in _dtypes(kind) or not t.is_contiguous() or t.numel() < rows * width
+                          or (t.dim() > 1 and t.shape[-1] != width)):
+        raise MoeError(MOE_EINVAL, f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()}, where [{rows}][{width}] "
+                       f"of {kind} are read, contiguous")
 
 
 def _ptr(t):
@@ -279,6 +296,9 @@ def moe_w4_bytes(fmt, N, K, group):
     return int(lib().moe_w4_bytes(fmt, N, K, group))
 
 
+_w4_bytes = functools.lru_cache(maxsize=256)(moe_w4_bytes)  # a call of the library takes as long as all other checks
+
+
 def moe_w4_pack(fmt, codes, scales, zeros, N, K, group, w, stream=None):
     if w.numel() * w.element_size() < moe_w4_bytes(fmt, N, K, group):
         raise MoeError(MOE_ECAPACITY, f"w holds {w.numel() * w.element_size()} bytes of "
@@ -288,11 +308,19 @@ def moe_w4_pack(fmt, codes, scales, zeros, N, K, group, w, stream=None):
 
 
 def moe_w4_linear(fmt, w, N, K, group, x, bias, y, stream=None):
-    """x [T][K] bf16 and y [T][N] (f32 or bf16), each with unit stride along its rows."""
+    """x [T][K] bf16 and y [T][N] (f32 or bf16), each with unit stride along its rows; bias [N] f32
+    or None; w as moe_w4_pack wrote it."""
     T, (x_ld, x_unit), (y_ld, y_unit) = x.shape[0], x.stride(), y.stride()
     if x.shape != (T, K) or y.shape != (T, N) or x_unit != 1 or (y_unit != 1 and N > 1):
         raise MoeError(MOE_EINVAL, f"x {tuple(x.shape)}, y {tuple(y.shape)} for a product of [T][{K}] to [T][{N}] "
                        "with unit stride along the rows")
+    if x.dtype not in _dtypes("bf16"):
+        raise MoeError(MOE_EINVAL, f"x of {x.dtype}, not bf16")
+    if bias is not None:
+        _want(bias, "bias", "f32", 1, N)
+    if not w.is_contiguous() or w.numel() * w.element_size() < _w4_bytes(fmt, N, K, group):
+        raise MoeError(MOE_EINVAL, f"w: {tuple(w.shape)} of {w.dtype} with strides {w.stride()}, where "
+                       f"{_w4_bytes(fmt, N, K, group)} bytes are read, contiguous")
     ydt = MOE_F32 if y.dtype is _torch().float32 else MOE_BF16 if y.dtype is _torch_mod.bfloat16 else -1
     if T <= 1:  # the stride of a single row's dimension means nothing
         x_ld, y_ld = K, N
