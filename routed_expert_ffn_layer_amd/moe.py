@@ -141,7 +141,7 @@ def _torch():
 def _dtypes(kind):
     """Torch types that hold the named values: bf16 and f16 also as the 16-bit integers of their bits."""
     t = _torch()
-    return {"bf16": (t.bfloat16, t.int16, t.uint16), "f32": (t.float32,)}[kind]
+    return {"bf16": (t.bfloat16, t.int16, t.uint16), "f32": (t.float32,), "int32": (t.int32,)}[kind]
 
 
 def _want(t, name, kind, rows, width):
@@ -149,9 +149,16 @@ def _want(t, name, kind, rows, width):
     other (more rows may follow).  The library sees addresses only and would read other types,
     strides or sizes as if they were these.  None is left to the library's own check."""
     if t is not None and (t.dtype not in _dtypes(kind) or not t.is_contiguous() or t.numel() < rows * width
-                          or (t.dim() > 1 and t.shape[-1] != width)):
+                          or (t.dim() > 1 and t.size(-1) != width)):
         raise MoeError(MOE_EINVAL, f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()}, where [{rows}][{width}] "
                        f"of {kind} are read, contiguous")
+
+
+def _holds(t, name, nbytes):
+    """Refuses t unless its elements follow one another and are nbytes or more."""
+    if t is not None and (not t.is_contiguous() or t.numel() * t.element_size() < nbytes):
+        raise MoeError(MOE_EINVAL, f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()}, where {nbytes} bytes "
+                       "are read, contiguous")
 
 
 def _ptr(t):
@@ -186,6 +193,9 @@ def moe_abi_version():
 
 def moe_expert_bytes(wdt, H, I):
     return int(lib().moe_expert_bytes(wdt, H, I))
+
+
+_expert_bytes = functools.lru_cache(maxsize=256)(moe_expert_bytes)  # shapes only; saves a call of the library
 
 
 def moe_route_topk(logits, k, topk_ids, topk_w, stream=None):
@@ -285,7 +295,22 @@ def moe_layer_decode_workspace(T, k, E, H, I, I_shared, wdt):
 
 def moe_layer_decode(wdt, slot_pool, slot_stride, slot_of_expert, shared_w, I_shared, x, logits, T, k, E, H, I,
                      topk_ids, topk_w, y, ydt, workspace, stream=None):
-    """logits None: topk_ids and topk_w are read instead of written."""
+    """logits None: topk_ids and topk_w are read instead of written.  The layer is the first
+    T rows of x, logits, topk_ids, topk_w and y."""
+    if T > 0:
+        _want(x, "x", "bf16", T, H)
+        _want(logits, "logits", "f32", T, E)
+        _want(topk_ids, "topk_ids", "int32", T, k)
+        _want(topk_w, "topk_w", "f32", T, k)
+        _want(y, "y", "f32" if ydt == MOE_F32 else "bf16", T, H)
+        _want(slot_of_expert, "slot_of_expert", "int32", 1, E)
+        # slots may be rows of a wider tensor; how many are read only the slot table on the device knows
+        eb = _expert_bytes(wdt, H, I)
+        if slot_pool is not None and (slot_pool.stride(-1) != 1 or slot_pool.numel() * slot_pool.element_size() < eb):
+            raise MoeError(MOE_EINVAL, f"slot_pool: {slot_pool.dtype} {tuple(slot_pool.shape)} with strides "
+                           f"{slot_pool.stride()}, where slots of {eb} consecutive bytes are read")
+        _holds(shared_w, "shared_w", _expert_bytes(wdt, H, I_shared))
+        _holds(workspace, "workspace", 0)
     st = _stream_of(stream, slot_pool, slot_of_expert, shared_w, x, logits, topk_ids, topk_w, y, workspace)
     _check(lib().moe_layer_decode(wdt, _ptr(slot_pool), slot_stride, _ptr(slot_of_expert), _ptr(shared_w), I_shared,
                                   _ptr(x), _ptr(logits), T, k, E, H, I, _ptr(topk_ids), _ptr(topk_w), _ptr(y), ydt,
@@ -296,7 +321,7 @@ def moe_w4_bytes(fmt, N, K, group):
     return int(lib().moe_w4_bytes(fmt, N, K, group))
 
 
-_w4_bytes = functools.lru_cache(maxsize=256)(moe_w4_bytes)  # a call of the library takes as long as all other checks
+_w4_bytes = functools.lru_cache(maxsize=256)(moe_w4_bytes)
 
 
 def moe_w4_pack(fmt, codes, scales, zeros, N, K, group, w, stream=None):
@@ -318,9 +343,7 @@ def moe_w4_linear(fmt, w, N, K, group, x, bias, y, stream=None):
         raise MoeError(MOE_EINVAL, f"x of {x.dtype}, not bf16")
     if bias is not None:
         _want(bias, "bias", "f32", 1, N)
-    if not w.is_contiguous() or w.numel() * w.element_size() < _w4_bytes(fmt, N, K, group):
-        raise MoeError(MOE_EINVAL, f"w: {tuple(w.shape)} of {w.dtype} with strides {w.stride()}, where "
-                       f"{_w4_bytes(fmt, N, K, group)} bytes are read, contiguous")
+    _holds(w, "w", _w4_bytes(fmt, N, K, group))
     ydt = MOE_F32 if y.dtype is _torch().float32 else MOE_BF16 if y.dtype is _torch_mod.bfloat16 else -1
     if T <= 1:  # the stride of a single row's dimension means nothing
         x_ld, y_ld = K, N

@@ -32,3 +32,39 @@ def test_linear(what, change):
     a = dict(w=_packed(), x=torch.zeros((T, K), dtype=BF16), bias=None, y=torch.zeros((T, N)))
     a.update(change)
     _refused(what, lambda: moe.moe_w4_linear(moe.MOE_INT4, a["w"], N, K, 64, a["x"], a["bias"], a["y"]))
+
+
+TD, H, I, E, TOPK = 4, 64, 32, 8, 2
+
+
+def _layer(**change):
+    eb = moe.moe_expert_bytes(moe.MOE_BF16, H, I)
+    a = dict(pool=torch.zeros((E, eb), dtype=U8), slots=torch.zeros(E, dtype=torch.int32), shared=None, ish=0,
+             x=torch.zeros((TD, H), dtype=BF16), logits=torch.zeros((TD, E)), ids=torch.zeros((TD, TOPK), dtype=torch.int32),
+             w=torch.zeros((TD, TOPK)), y=torch.zeros((TD, H), dtype=BF16), ydt=moe.MOE_BF16,
+             ws=torch.zeros(moe.moe_layer_decode_workspace(TD, TOPK, E, H, I, 32, moe.MOE_BF16), dtype=U8))
+    a.update(change)
+    moe.moe_layer_decode(moe.MOE_BF16, a["pool"], eb, a["slots"], a["shared"], a["ish"], a["x"], a["logits"], TD, TOPK, E, H,
+                         I, a["ids"], a["w"], a["y"], a["ydt"], a["ws"])
+
+
+@pytest.mark.parametrize("what,change", [
+    ("x", dict(x=torch.zeros((TD, H)))), ("x", dict(x=torch.zeros((TD, H), dtype=torch.float16))),
+    ("x", dict(x=torch.zeros((TD - 1, H), dtype=BF16))), ("x", dict(x=torch.zeros((TD, 2 * H), dtype=BF16)[:, :H])),
+    ("x", dict(x=torch.zeros((H, TD), dtype=BF16).t())), ("x", dict(x=torch.zeros((TD, 2 * H), dtype=BF16))),
+    ("x", dict(x=torch.zeros((1, H), dtype=BF16).expand(TD, H))),
+    ("logits", dict(logits=torch.zeros((TD, E), dtype=BF16))), ("logits", dict(logits=torch.zeros((TD, E + 1))[:, :E])),
+    ("logits", dict(logits=torch.zeros((TD - 1, E)))),
+    ("topk_ids", dict(ids=torch.zeros((TD, TOPK), dtype=torch.int64))), ("topk_ids", dict(ids=torch.zeros((TD, 1), dtype=torch.int32))),
+    ("topk_ids", dict(logits=None, ids=torch.zeros((TD, TOPK), dtype=torch.int64))),
+    ("topk_w", dict(w=torch.zeros((TD, TOPK), dtype=BF16))), ("topk_w", dict(w=torch.zeros((1, TOPK)))),
+    ("topk_w", dict(logits=None, w=torch.zeros((TD, TOPK), dtype=torch.float64))),
+    ("slot_of_expert", dict(slots=torch.zeros(E, dtype=torch.int64))), ("slot_of_expert", dict(slots=torch.zeros(E - 1, dtype=torch.int32))),
+    ("slot_of_expert", dict(slots=torch.zeros(2 * E, dtype=torch.int32)[::2])),
+    ("y", dict(y=torch.zeros((TD, H)))), ("y", dict(ydt=moe.MOE_F32)), ("y", dict(y=torch.zeros((TD, H), dtype=torch.float16))),
+    ("y", dict(y=torch.zeros((TD - 1, H), dtype=BF16))), ("y", dict(y=torch.zeros((TD, H + 8), dtype=BF16)[:, :H])),
+    ("slot_pool", dict(pool=torch.zeros((1, 6000 * 2), dtype=U8))), ("slot_pool", dict(pool=torch.zeros((E, 40000), dtype=U8)[:, ::2])),
+    ("shared_w", dict(shared=torch.zeros(12287, dtype=U8), ish=32)), ("shared_w", dict(shared=torch.zeros(24576, dtype=U8)[::2], ish=32)),
+    ("workspace", dict(ws=torch.zeros(1, dtype=U8).expand(1 << 20)))])
+def test_layer(what, change):
+    _refused(what, lambda: _layer(**change))
