@@ -139,9 +139,12 @@ def _torch():
 
 @functools.lru_cache(maxsize=None)
 def _dtypes(kind):
-    """Torch types that hold the named values: bf16 and f16 also as the 16-bit integers of their bits."""
+    """Torch types that hold the named values: bf16 and f16 also as the 16-bit integers of their
+    bits, E8M0 scales and pairs of 4-bit codes also as bytes."""
     t = _torch()
-    return {"bf16": (t.bfloat16, t.int16, t.uint16), "f32": (t.float32,), "int32": (t.int32,)}[kind]
+    return {"bf16": (t.bfloat16, t.int16, t.uint16), "f32": (t.float32,), "int32": (t.int32,),
+            "f16": (t.float16, t.int16, t.uint16), "uint8": (t.uint8,),
+            "codes": (t.uint8, t.float4_e2m1fn_x2), "e8m0": (t.uint8, t.float8_e8m0fnu)}[kind]
 
 
 def _want(t, name, kind, rows, width):
@@ -152,6 +155,13 @@ def _want(t, name, kind, rows, width):
                           or (t.dim() > 1 and t.size(-1) != width)):
         raise MoeError(MOE_EINVAL, f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()}, where [{rows}][{width}] "
                        f"of {kind} are read, contiguous")
+
+
+def _exactly(t, name, kind, rows, width):
+    """_want with no rows behind the last."""
+    _want(t, name, kind, rows, width)
+    if t is not None and t.numel() != rows * width:
+        raise MoeError(MOE_EINVAL, f"{name}: {tuple(t.shape)} where [{rows}][{width}] is the whole")
 
 
 def _holds(t, name, nbytes):
@@ -325,9 +335,17 @@ _w4_bytes = functools.lru_cache(maxsize=256)(moe_w4_bytes)
 
 
 def moe_w4_pack(fmt, codes, scales, zeros, N, K, group, w, stream=None):
+    """codes [N][K / 2] uint8; scales [N][ceil(K / group)], uint8 (MXFP4) or f16 (INT4); zeros of
+    the scales' shape, uint8, or None."""
     if w.numel() * w.element_size() < moe_w4_bytes(fmt, N, K, group):
         raise MoeError(MOE_ECAPACITY, f"w holds {w.numel() * w.element_size()} bytes of "
                        f"{moe_w4_bytes(fmt, N, K, group)}")
+    if moe_w4_bytes(fmt, N, K, group) > 0:  # 0: shapes that the library refuses
+        groups = -(-K // group)
+        _exactly(codes, "codes", "codes", N, K // 2)
+        _exactly(scales, "scales", "e8m0" if fmt == MOE_MXFP4 else "f16", N, groups)
+        _exactly(zeros, "zeros", "uint8", N, groups)
+        _holds(w, "w", 0)
     st = _stream_of(stream, codes, scales, zeros, w)
     _check(lib().moe_w4_pack(fmt, _ptr(codes), _ptr(scales), _ptr(zeros), N, K, group, _ptr(w), st))
 

@@ -68,3 +68,47 @@ def _layer(**change):
     ("workspace", dict(ws=torch.zeros(1, dtype=U8).expand(1 << 20)))])
 def test_layer(what, change):
     _refused(what, lambda: _layer(**change))
+
+
+def _pack(fmt, **change):
+    group = 32 if fmt == moe.MOE_MXFP4 else 64
+    a = dict(codes=torch.zeros((N, K // 2), dtype=U8), zeros=None,
+             scales=torch.zeros((N, K // group), dtype=U8 if fmt == moe.MOE_MXFP4 else torch.float16),
+             w=torch.zeros(moe.moe_w4_bytes(fmt, N, K, group), dtype=U8))
+    a.update(change)
+    moe.moe_w4_pack(fmt, a["codes"], a["scales"], a["zeros"], N, K, group, a["w"])
+
+
+@pytest.mark.parametrize("fmt,what,change", [
+    (moe.MOE_INT4, "codes", dict(codes=torch.zeros((N, K // 2), dtype=torch.int8))),
+    (moe.MOE_INT4, "codes", dict(codes=torch.zeros((N, K), dtype=U8))),           # one code a byte
+    (moe.MOE_INT4, "codes", dict(codes=torch.zeros((N - 1, K // 2), dtype=U8))),
+    (moe.MOE_INT4, "codes", dict(codes=torch.zeros((N + 1, K // 2), dtype=U8))),
+    (moe.MOE_INT4, "codes", dict(codes=torch.zeros((N, K), dtype=U8)[:, ::2])),
+    (moe.MOE_MXFP4, "codes", dict(codes=torch.zeros((K // 2, N + 8), dtype=U8).t()[:N])),
+    (moe.MOE_INT4, "codes", dict(codes=torch.zeros((N, K // 8), dtype=torch.int32))),
+    (moe.MOE_INT4, "scales", dict(scales=torch.zeros((N, 1), dtype=BF16))),
+    (moe.MOE_INT4, "scales", dict(scales=torch.zeros((N, 1)))),
+    (moe.MOE_INT4, "scales", dict(scales=torch.zeros((1, N), dtype=torch.float16))),
+    (moe.MOE_INT4, "scales", dict(scales=torch.zeros((N, 2), dtype=torch.float16))),
+    (moe.MOE_MXFP4, "scales", dict(scales=torch.zeros((N, 2), dtype=torch.float16))),
+    (moe.MOE_MXFP4, "scales", dict(scales=torch.zeros((N, 1), dtype=U8))),
+    (moe.MOE_INT4, "zeros", dict(zeros=torch.zeros((N, 1), dtype=torch.int8))),
+    (moe.MOE_INT4, "zeros", dict(zeros=torch.zeros((N, 1), dtype=torch.float16))),
+    (moe.MOE_INT4, "zeros", dict(zeros=torch.zeros((N // 2, 1), dtype=U8))),
+    (moe.MOE_INT4, "zeros", dict(zeros=torch.zeros((N, 2), dtype=U8)[:, :1])),
+    (moe.MOE_INT4, "w", dict(w=torch.zeros(1, dtype=U8).expand(1 << 20)))])
+def test_pack(fmt, what, change):
+    _refused(what, lambda: _pack(fmt, **change))
+
+
+def test_types_that_pass():
+    """The types of the same bits go on to the look at the device, which refuses CPU tensors or has none."""
+    for fmt, change in ((moe.MOE_MXFP4, {}), (moe.MOE_INT4, {}),
+                        (moe.MOE_MXFP4, dict(scales=torch.zeros((N, 2), dtype=U8).view(torch.float8_e8m0fnu))),
+                        (moe.MOE_MXFP4, dict(codes=torch.zeros((N, K // 2), dtype=U8).view(torch.float4_e2m1fn_x2))),
+                        (moe.MOE_INT4, dict(scales=torch.zeros((N, 1), dtype=torch.int16))),
+                        (moe.MOE_INT4, dict(codes=torch.zeros(N * K // 2, dtype=U8)))):
+        with pytest.raises((moe.MoeError, RuntimeError)) as e:
+            _pack(fmt, **change)
+        assert not isinstance(e.value, moe.MoeError) or "device" in str(e.value)
