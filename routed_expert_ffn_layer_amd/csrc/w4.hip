@@ -59,9 +59,16 @@ static size_t w4_scale_bytes(int fmt, int N, int K, int group) {
 size_t w4_bytes(int fmt, int N, int K, int group) { return w4_code_bytes(N, K) + w4_scale_bytes(fmt, N, K, group); }
 
 // ---------------------------------------------------------------------------
-// Layout.  One thread per 16-byte code fragment, then per 16 bytes of scales.  Rows past
-// N and columns past K become zero codes and zero scales.
+// Layout.  A thread lays out a 16-byte code fragment at a time, then 16 bytes (MXFP4) or one word
+// of scales, and goes on by the size of the grid: a launch holds fewer than 2^32 threads, a
+// large matrix more fragments.  Rows past N and columns past K become zero codes and zero scales.
 // ---------------------------------------------------------------------------
+constexpr unsigned kPackBlocks = 1 << 16;  // 256 MiB of codes a turn
+static dim3 pack_grid(size_t threads) {
+  const size_t blocks = (threads + 255) / 256;
+  return dim3((unsigned)(blocks < kPackBlocks ? blocks : kPackBlocks));
+}
+
 // The 8 codes of 4 source bytes (element 2i in the low nibble of byte i) in the word order
 // above: nibble 2j holds element j, nibble 2j + 1 element 4 + j (j < 4).
 __device__ __forceinline__ uint32_t int4_word(uint32_t v) {
@@ -75,38 +82,38 @@ template <int FMT>
 __global__ __launch_bounds__(256) void w4_pack_codes(const uint8_t* __restrict__ codes, int N, int K, uint8_t* w) {
   const int nk = (K + 127) / 128;
   const int64_t total = (int64_t)((N + 15) / 16) * nk * 64;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= total) return;
-  const int f = i & 63, r = f & 15, g = f >> 4;
-  const int64_t ts = i >> 6;
-  const int step = ts % nk;
-  const int64_t row = ts / nk * 16 + r;
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (row < N) {
-    const uint8_t* src = codes + row * (K / 2);
-    if constexpr (FMT == kW4Mxfp4) {
-      if (step * 128 + 32 * g < K) v = ldg16(src + step * 64 + 16 * g);
-    } else {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int f = i & 63, r = f & 15, g = f >> 4;
+    const int64_t ts = i >> 6;
+    const int step = ts % nk;
+    const int64_t row = ts / nk * 16 + r;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (row < N) {
+      const uint8_t* src = codes + row * (K / 2);
+      if constexpr (FMT == kW4Mxfp4) {
+        if (step * 128 + 32 * g < K) v = ldg16(src + step * 64 + 16 * g);
+      } else {
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
-        if (step * 128 + 32 * m < K)
-          v[m] = int4_word(*reinterpret_cast<const uint32_t*>(src + step * 64 + 16 * m + 4 * g));
+        for (int m = 0; m < 4; ++m)
+          if (step * 128 + 32 * m < K)
+            v[m] = int4_word(*reinterpret_cast<const uint32_t*>(src + step * 64 + 16 * m + 4 * g));
+      }
     }
+    *reinterpret_cast<u32x4*>(w + i * 16) = v;
   }
-  *reinterpret_cast<u32x4*>(w + i * 16) = v;
 }
 
 __global__ __launch_bounds__(256) void w4_pack_mx_scales(const uint8_t* __restrict__ scales, int N, int K, uint8_t* w) {
   const int nb = ((K + 127) / 128 + 15) / 16, groups = K / 32;
   const int64_t total = (int64_t)((N + 15) / 16) * nb * 64;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= total) return;
-  const int f = i & 63, r = f & 15, g = f >> 4;
-  const int blk = (i >> 6) % nb;
-  const int64_t row = (i >> 6) / nb * 16 + r;
-  for (int b = 0; b < 16; ++b) {
-    const int grp = (blk * 16 + b) * 4 + g;
-    w[i * 16 + b] = row < N && grp < groups ? scales[row * groups + grp] : 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int f = i & 63, r = f & 15, g = f >> 4;
+    const int blk = (i >> 6) % nb;
+    const int64_t row = (i >> 6) / nb * 16 + r;
+    for (int b = 0; b < 16; ++b) {
+      const int grp = (blk * 16 + b) * 4 + g;
+      w[i * 16 + b] = row < N && grp < groups ? scales[row * groups + grp] : 0;
+    }
   }
 }
 
@@ -115,31 +122,31 @@ __global__ __launch_bounds__(256) void w4_pack_int4_scales(const uint16_t* __res
                                                            uint8_t* w) {
   const int nb = (groups + 3) / 4;
   const int64_t total = (int64_t)((N + 15) / 16) * nb * 64;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= total) return;
-  const int q = i & 3, r = (i >> 2) & 15;
-  const int grp = (i >> 6) % nb * 4 + q;
-  const int64_t row = (i >> 6) / nb * 16 + r;
-  uint32_t word = 0;
-  if (row < N && grp < groups) {
-    const int z = zeros ? zeros[row * groups + grp] : 8;
-    word = scales[row * groups + grp] | (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)z) << 16;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int q = i & 3, r = (i >> 2) & 15;
+    const int grp = (i >> 6) % nb * 4 + q;
+    const int64_t row = (i >> 6) / nb * 16 + r;
+    uint32_t word = 0;
+    if (row < N && grp < groups) {
+      const int z = zeros ? zeros[row * groups + grp] : 8;
+      word = scales[row * groups + grp] | (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)z) << 16;
+    }
+    reinterpret_cast<uint32_t*>(w)[i] = word;
   }
-  reinterpret_cast<uint32_t*>(w)[i] = word;
 }
 
 hipError_t launch_w4_pack(int fmt, const uint8_t* codes, const void* scales, const uint8_t* zeros, int N, int K,
                           int group, uint8_t* w, hipStream_t st) {
   const size_t cb = w4_code_bytes(N, K), sb = w4_scale_bytes(fmt, N, K, group);
-  const dim3 gc((unsigned)((cb / 16 + 255) / 256)), block(256);
+  const dim3 gc = pack_grid(cb / 16), block(256);
   if (fmt == kW4Mxfp4) {
     hipLaunchKernelGGL(w4_pack_codes<kW4Mxfp4>, gc, block, 0, st, codes, N, K, w);
-    hipLaunchKernelGGL(w4_pack_mx_scales, dim3((unsigned)((sb / 16 + 255) / 256)), block, 0, st,
-                       static_cast<const uint8_t*>(scales), N, K, w + cb);
+    hipLaunchKernelGGL(w4_pack_mx_scales, pack_grid(sb / 16), block, 0, st, static_cast<const uint8_t*>(scales), N, K,
+                       w + cb);
   } else {
     hipLaunchKernelGGL(w4_pack_codes<kW4Int4>, gc, block, 0, st, codes, N, K, w);
-    hipLaunchKernelGGL(w4_pack_int4_scales, dim3((unsigned)((sb / 4 + 255) / 256)), block, 0, st,
-                       static_cast<const uint16_t*>(scales), zeros, N, (K + group - 1) / group, w + cb);
+    hipLaunchKernelGGL(w4_pack_int4_scales, pack_grid(sb / 4), block, 0, st, static_cast<const uint16_t*>(scales), zeros,
+                       N, (K + group - 1) / group, w + cb);
   }
   return hipGetLastError();
 }

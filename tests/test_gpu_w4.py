@@ -354,3 +354,29 @@ def test_infinite_and_huge_activations(T, N, K, group):
                 assert np.isfinite(got[t]).all() and np.all(np.abs(got[t] - ref) <= lim), t
             if far.any():
                 np.testing.assert_array_equal(got[t], ref, err_msg=str(t))
+
+
+def test_the_most_rows():
+    """2^30 rows: 2^32 fragments of codes and as many words of scales, one more than a launch can
+    have threads.  100 GiB in all; each output has 32 products, so the bound is tight."""
+    N, K, group = 1 << 30, 32, 32
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GiB of free device memory")
+    g = torch.Generator(device=dev()).manual_seed(9)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=dev(), generator=g)
+    scales = torch.full((N, 1), 0.01, dtype=torch.float16, device=dev())
+    scales.view(torch.int16).add_(torch.arange(N, device=dev(), dtype=torch.int32).remainder_(257).to(torch.int16)[:, None])
+    w = torch.empty(moe.moe_w4_bytes(moe.MOE_INT4, N, K, group), dtype=torch.uint8, device=dev())
+    moe.moe_w4_pack(moe.MOE_INT4, codes, scales, None, N, K, group, w)
+    x = _x(1, K, 4)
+    y = torch.empty((1, N), dtype=torch.bfloat16, device=dev())
+    moe.moe_w4_linear(moe.MOE_INT4, w, N, K, group, to_dev(x), None, y)
+    torch.cuda.synchronize()
+    edge = [b + d for b in (1 << 22, 1 << 28, 1 << 29, 3 << 28) for d in (-17, -1, 0, 16)]
+    rows = torch.tensor([0, 1, 15, 16, N - 17, N - 16, N - 1] + edge, device=dev())
+    rows = torch.cat([rows, torch.randint(0, N, (4000,), device=dev(), generator=g)])
+    wr, mag = _dequant(moe.MOE_INT4, codes[rows].cpu().numpy(), scales[rows].cpu().numpy(), None, K, group)
+    _check(y[:, rows], wr, mag, x, None, True, "2^30 rows")
+    del codes, scales, w, y
+    torch.cuda.empty_cache()
