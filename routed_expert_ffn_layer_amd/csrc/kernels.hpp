@@ -78,8 +78,7 @@ size_t decode_layer_plan_bytes();
 constexpr int kDecodeLayerMaxH = 65536;  // one token row fits the gate/up kernel's LDS
 hipError_t launch_decode_layer(int wtype, const DecodeLayerArgs& a, bool bf16_out, hipStream_t st);
 
-// Linear product with 4-bit weights (w4.hip).
-constexpr int kW4Mxfp4 = 2, kW4Int4 = 4;
+// Linear product with 4-bit weights (w4.hip).  fmt: W_MXFP4 or W_INT4.
 struct W4Args {
   const uint8_t* w;    // laid out by launch_w4_pack
   const uint16_t* x;   // rows of K bf16, x_ld elements apart
@@ -88,8 +87,7 @@ struct W4Args {
   int64_t x_ld, y_ld;
   int T, N, K, group;
 };
-// Bytes of the codes and of the whole laid-out matrix.
-size_t w4_code_bytes(int N, int K);
+// Bytes of the laid-out matrix.
 size_t w4_bytes(int fmt, int N, int K, int group);
 hipError_t launch_w4_pack(int fmt, const uint8_t* codes, const void* scales, const uint8_t* zeros, int N, int K,
                           int group, uint8_t* w, hipStream_t st);

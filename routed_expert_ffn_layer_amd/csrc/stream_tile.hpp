@@ -24,12 +24,11 @@ __device__ __forceinline__ int a_token(int lane) {
 constexpr int kPastEnd = 0x7ffffff0;
 
 // Byte offset, inside a token row, of fragment m of step s for k group g, or kPastEnd
-// past column K (K a multiple of 32).  bf16 and MXFP4 follow the slot layout (an MXFP4
-// lane owns a whole 32-element block); INT4 words hold 8 columns of block m.
-template <int WT>
+// past column K (K a multiple of 32).  MXFP4 follows the slot layout (a lane owns a whole
+// 32-element block), words of other 4-bit codes hold 8 columns of block m.
+template <int FMT>
 __device__ __forceinline__ int frag_offset(int s, int m, int g, int K) {
-  if constexpr (WT == W_BF16) return s * 64 + 16 * g;
-  if constexpr (WT == W_MXFP4) return s * 128 + 32 * g < K ? s * 256 + 64 * g + 16 * m : kPastEnd;
+  if constexpr (FMT == W_MXFP4) return s * 128 + 32 * g < K ? s * 256 + 64 * g + 16 * m : kPastEnd;
   return s * 128 + 32 * m < K ? s * 256 + 64 * m + 16 * g : kPastEnd;
 }
 

@@ -47,11 +47,11 @@ constexpr int kW4WideWork = 1024;    // row tiles x passes of 16 tokens from whi
 constexpr int kW4WideTiles = 2049;   // row tiles from which its blocks have 16
 constexpr int kW4WideTiles32 = 2800; // the same up to 32 tokens
 
-size_t w4_code_bytes(int N, int K) { return (size_t)((N + 15) / 16) * ((K + 127) / 128) * 1024; }
+static size_t w4_code_bytes(int N, int K) { return (size_t)((N + 15) / 16) * ((K + 127) / 128) * 1024; }
 
 static size_t w4_scale_bytes(int fmt, int N, int K, int group) {
   const size_t rt = (N + 15) / 16;
-  if (fmt == kW4Mxfp4) return rt * (((K + 127) / 128 + 15) / 16) * 1024;
+  if (fmt == W_MXFP4) return rt * (((K + 127) / 128 + 15) / 16) * 1024;
   const size_t groups = (K + group - 1) / group;
   return rt * ((groups + 3) / 4) * 256;
 }
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(256) void w4_pack_codes(const uint8_t* __restrict__
     u32x4 v = {0u, 0u, 0u, 0u};
     if (row < N) {
       const uint8_t* src = codes + row * (K / 2);
-      if constexpr (FMT == kW4Mxfp4) {
+      if constexpr (FMT == W_MXFP4) {
         if (step * 128 + 32 * g < K) v = ldg16(src + step * 64 + 16 * g);
       } else {
 #pragma unroll
@@ -139,12 +139,12 @@ hipError_t launch_w4_pack(int fmt, const uint8_t* codes, const void* scales, con
                           int group, uint8_t* w, hipStream_t st) {
   const size_t cb = w4_code_bytes(N, K), sb = w4_scale_bytes(fmt, N, K, group);
   const dim3 gc = pack_grid(cb / 16), block(256);
-  if (fmt == kW4Mxfp4) {
-    hipLaunchKernelGGL(w4_pack_codes<kW4Mxfp4>, gc, block, 0, st, codes, N, K, w);
+  if (fmt == W_MXFP4) {
+    hipLaunchKernelGGL(w4_pack_codes<W_MXFP4>, gc, block, 0, st, codes, N, K, w);
     hipLaunchKernelGGL(w4_pack_mx_scales, pack_grid(sb / 16), block, 0, st, static_cast<const uint8_t*>(scales), N, K,
                        w + cb);
   } else {
-    hipLaunchKernelGGL(w4_pack_codes<kW4Int4>, gc, block, 0, st, codes, N, K, w);
+    hipLaunchKernelGGL(w4_pack_codes<W_INT4>, gc, block, 0, st, codes, N, K, w);
     hipLaunchKernelGGL(w4_pack_int4_scales, pack_grid(sb / 4), block, 0, st, static_cast<const uint16_t*>(scales), zeros,
                        N, (K + group - 1) / group, w + cb);
   }
@@ -172,7 +172,7 @@ __device__ __forceinline__ float f16_hi(uint32_t w) { return (float)__builtin_bi
 // lane, this lane's weight row.  MXFP4: one word of E8M0 bytes.  INT4: 128 / G words a step.
 template <int FMT, int G>
 struct W4Params {
-  static constexpr int words = FMT == kW4Mxfp4 ? 1 : 256 / G;
+  static constexpr int words = FMT == W_MXFP4 ? 1 : 256 / G;
   uint32_t v[words];
 };
 
@@ -184,7 +184,7 @@ struct W4Shape {
     nk = (K + 127) / 128;
     code_tile = nk * 1024;
     par_at = (size_t)((N + 15) / 16) * code_tile;
-    par_tile = fmt == kW4Mxfp4 ? (nk + 15) / 16 * 1024 : ((K + G - 1) / G + 3) / 4 * 256;
+    par_tile = fmt == W_MXFP4 ? (nk + 15) / 16 * 1024 : ((K + G - 1) / G + 3) / 4 * 256;
   }
 };
 
@@ -192,7 +192,7 @@ struct W4Shape {
 template <int FMT, int G>
 __device__ __forceinline__ void load_params(W4Params<FMT, G>& p, __amdgpu_buffer_rsrc_t buf, int step, bool live) {
   const int lane = threadIdx.x & 63;
-  if constexpr (FMT == kW4Mxfp4) {
+  if constexpr (FMT == W_MXFP4) {
     p.v[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(buf, lane * 16, live ? step / 16 * 1024 + step % 16 / 4 * 4 : 0, 0);
   } else {
     // word (group % 4) of block group / 4, 16 bytes a row
@@ -221,7 +221,7 @@ __device__ __forceinline__ void load_params(W4Params<FMT, G>& p, __amdgpu_buffer
 template <int FMT, int G, int R, int NT, typename Frag>
 __device__ __forceinline__ void w4_step(f32x4 (&acc)[R][NT], const u32x4 (&w)[R],
                                         const W4Params<FMT, G> (&p)[R], int u, int step, const Frag& frag) {
-  if constexpr (FMT == kW4Mxfp4) {
+  if constexpr (FMT == W_MXFP4) {
     float sc[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) sc[r] = scale_of_word(p[r].v[0], step);
@@ -344,7 +344,7 @@ template <int FMT, int G, int VN>
 __device__ __forceinline__ void w4_step_few(float (&acc)[VN], f32x4 (&part)[4 / VN], u32x4 w, const W4Params<FMT, G>& p,
                                             int u, int step, const u32x4 (&x)[VN]) {
   constexpr int NA = 4 / VN;
-  if constexpr (FMT == kW4Mxfp4) {
+  if constexpr (FMT == W_MXFP4) {
     const float sc = scale_of_word(p.v[0], step);
 #pragma unroll
     for (int m = 0; m < 4; ++m) part[m % NA] = mfma16(x[m / NA], fp4x8_to_bf16x8(w[m], sc), part[m % NA]);
@@ -471,7 +471,7 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
 #pragma unroll
     for (int v = 0; v < VN; ++v) {
       float d = acc[v];
-      if constexpr (FMT == kW4Mxfp4 || VN == 4) {
+      if constexpr (FMT == W_MXFP4 || VN == 4) {
         d = sums[0][v];
 #pragma unroll
         for (int f = 1; f < NA; ++f) d += sums[f][v + VN * f];
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
       const int64_t col = (int64_t)q * 16 + (lane & 15);
       const bool mine = g + 4 * v < m && col < a.N;
       if (mine) store_y<BF16OUT>(a, t0 + g + 4 * v, col, y);
-      if constexpr (FMT == kW4Int4) again |= __ballot(mine && !isfinite(y));
+      if constexpr (FMT == W_INT4) again |= __ballot(mine && !isfinite(y));
     }
     half ^= 1;
     return ++q < hi;
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(1024) void w4_few(W4Args a, int nc) {
     while (turn(buf[0]) && turn(buf[1])) {
     }
   }
-  if constexpr (FMT == kW4Int4) {
+  if constexpr (FMT == W_INT4) {
     if (again == 0) return;
     // the lane anew: kept until here it would take a register from the loop
     const int l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
@@ -548,7 +548,7 @@ __global__ __launch_bounds__(64 * W) void w4_wide(W4Args a) {
   // groups of 64 19.8 -> 17.4 us, MXFP4 14.5 -> 13.6).  Blocks of 16 row tiles gain nothing
   // or run out of registers (INT4 in groups of 128, N = 65536, 64 tokens: 67 -> 73 us), and so
   // does INT4 in groups of 32 with 64 tokens (39 -> 142).
-  constexpr bool BOTH = R == 1 && !(FMT == kW4Int4 && G == 32 && NT > 2);
+  constexpr bool BOTH = R == 1 && !(FMT == W_INT4 && G == 32 && NT > 2);
   constexpr int ROWS = 16 * NT, LD = 512 + 16;
   constexpr int PIECES = ROWS * 32 / (64 * W);  // 16-byte pieces of a slice per thread
   __shared__ __attribute__((aligned(16))) uint8_t xs[2][ROWS * LD];
@@ -618,7 +618,7 @@ __global__ __launch_bounds__(64 * W) void w4_wide(W4Args a) {
     for (int u = 0; u < 2; ++u)
       if (BOTH || 2 * s + u < sh.nk)
         w4_step<FMT, G, R, NT>(acc, b.w[u], b.p, u, 2 * s + u, [&](int nt, int f) {
-          return *reinterpret_cast<const u32x4*>(x + nt * 16 * LD + u * 256 + (FMT == kW4Mxfp4 ? 64 * g + 16 * f : 64 * f + 16 * g));
+          return *reinterpret_cast<const u32x4*>(x + nt * 16 * LD + u * 256 + (FMT == W_MXFP4 ? 64 * g + 16 * f : 64 * f + 16 * g));
         });
     store_slice((s + 1) & 1);
     load_slice(s + 2);  // past the last slice: nothing is read
@@ -644,7 +644,7 @@ __global__ __launch_bounds__(64 * W) void w4_wide(W4Args a) {
         }
       }
   }
-  if constexpr (FMT == kW4Int4) {
+  if constexpr (FMT == W_INT4) {
     if (!again) return;
 #pragma unroll 1
     for (int r = 0; r < R; ++r) {
@@ -695,10 +695,10 @@ static void launch_out(const W4Args& a, bool bf16_out, hipStream_t st) {
 
 hipError_t launch_w4_linear(int fmt, const W4Args& a, bool bf16_out, hipStream_t st) {
   if (a.T == 0) return hipSuccess;
-  if (fmt == kW4Mxfp4) launch_out<kW4Mxfp4, 32>(a, bf16_out, st);
-  else if (a.group == 32) launch_out<kW4Int4, 32>(a, bf16_out, st);
-  else if (a.group == 64) launch_out<kW4Int4, 64>(a, bf16_out, st);
-  else launch_out<kW4Int4, 128>(a, bf16_out, st);
+  if (fmt == W_MXFP4) launch_out<W_MXFP4, 32>(a, bf16_out, st);
+  else if (a.group == 32) launch_out<W_INT4, 32>(a, bf16_out, st);
+  else if (a.group == 64) launch_out<W_INT4, 64>(a, bf16_out, st);
+  else launch_out<W_INT4, 128>(a, bf16_out, st);
   return hipGetLastError();
 }
 
