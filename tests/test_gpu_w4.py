@@ -380,3 +380,27 @@ def test_the_most_rows():
     _check(y[:, rows], wr, mag, x, None, True, "2^30 rows")
     del codes, scales, w, y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,N", [(2, 77), (6, 77), (13, 77), (40, 9003)])
+def test_infinite_activations_with_bias_strides_and_bf16(T, N):
+    """An output formed again takes its bias and its place in a wider tensor; a bias of -inf (a masked
+    row) makes that row -inf for finite tokens; other tokens are those of a batch without the infinite one."""
+    K, group = 544, 64
+    codes, scales, zeros = _weights(moe.MOE_INT4, N, K, group, seed=91)
+    scales[scales == 0] = np.float16(0.001)
+    w = _pack(moe.MOE_INT4, codes, scales, zeros, K, group)
+    bias = np.random.default_rng(92).standard_normal(N).astype(np.float32)
+    bias[5] = -np.inf
+    x = to_dev(_x(T, K, 93)).view(torch.bfloat16)
+    out = torch.full((T + 1, N + 5), 7.0, dtype=torch.bfloat16, device=dev())
+    clean, y = torch.empty((T, N), dtype=torch.bfloat16, device=dev()), out[:T, :N]
+    moe.moe_w4_linear(moe.MOE_INT4, w, N, K, group, x, to_dev(bias), clean)
+    x[1, 100] = -float("inf")
+    moe.moe_w4_linear(moe.MOE_INT4, w, N, K, group, x, to_dev(bias), y)
+    keep = [t for t in range(T) if t != 1]
+    assert torch.equal(y[keep], clean[keep]) and bool((clean[:, 5] == -float("inf")).all())
+    d = _dequant(moe.MOE_INT4, codes, scales, zeros, K, group)[0][:, 100]
+    with np.errstate(invalid="ignore"):
+        np.testing.assert_array_equal(y[1].float().cpu().numpy(), d * -np.inf + bias)
+    assert bool((out[T] == 7).all()) and bool((out[:, N:] == 7).all())
