@@ -24,10 +24,12 @@
 // and finite ones may pass the f32 range before the scale brings them back.  Either leaves the
 // output infinite or NaN, so an output that is gets formed again from W itself (int4_redo).
 //
-// Up to 16 tokens the codes bound the product (MXFP4, 65536 x 4096, 16 tokens: 33 us,
-// 4.4 TB/s); small matrices are bound by one launch and one round trip to memory (2048 x 2048:
-// 3.8 us); 64 tokens by the instructions that unpack, scale and multiply (INT4, 65536 x 4096:
-// 58 us, of which products and sums alone take 35).
+// Times here and below: captured calls over enough weight sets to come from HBM, K = 4096.  Up to 16
+// tokens the codes bound the product (MXFP4, 65536 rows, 16 tokens: 35.5 us, 83% of a large copy's rate);
+// small matrices are bound by one launch and one round trip to memory (2048 x 2048: 3.7 us). 64 tokens over
+// many rows are bound by the instructions that unpack, scale and multiply (INT4 in groups of 128, 65536 rows:
+// 58 us, floor 32), and 17 to 64 over 2048 to 36000 rows by w4_wide's walk of the whole K in one wave: 64 tokens
+// take 24 us at 4096 rows and 26 at 12288 (floors 2 and 6).
 #include <type_traits>
 
 #include "kernels.hpp"
@@ -37,12 +39,18 @@ namespace moe {
 
 // More than 16 tokens: w4_few reads the codes once per 16 tokens, w4_wide once per 64 with blocks
 // of 4 row tiles (4 waves of one) or 16 (8 waves of two, which read a token from LDS half as
-// often).  Measured at K = 4096, INT4 in groups of 128: 64 tokens, N = 2048: w4_few 14 us,
-// w4_wide 23; N = 4096: 27 and 24; 24 tokens, N = 6000: 16.0 and 15.4, N = 4096: 13 and 15.
-// Above 32 tokens a CU holds two blocks of 4 row tiles, so 2048 tiles are one round of them: N =
-// 24576: 4-tile blocks 39, 16-tile blocks 47 (MXFP4 29 and 33, groups of 64 55 and 51); N = 36000: 57
-// and 49 (44 and 36, 79 and 51); N = 65536: 84 and 63.  Up to 32 it holds four: N = 36000: 30 and 31,
-// N = 65536: 48 and 41.
+// often).  Measured at K = 4096, us, for INT4 in groups of 128 / 64 / 32 and MXFP4:
+//   64 tokens, N = 2048:   w4_few 15 / 15 / 16, 15     w4_wide 24 / 27 / 38, 19
+//              N = 4096:          27 / 27 / 30, 27             24 / 27 / 38, 20
+//   24 tokens, N = 6000:          16 / 16 / 18, 16             15 / 17 / 20, 13
+//              N = 12288:         19 / 20 / 22, 18             16 / 18 / 21, 14
+// Above 32 tokens a CU holds two blocks of 4 row tiles, so 2048 tiles are one round of them; up to 32 it
+// holds more, by the registers (groups of 32 one: there the second limit costs 20 us at N = 36000).
+//   64 tokens, N = 24576:  4 tiles 39 / 56 / 60, 30     16 tiles 48 / 51 / 65, 36
+//              N = 36000:          59 / 83 / 90, 48              49 / 52 / 67, 38
+//              N = 65536:          82 / 122 / 117, 62            60 / 65 / 75, 47
+//   32 tokens, N = 36000:          32 / 41 / 62, 30              33 / 34 / 42, 29
+//              N = 65536:          47 / 56 / 84, 41              43 / 44 / 48, 39
 constexpr int kW4WideWork = 1024;    // row tiles x passes of 16 tokens from which w4_wide is taken
 constexpr int kW4WideTiles = 2049;   // row tiles from which its blocks have 16
 constexpr int kW4WideTiles32 = 2800; // the same up to 32 tokens
@@ -545,9 +553,9 @@ __global__ __launch_bounds__(64 * W) void w4_wide(W4Args a) {
   // Both steps of a slice are multiplied, also where the last has one: the missing one's codes,
   // parameters and tokens are zeros, and without a branch between them the compiler runs the
   // second's loads and products into the first's (N = 12288, K = 4096, 24 tokens: INT4 in
-  // groups of 64 19.8 -> 17.4 us, MXFP4 14.5 -> 13.6).  Blocks of 16 row tiles gain nothing
-  // or run out of registers (INT4 in groups of 128, N = 65536, 64 tokens: 67 -> 73 us), and so
-  // does INT4 in groups of 32 with 64 tokens (39 -> 142).
+  // groups of 64 20.7 -> 18.2 us, MXFP4 15.5 -> 14.6).  Blocks of 16 row tiles gain nothing
+  // or run out of registers (INT4 in groups of 128, N = 65536, 64 tokens: 60 -> 68 us), and so
+  // does INT4 in groups of 32 with 64 tokens (42 -> 155).
   constexpr bool BOTH = R == 1 && !(FMT == W_INT4 && G == 32 && NT > 2);
   constexpr int ROWS = 16 * NT, LD = 512 + 16;
   constexpr int PIECES = ROWS * 32 / (64 * W);  // 16-byte pieces of a slice per thread
