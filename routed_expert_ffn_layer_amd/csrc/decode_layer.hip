@@ -20,9 +20,10 @@
 // ascending j), so results are the same on every run.
 //
 // Measured: bf16 layer (H = 2048, I = 512, 8 of 256 experts and a shared one) of 16 tokens
-// 85 + 42 us, 645 MB, 5.1 TB/s; of one token 12.5 + 7.2 us for 57 MB, about 6 us of the
+// 85 + 42 us, 645 MB, 5.1 TB/s; of one token 13.0 + 7.3 us for 57 MB, about 6 us of the
 // first kernel before its first weights; MXFP4 layer (H = 4096, I = 2048, 6 of 256) of 64 tokens
-// 101 + 65 us, 20 us of the first kernel for routing and first weights.
+// 103 + 66 us, 20 us of the first kernel for routing and first weights (the separate calls take
+// 145 us for the whole layer there: they read W13 once per 32 tokens).
 #include "kernels.hpp"
 #include "stream_tile.hpp"
 

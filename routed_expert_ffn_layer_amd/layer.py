@@ -68,7 +68,8 @@ def forward_decode(b: LayerBuffers, logits, x, slot_pool, slot_stride, slot_of_e
     """The layer of `forward` for a few tokens (T <= 64, T*k <= 512, bf16 or MXFP4
     weights) in one library call of two kernels; b.topk_ids and b.topk_w are written,
     or with logits None read as the routing.  The permutation and the expert rows of
-    b are not touched."""
+    b are not touched.  From about 40 tokens of MXFP4 experts `forward` is the faster of
+    the two (64 tokens, hidden 4096: 145 us against 160)."""
     moe.moe_layer_decode(b.wdt, slot_pool, slot_stride, slot_of_expert, shared_w,
                          b.I_shared if shared_w is not None else 0, x, logits, b.T, b.k, b.E, b.H, b.I, b.topk_ids,
                          b.topk_w, b.y, b.ydt, b.workspace, stream)

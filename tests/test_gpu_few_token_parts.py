@@ -227,3 +227,25 @@ def test_every_row_past_4_gib(fmt, group, T):
     """More than 2^32 bytes of codes: every output, not those of a few rows."""
     y, ref = _product(fmt, group, T, 70000, 131072)
     assert torch.equal(y.double(), ref)
+
+
+@pytest.mark.parametrize("T", [1, 7, 16, 40])
+def test_e8m0_scales_at_the_ends(T):
+    """E2M1 times 2^(scale - 127) is exact from the smallest scale (a bf16 subnormal of two bits) up, infinite
+    from 2^128 on, and NaN for 255; one product an output, so each is exact."""
+    N, K = 16, 64
+    mags = _E2M1[:8]
+    for s in (0, 1, 2, 127, 252, 253, 254, 255):
+        codes = torch.zeros((N, K // 2), dtype=torch.uint8, device=dev())
+        codes[:8, 0] = torch.arange(8, device=dev()).to(torch.uint8)
+        scales = torch.full((N, 2), s, dtype=torch.uint8, device=dev())
+        scales[:, 1] = 127
+        w = torch.empty(moe.moe_w4_bytes(moe.MOE_MXFP4, N, K, 32), dtype=torch.uint8, device=dev())
+        moe.moe_w4_pack(moe.MOE_MXFP4, codes, scales, None, N, K, 32, w)
+        x = torch.zeros((T, K), dtype=torch.bfloat16, device=dev())
+        x[:, 0] = 2.0 ** -20 if s > 200 else 2.0 ** 20
+        y = torch.empty((T, N), device=dev())
+        moe.moe_w4_linear(moe.MOE_MXFP4, w, N, K, 32, x, None, y)
+        wv = mags * 2.0 ** (s - 127) if s < 255 else torch.full((8,), float("nan"), dtype=torch.float64)
+        wv = torch.where(wv >= 2.0 ** 128, float("inf"), wv)
+        torch.testing.assert_close(y[:, :8].double().cpu(), (wv * float(x[0, 0])).expand(T, 8), rtol=0, atol=0, equal_nan=True)
