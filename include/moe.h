@@ -420,9 +420,10 @@ int moe_layer_decode(int wdt, const void* slot_pool, size_t slot_stride, const i
  * overlapping x; bias [N] f32 or NULL.  0 <= T <= 2^19: the weights are read once for up to 16
  * tokens, or (many rows) 64, and again for every such batch.  Products are exact, sums
  * are in f32 in a fixed order, one rounding to ydt.  MOE_INT4 sums s (sum x q - z sum x)
- * group by group; where that comes out infinite or NaN (an infinite x, or x so large that
- * a sum with the codes alone passes the f32 range) the output is formed again as sum s (q - z) x in
- * ascending k, so it is the definition's for every x; the tokens concerned take longer.
+ * group by group, so its roundings are relative to the magnitudes s (q + z) |x|; where that comes
+ * out infinite or NaN (an infinite x, or x so large that a sum with the codes alone passes the f32
+ * range) the output is formed again as the f32 sum of s (q - z) x in ascending k: an infinite x gives the
+ * infinity of its products' sign, NaN where q = z.  Tokens concerned take longer.
  * Asynchronous, no workspace. */
 enum { MOE_INT4 = 4 };
 size_t moe_w4_bytes(int fmt, int N, int K, int group);
