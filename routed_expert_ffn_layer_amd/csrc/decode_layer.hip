@@ -38,9 +38,11 @@ constexpr int kDlHalfTiles = 128;  // row tiles of W2 up to which the down kerne
 // significant bits), larger batches round it to bf16.  One rounding of h costs y as much
 // as y's own rounding to bf16 (an RMS error of 0.0024 instead of 0.0017); the remainder rides in
 // operand rows that a few tokens leave empty, but doubles the h loads that bound the down
-// products of many (MXFP4, h in one and in two parts: 28.2 and 28.9 us a layer at one token,
-// 65 and 70 at 8; with the limit at 64 a layer of 16, 32 and 64 tokens goes from 82, 100
-// and 165 us to 89, 117 and 194).
+// products of many.  MXFP4, h in one and in two parts: 28.2 and 28.9 us a layer at one token,
+// 65 and 70 at 8.  With the limit at 32, over eight shapes (H 256 to 7168, 16 to 256 experts), a layer
+// of 9 / 16 / 32 tokens takes 2-12 / 3-14 / 5-20% longer in MXFP4 and 0-2 / 0-5 / 0-13% in bf16 (least where
+// 256 experts keep HBM busy: 129.6 and 130.2 us at 16 tokens of H = 2048, I = 512, most at H = 7168, I = 2048:
+// 491 and 516, 640 and 723 at 32).  Above the limit y has the precision of the separate calls.
 constexpr int kDlSplitT = 8;
 
 // A run: pairs of one expert (or tokens of the shared expert) that one matrix tile serves.
