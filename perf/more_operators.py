@@ -237,13 +237,10 @@ def _run_own(s):
         moe.moe_block_norm(s["block"], post, s["gate"], 0.7, s["res"], 0.9, pre, EPS, s["res_out"], s["x"])
         return (s["res_out"], s["x"]) if c["pre"] else s["res_out"]
     if c["op"] == "linear":
-        if "ws" not in s:  # as a program that calls the product again and again keeps it
-            n = moe.moe_linear_workspace(c["dt"], c["T"], c["N"], c["K"])
-            s["ws"] = torch.empty(n, dtype=torch.uint8, device=s["x"].device)
-        moe.moe_linear(s["w"], s["x"], s["bias"], ACTS.index(c["act"]), s["res"], s["y"], s["ws"])
+        moe.moe_linear(s["w"], s["x"], s["bias"], ACTS.index(c["act"]), s["res"], s["y"])
         return s["y"]
     if c["way"] == "forward":
-        if "ws" not in s:
+        if "ws" not in s:  # as a program that dispatches again and again keeps it
             n = moe.moe_dispatch_workspace(c["T"], c["k"], c["E"])
             s["ws"] = torch.empty(n, dtype=torch.uint8, device=s["x"].device)
         moe.moe_dispatch(s["x"], s["ids"], c["E"], s["counts"], s["offsets"], s["sorted"], s["inv"], s["rows"], s["ws"])
