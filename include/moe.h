@@ -14,6 +14,10 @@
  *   moe_layer_decode       all of the above for a few tokens in two kernels
  *   moe_layer_stream_*     whole-layer double buffering for prefill
  *   moe_w4_linear          linear product with 4-bit weights and group scales
+ *   moe_linear             linear product with f32 or bf16 weights, bias, activation and residual
+ *   moe_block_norm         norms before and after a block with its gate and residual
+ *   moe_dispatch           token rows sorted by expert; moe_combine_rows: and back, with weights;
+ *                          their gradients and the gate's: moe_..._backward
  *
  * Conventions
  *  - Pointers are device pointers unless the name ends in _host.
@@ -431,6 +435,91 @@ int moe_w4_pack(int fmt, const uint8_t* codes, const void* scales, const uint8_t
                 void* w, hipStream_t stream);
 int moe_w4_linear(int fmt, const void* w, int N, int K, int group, const void* x, int64_t x_ld, int T,
                   const float* bias, void* y, int64_t y_ld, int ydt, hipStream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Linear product with f32 or bf16 weights, for the dense products around the experts
+ * (projections, a dense feed-forward part, a head) of a model whose weights are not 4-bit.
+ *     y[t][n] = act( sum_k x[t][k] * w[n][k] + bias[n] ) + res[t][n]
+ *   wdt   type of w and x: MOE_BF16 or MOE_F32 (MOE_EUNSUPPORTED otherwise)
+ *   w     N rows of K, w_ld elements apart, as a checkpoint holds them: no packing
+ *   x     T rows of K, x_ld elements apart
+ *   bias  [N] f32 or NULL
+ *   act   SiLU z / (1 + e^-z); GELU z P(Z <= z) of a normal Z; GELU_TANH its form with
+ *         tanh( sqrt(2 / pi) (z + 0.044715 z^3) )
+ *   res   T rows of N of rdt, r_ld apart, or NULL; may be y itself (same start, type and stride)
+ *   y     T rows of N of ydt, y_ld apart; apart from that overlaps no operand (MOE_EINVAL)
+ * K, w_ld and x_ld multiples of 8 (bf16) or 4 (f32), K <= 2^20, w_ld and x_ld <= 2^21; y_ld and r_ld
+ * any; T and N at most 2^22, T * N at most 2^35.  Products of bf16 are exact, sums are in f32 in an
+ * order that the shape fixes, bias, activation and residual are applied in f32 before the one
+ * rounding to ydt; f32 weights are multiplied in f32.  The erf inside GELU is within 1.5e-7.
+ * Asynchronous, no workspace, may be captured into a graph. */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4 };
+int moe_linear(int wdt, const void* w, int64_t w_ld, int N, int K, const void* x, int64_t x_ld, int T,
+               const float* bias, int act, const void* res, int rdt, int64_t r_ld, void* y, int ydt, int64_t y_ld,
+               hipStream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* The boundary of two blocks (attention, this layer, a dense part) in one call: the norm after
+ * a block, its gate, the residual sum, and the norm before the next block.
+ *     n = norm_post(block[t]);  r' = res_scale * res[t] + block_scale * gate * n;  x[t] = norm_pre(r')
+ *     norm RMS:   v / sqrt(mean(v^2) + eps) * w (+ b);  LAYER: (v - mean(v)) / sqrt(var(v) + eps) * w (+ b)
+ *   block    T rows of H of bdt, b_ld apart; NULL: nothing is added to res (the first norm of a model)
+ *   gate     of gdt: [H] for every token (gate_ld 0) or T rows gate_ld apart; NULL: 1
+ *   res      T rows of H of rdt, r_ld apart; NULL: no residual
+ *   post_w, post_b, pre_w, pre_b   [H] f32; NULL: 1 and 0
+ *   res_out  T rows of rdt, ro_ld apart, receives r'; NULL: not wanted
+ *   x        T rows of xdt, x_ld apart; NULL: no next norm.  Of the f32 r', not of its rounding
+ * Results may lie on block, res or a gate of T rows where start, type and stride agree (in place);
+ * any other overlap is refused, as far as the addresses show it.  1 <= H <= 32768 (MOE_EUNSUPPORTED
+ * beyond), T <= 2^21, strides any from H on, eps >= 0.  Statistics in f32, exact to its rounding over
+ * the whole range of the types.  Asynchronous, no workspace, may be captured. */
+enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 };
+int moe_block_norm(const void* block, int bdt, int64_t b_ld, int post_kind, const float* post_w, const float* post_b,
+                   const void* gate, int gdt, int64_t gate_ld, float block_scale, const void* res, int64_t r_ld,
+                   float res_scale, int pre_kind, const float* pre_w, const float* pre_b, float eps, int T, int H,
+                   void* res_out, int rdt, int64_t ro_ld, void* x, int xdt, int64_t x_ld, hipStream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Tokens sorted by expert and back, for experts that are not moe_grouped_ffn's (products of
+ * the caller, other devices), and the gradients for training a router or such experts.
+ *
+ * moe_dispatch: permutation and token rows in one call.  counts, offsets, sorted_rows and inv_rows as
+ * moe_permute, except that ids outside [0, E) are allowed: such pairs go to no expert (an expert shard,
+ * a capacity limit), inv_rows is -1 for them, offsets[E] counts the others, and sorted_rows holds -1
+ * from there on.  Then rows[p] = x[sorted_rows[p] / k] for p < min(offsets[E], n_rows); rows behind
+ * are left as they were.  x and rows of xdt (MOE_F32 or MOE_BF16), x_ld and rows_ld apart (any from H on).
+ * workspace >= moe_dispatch_workspace() bytes (0 for few pairs: NULL is fine then), written by the call.
+ *
+ * moe_combine_rows: y[t] = sum_j topk_w[t][j] * rows[inv_rows[t*k+j]], j ascending, in f32, one rounding
+ * to ydt.  Pairs whose place is negative or n_rows and beyond contribute nothing; a token without
+ * any gets zeros.  Unlike moe_combine, rows may be bf16, strided and fewer than T*k.
+ *
+ * moe_combine_rows_backward: from dy, for every pair with a place p in [0, n_rows), t its token:
+ *     d_rows[p] = topk_w[t][j] * dy[t]  (of rdt),  d_topk_w[t][j] = sum_h dy[t][h] * rows[p][h]  (f32)
+ * and d_topk_w = 0 for the other pairs; rows of d_rows that no pair has are left as they were.  d_rows
+ * may be rows itself (same start and stride).  No place may occur twice in inv_rows.
+ *
+ * moe_dispatch_backward: dx[t] = sum_j d_rows[inv_rows[t*k+j]], as moe_combine_rows with weights of 1.
+ *
+ * moe_gate_backward: gradient of the softmax over the selected logits (moe_route_topk's weights):
+ *     d_logits[t][e] = sum over j with topk_ids[t][j] = e of w_j (d_w_j - sum_i w_i d_w_i)
+ * for all e (0 where e was not selected; the selection itself has no gradient); [T][E] f32.
+ *
+ * All: 0 <= T <= 2^21, 1 <= k <= 32, H any positive up to 2^24.  No atomics on results: the same inputs give the
+ * same bits.  Asynchronous, may be captured (two calls that may overlap need a workspace each). */
+size_t moe_dispatch_workspace(int T, int k, int E);
+int moe_dispatch(const void* x, int xdt, int64_t x_ld, const int32_t* topk_ids, int T, int k, int E, int H,
+                 int32_t* counts, int32_t* offsets, int32_t* sorted_rows, int32_t* inv_rows, void* rows,
+                 int64_t rows_ld, int n_rows, void* workspace, size_t ws_bytes, hipStream_t stream);
+int moe_dispatch_backward(const void* d_rows, int rdt, int64_t dr_ld, int n_rows, const int32_t* inv_rows, int T,
+                          int k, int H, void* dx, int xdt, int64_t dx_ld, hipStream_t stream);
+int moe_combine_rows(const void* rows, int rdt, int64_t rows_ld, int n_rows, const float* topk_w,
+                     const int32_t* inv_rows, int T, int k, int H, void* y, int ydt, int64_t y_ld, hipStream_t stream);
+int moe_combine_rows_backward(const void* dy, int ydt, int64_t dy_ld, const void* rows, int rdt, int64_t rows_ld,
+                              int n_rows, const float* topk_w, const int32_t* inv_rows, int T, int k, int H,
+                              void* d_rows, int64_t dr_ld, float* d_topk_w, hipStream_t stream);
+int moe_gate_backward(const int32_t* topk_ids, const float* topk_w, const float* d_topk_w, int T, int E, int k,
+                      float* d_logits, hipStream_t stream);
 
 /* ------------------------------------------------------------------------- */
 /* Whole-layer streaming for prefill.  The pages: in prefill, whole layers are

@@ -348,6 +348,318 @@ int moe_w4_linear(int fmt, const void* w, int N, int K, int group, const void* x
 }
 
 // ---------------------------------------------------------------------------
+namespace {
+
+bool is_float_type(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
+
+// Tokens of the row operators: their grids stay under 2^32 threads.
+constexpr int kMaxRowTokens = 1 << 21;
+
+// Rows of `width` elements, ld apart, that must hold their width and be 16-byte aligned at the first.
+int check_rows(const void* p, int64_t ld, int width, const char* what) {
+  if (!p) return fail(MOE_EINVAL, "%s must not be null", what);
+  if (!aligned16(p)) return fail(MOE_EINVAL, "%s must be 16-byte aligned", what);
+  if (ld < width) return fail(MOE_EINVAL, "%s: rows %lld elements apart, each of %d", what, (long long)ld, width);
+  return MOE_OK;
+}
+
+// A result on the memory of an input is allowed where both are the same rows: same start, type and stride.
+struct Span {
+  const void* p;
+  int64_t ld;
+  int rows, width, dt;
+};
+bool overlaps(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+  auto bytes = [](const Span& s) { return (uint64_t)((s.rows - 1) * s.ld + s.width) * (s.dt == MOE_F32 ? 4 : 2); };
+  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+  if (a0 >= b0 + bytes(b) || b0 >= a0 + bytes(a)) return false;
+  // columns of one buffer: the same distance between rows, apart from each other inside it
+  const uint64_t ea = a.dt == MOE_F32 ? 4 : 2, eb = b.dt == MOE_F32 ? 4 : 2, step = a.ld * ea;
+  if (a.rows > 1 && b.rows > 1 && step == b.ld * eb) {
+    const uint64_t d = b0 >= a0 ? (b0 - a0) % step : (step - (a0 - b0) % step) % step;
+    return !(d >= a.width * ea && d + b.width * eb <= step);
+  }
+  return true;
+}
+bool same_rows(const Span& a, const Span& b) {
+  return a.p == b.p && a.dt == b.dt && (a.ld == b.ld || a.rows <= 1);
+}
+
+}  // namespace
+
+int moe_block_norm(const void* block, int bdt, int64_t b_ld, int post_kind, const float* post_w, const float* post_b,
+                   const void* gate, int gdt, int64_t gate_ld, float block_scale, const void* res, int64_t r_ld,
+                   float res_scale, int pre_kind, const float* pre_w, const float* pre_b, float eps, int T, int H,
+                   void* res_out, int rdt, int64_t ro_ld, void* x, int xdt, int64_t x_ld, hipStream_t stream) {
+  const CallRange range_(__func__);
+  REQUIRE(T >= 0 && T <= kMaxRowTokens, "moe_block_norm: T=%d must be in [0, 2^21]", T);
+  REQUIRE(H > 0, "moe_block_norm: H=%d must be positive", H);
+  if (H > moe::kBlockNormMaxH)
+    return fail(MOE_EUNSUPPORTED, "moe_block_norm: H=%d > %d", H, moe::kBlockNormMaxH);
+  REQUIRE(post_kind >= MOE_NORM_NONE && post_kind <= MOE_NORM_LAYER && pre_kind >= MOE_NORM_NONE &&
+              pre_kind <= MOE_NORM_LAYER, "moe_block_norm: unknown kind of norm (%d, %d)", post_kind, pre_kind);
+  REQUIRE(is_float_type(rdt), "moe_block_norm: rdt must be MOE_F32 or MOE_BF16");
+  REQUIRE(!block || is_float_type(bdt), "moe_block_norm: bdt must be MOE_F32 or MOE_BF16");
+  REQUIRE(!x || is_float_type(xdt), "moe_block_norm: xdt must be MOE_F32 or MOE_BF16");
+  REQUIRE(!gate || is_float_type(gdt), "moe_block_norm: gdt must be MOE_F32 or MOE_BF16");
+  REQUIRE(eps >= 0.0f && eps < 1e30f, "moe_block_norm: eps must be in [0, 1e30)");
+  if (T == 0) return MOE_OK;
+  REQUIRE(block || res, "moe_block_norm: neither block nor res");
+  REQUIRE(res_out || x, "moe_block_norm: neither res_out nor x");
+  REQUIRE(block || (post_kind == MOE_NORM_NONE && !gate), "moe_block_norm: a post norm or gate without a block");
+  REQUIRE(post_kind != MOE_NORM_NONE || (!post_w && !post_b), "moe_block_norm: post weights without a post norm");
+  REQUIRE(x || pre_kind == MOE_NORM_NONE, "moe_block_norm: a pre norm without x");
+  REQUIRE(pre_kind != MOE_NORM_NONE || (!pre_w && !pre_b), "moe_block_norm: pre weights without a pre norm");
+  if (block)
+    if (int rc = check_rows(block, b_ld, H, "block")) return rc;
+  if (res)
+    if (int rc = check_rows(res, r_ld, H, "res")) return rc;
+  if (gate)
+    if (int rc = check_rows(gate, gate_ld == 0 ? H : gate_ld, H, "gate")) return rc;
+  if (res_out)
+    if (int rc = check_rows(res_out, ro_ld, H, "res_out")) return rc;
+  if (x)
+    if (int rc = check_rows(x, x_ld, H, "x")) return rc;
+  for (const float* p : {post_w, post_b, pre_w, pre_b}) REQUIRE(aligned16(p), "moe_block_norm: norm weights must be 16-byte aligned");
+  const Span sb{block, b_ld, T, H, bdt}, sr{res, r_ld, T, H, rdt}, so{res_out, ro_ld, T, H, rdt}, sx{x, x_ld, T, H, xdt},
+      sg{gate, gate_ld, gate_ld ? T : 1, H, gdt};
+  REQUIRE(!overlaps(so, sx), "moe_block_norm: res_out and x overlap");
+  for (const Span& in : {sb, sr, sg})
+    for (const Span& out : {so, sx})
+      REQUIRE(!overlaps(in, out) || (same_rows(in, out) && (in.p != gate || gate_ld)),
+              "moe_block_norm: a result overlaps an input without being the same rows");
+  for (const float* p : {post_w, post_b, pre_w, pre_b})
+    for (const Span& out : {so, sx}) REQUIRE(!overlaps(Span{p, H, 1, H, MOE_F32}, out), "moe_block_norm: a result overlaps norm weights");
+  moe::BlockNormArgs a;
+  a.block = block;
+  a.post_w = post_w;
+  a.post_b = post_b;
+  a.gate = gate;
+  a.res = res;
+  a.pre_w = pre_w;
+  a.pre_b = pre_b;
+  a.res_out = res_out;
+  a.x = x;
+  a.b_ld = b_ld;
+  a.gate_ld = gate_ld;
+  a.r_ld = r_ld;
+  a.ro_ld = ro_ld;
+  a.x_ld = x_ld;
+  a.block_scale = block_scale;
+  a.res_scale = res_scale;
+  a.eps = eps;
+  a.T = T;
+  a.H = H;
+  a.post_kind = post_kind;
+  a.pre_kind = pre_kind;
+  a.gate_bf16 = gdt == MOE_BF16;
+  hipError_t e = moe::launch_block_norm(a, bdt == MOE_BF16, rdt == MOE_BF16, xdt == MOE_BF16, stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_block_norm launch");
+}
+
+int moe_linear(int wdt, const void* w, int64_t w_ld, int N, int K, const void* x, int64_t x_ld, int T,
+               const float* bias, int act, const void* res, int rdt, int64_t r_ld, void* y, int ydt, int64_t y_ld,
+               hipStream_t stream) {
+  const CallRange range_(__func__);
+  if (wdt != MOE_F32 && wdt != MOE_BF16)
+    return fail(MOE_EUNSUPPORTED, "moe_linear: weights are MOE_F32 or MOE_BF16 (4-bit ones: moe_w4_linear)");
+  const int q = wdt == MOE_F32 ? 4 : 8;  // elements in 16 bytes
+  REQUIRE(T >= 0 && T <= 1 << 22 && N > 0 && N <= 1 << 22 && (int64_t)T * N <= (int64_t)1 << 35,
+          "moe_linear: T=%d, N=%d (each at most 2^22, together 2^35)", T, N);
+  REQUIRE(K > 0 && K % q == 0 && K <= 1 << 20, "moe_linear: K=%d must be a positive multiple of %d, at most 2^20", K, q);
+  REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH, "moe_linear: unknown activation %d", act);
+  REQUIRE(is_float_type(ydt), "moe_linear: ydt must be MOE_F32 or MOE_BF16");
+  REQUIRE(!res || is_float_type(rdt), "moe_linear: rdt must be MOE_F32 or MOE_BF16");
+  if (T == 0) return MOE_OK;
+  if (int rc = check_rows(w, w_ld, K, "w")) return rc;
+  if (int rc = check_rows(x, x_ld, K, "x")) return rc;
+  REQUIRE(w_ld % q == 0 && w_ld <= 1 << 21 && x_ld % q == 0 && x_ld <= 1 << 21,
+          "moe_linear: rows of w and x %lld and %lld apart (multiples of %d, at most 2^21)", (long long)w_ld,
+          (long long)x_ld, q);
+  if (int rc = check_rows(y, y_ld, N, "y")) return rc;
+  if (res)
+    if (int rc = check_rows(res, r_ld, N, "res")) return rc;
+  if (bias) REQUIRE_PTR(bias);
+  const Span sy{y, y_ld, T, N, ydt}, sres{res, r_ld, T, N, rdt};
+  REQUIRE(!overlaps(sy, Span{w, w_ld, N, K, wdt}) && !overlaps(sy, Span{x, x_ld, T, K, wdt}) &&
+              !overlaps(sy, Span{bias, N, 1, N, MOE_F32}), "moe_linear: y overlaps w, x or bias");
+  REQUIRE(!overlaps(sy, sres) || same_rows(sy, sres), "moe_linear: y overlaps res without being the same rows");
+  moe::LinearArgs a;
+  a.w = w;
+  a.x = x;
+  a.bias = bias;
+  a.res = res;
+  a.y = y;
+  a.w_ld = w_ld;
+  a.x_ld = x_ld;
+  a.r_ld = r_ld;
+  a.y_ld = y_ld;
+  a.T = T;
+  a.N = N;
+  a.K = K;
+  a.act = act;
+  a.res_bf16 = rdt == MOE_BF16;
+  a.y_bf16 = ydt == MOE_BF16;
+  hipError_t e = moe::launch_linear(wdt == MOE_BF16, a, stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_linear launch");
+}
+
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_pairs(int T, int k, int H, int n_rows, const char* what) {
+  if (T < 0 || T > kMaxRowTokens) return fail(MOE_EINVAL, "%s: T=%d must be in [0, 2^21]", what, T);
+  if (k < 1 || k > 32) return fail(MOE_EINVAL, "%s: k=%d must be in [1, 32]", what, k);
+  if (H < 1 || H > 1 << 24) return fail(MOE_EINVAL, "%s: H=%d must be in [1, 2^24]", what, H);
+  if (n_rows < 0) return fail(MOE_EINVAL, "%s: n_rows=%d < 0", what, n_rows);
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_dispatch_workspace(int T, int k, int E) {
+  const CallRange range_(__func__);
+  if (check_routing(T, E, k) || T > kMaxRowTokens) return 0;
+  return moe::dispatch_workspace_bytes(T, k, E);
+}
+
+int moe_dispatch(const void* x, int xdt, int64_t x_ld, const int32_t* topk_ids, int T, int k, int E, int H,
+                 int32_t* counts, int32_t* offsets, int32_t* sorted_rows, int32_t* inv_rows, void* rows,
+                 int64_t rows_ld, int n_rows, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  const CallRange range_(__func__);
+  if (int rc = check_routing(T, E, k)) return rc;
+  if (int rc = check_pairs(T, k, H, n_rows, "moe_dispatch")) return rc;
+  REQUIRE(is_float_type(xdt), "moe_dispatch: xdt must be MOE_F32 or MOE_BF16");
+  REQUIRE_PTR(counts);
+  REQUIRE_PTR(offsets);
+  if (T > 0) {
+    REQUIRE_PTR(topk_ids);
+    REQUIRE_PTR(sorted_rows);
+    REQUIRE_PTR(inv_rows);
+    if (int rc = check_rows(x, x_ld, H, "x")) return rc;
+    if (n_rows > 0) {
+      if (int rc = check_rows(rows, rows_ld, H, "rows")) return rc;
+      REQUIRE(!overlaps(Span{x, x_ld, T, H, xdt}, Span{rows, rows_ld, n_rows, H, xdt}), "moe_dispatch: rows overlap x");
+    }
+  }
+  const size_t need = moe::dispatch_workspace_bytes(T, k, E);
+  if (need) REQUIRE_PTR(workspace);
+  if (ws_bytes < need) return fail(MOE_ECAPACITY, "moe_dispatch: workspace %zu bytes < %zu needed", ws_bytes, need);
+  moe::DispatchArgs a;
+  a.x = x;
+  a.ids = topk_ids;
+  a.counts = counts;
+  a.offsets = offsets;
+  a.sorted_rows = sorted_rows;
+  a.inv_rows = inv_rows;
+  a.rows = rows;
+  a.x_ld = x_ld;
+  a.rows_ld = rows_ld;
+  a.T = T;
+  a.k = k;
+  a.E = E;
+  a.H = H;
+  a.n_rows = n_rows;
+  hipError_t e = moe::launch_dispatch(a, static_cast<int32_t*>(workspace), xdt == MOE_BF16, stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_dispatch launch");
+}
+
+namespace {
+
+int combine_rows(const void* rows, int rdt, int64_t rows_ld, int n_rows, const float* topk_w, const int32_t* inv_rows,
+                 int T, int k, int H, void* y, int ydt, int64_t y_ld, hipStream_t stream, const char* what) {
+  if (int rc = check_pairs(T, k, H, n_rows, what)) return rc;
+  REQUIRE(is_float_type(rdt) && is_float_type(ydt), "%s: rows and results are MOE_F32 or MOE_BF16", what);
+  if (T == 0) return MOE_OK;
+  if (n_rows > 0)
+    if (int rc = check_rows(rows, rows_ld, H, "rows")) return rc;
+  REQUIRE_PTR(inv_rows);
+  if (int rc = check_rows(y, y_ld, H, "y")) return rc;
+  REQUIRE(!overlaps(Span{rows, rows_ld, n_rows, H, rdt}, Span{y, y_ld, T, H, ydt}), "%s: the result overlaps the rows", what);
+  moe::CombineRowsArgs a = {};
+  a.rows = rows;
+  a.topk_w = topk_w;
+  a.inv_rows = inv_rows;
+  a.y = y;
+  a.rows_ld = rows_ld;
+  a.y_ld = y_ld;
+  a.T = T;
+  a.k = k;
+  a.H = H;
+  a.n_rows = n_rows;
+  hipError_t e = moe::launch_combine_rows(a, rdt == MOE_BF16, ydt == MOE_BF16, stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, what);
+}
+
+}  // namespace
+
+int moe_dispatch_backward(const void* d_rows, int rdt, int64_t dr_ld, int n_rows, const int32_t* inv_rows, int T,
+                          int k, int H, void* dx, int xdt, int64_t dx_ld, hipStream_t stream) {
+  const CallRange range_(__func__);
+  return combine_rows(d_rows, rdt, dr_ld, n_rows, nullptr, inv_rows, T, k, H, dx, xdt, dx_ld, stream,
+                      "moe_dispatch_backward");
+}
+
+int moe_combine_rows(const void* rows, int rdt, int64_t rows_ld, int n_rows, const float* topk_w,
+                     const int32_t* inv_rows, int T, int k, int H, void* y, int ydt, int64_t y_ld, hipStream_t stream) {
+  const CallRange range_(__func__);
+  if (T > 0) REQUIRE_PTR(topk_w);
+  return combine_rows(rows, rdt, rows_ld, n_rows, topk_w, inv_rows, T, k, H, y, ydt, y_ld, stream, "moe_combine_rows");
+}
+
+int moe_combine_rows_backward(const void* dy, int ydt, int64_t dy_ld, const void* rows, int rdt, int64_t rows_ld,
+                              int n_rows, const float* topk_w, const int32_t* inv_rows, int T, int k, int H,
+                              void* d_rows, int64_t dr_ld, float* d_topk_w, hipStream_t stream) {
+  const CallRange range_(__func__);
+  if (int rc = check_pairs(T, k, H, n_rows, "moe_combine_rows_backward")) return rc;
+  REQUIRE(is_float_type(rdt) && is_float_type(ydt), "moe_combine_rows_backward: dy and rows are MOE_F32 or MOE_BF16");
+  if (T == 0) return MOE_OK;
+  if (int rc = check_rows(dy, dy_ld, H, "dy")) return rc;
+  const Span sdy{dy, dy_ld, T, H, ydt}, sr{rows, rows_ld, n_rows, H, rdt}, sd{d_rows, dr_ld, n_rows, H, rdt};
+  if (n_rows > 0) {
+    if (int rc = check_rows(rows, rows_ld, H, "rows")) return rc;
+    if (int rc = check_rows(d_rows, dr_ld, H, "d_rows")) return rc;
+    REQUIRE(!overlaps(sd, sdy), "moe_combine_rows_backward: d_rows overlap dy");
+    REQUIRE(!overlaps(sd, sr) || same_rows(sd, sr), "moe_combine_rows_backward: d_rows overlap rows without being the same");
+  }
+  REQUIRE_PTR(topk_w);
+  REQUIRE_PTR(inv_rows);
+  REQUIRE_PTR(d_topk_w);
+  REQUIRE(d_topk_w != topk_w, "moe_combine_rows_backward: d_topk_w is topk_w");
+  moe::CombineRowsArgs a = {};
+  a.rows = rows;
+  a.topk_w = topk_w;
+  a.inv_rows = inv_rows;
+  a.y = const_cast<void*>(dy);
+  a.d_rows = d_rows;
+  a.d_w = d_topk_w;
+  a.rows_ld = rows_ld;
+  a.y_ld = dy_ld;
+  a.dr_ld = dr_ld;
+  a.T = T;
+  a.k = k;
+  a.H = H;
+  a.n_rows = n_rows;
+  hipError_t e = moe::launch_combine_rows_backward(a, ydt == MOE_BF16, rdt == MOE_BF16, stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_combine_rows_backward launch");
+}
+
+int moe_gate_backward(const int32_t* topk_ids, const float* topk_w, const float* d_topk_w, int T, int E, int k,
+                      float* d_logits, hipStream_t stream) {
+  const CallRange range_(__func__);
+  if (int rc = check_routing(T, E, k)) return rc;
+  REQUIRE(T <= kMaxRowTokens, "moe_gate_backward: T=%d must be at most 2^21", T);
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(topk_ids);
+  REQUIRE_PTR(topk_w);
+  REQUIRE_PTR(d_topk_w);
+  REQUIRE_PTR(d_logits);
+  hipError_t e = moe::launch_gate_backward(topk_ids, topk_w, d_topk_w, T, E, k, d_logits, stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_gate_backward launch");
+}
+
+// ---------------------------------------------------------------------------
 size_t moe_grouped_ffn_workspace(int T, int k, int E, int H, int I, int I_shared, int wdt) {
   const CallRange range_(__func__);
   (void)E;

@@ -93,4 +93,67 @@ hipError_t launch_w4_pack(int fmt, const uint8_t* codes, const void* scales, con
                           int group, uint8_t* w, hipStream_t st);
 hipError_t launch_w4_linear(int fmt, const W4Args& a, bool bf16_out, hipStream_t st);
 
+// The boundary of two blocks (block_norm.hip).
+enum NormKind { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
+struct BlockNormArgs {
+  const void* block;  // nullable
+  const float* post_w;
+  const float* post_b;
+  const void* gate;  // nullable; rows gate_ld apart (0: one row for every token)
+  const void* res;   // nullable
+  const float* pre_w;
+  const float* pre_b;
+  void* res_out;  // nullable
+  void* x;        // nullable
+  int64_t b_ld, gate_ld, r_ld, ro_ld, x_ld;
+  float block_scale, res_scale, eps;
+  int T, H, post_kind, pre_kind;
+  bool gate_bf16;
+};
+constexpr int kBlockNormMaxH = 32768;  // a row in the registers of 1024 threads, 32 elements each
+hipError_t launch_block_norm(const BlockNormArgs& a, bool block_bf16, bool res_bf16, bool x_bf16, hipStream_t st);
+
+// Linear product with bias, activation and residual (linear.hip); f32 or bf16 operands.
+enum Activation { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+struct LinearArgs {
+  const void* w;      // N rows of K, w_ld elements apart
+  const void* x;      // T rows of K, x_ld elements apart
+  const float* bias;  // [N] or null
+  const void* res;    // T rows of N, r_ld elements apart, or null
+  void* y;            // T rows of N, y_ld elements apart
+  int64_t w_ld, x_ld, r_ld, y_ld;
+  int T, N, K, act;
+  bool res_bf16, y_bf16;
+};
+hipError_t launch_linear(bool bf16, const LinearArgs& a, hipStream_t st);
+
+// Tokens sorted by expert and back, with the gradients (token_sort.hip).
+struct DispatchArgs {
+  const void* x;  // T rows of H, x_ld elements apart
+  const int32_t* ids;
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* sorted_rows;
+  int32_t* inv_rows;
+  void* rows;  // n_rows rows of H, rows_ld elements apart
+  int64_t x_ld, rows_ld;
+  int T, k, E, H, n_rows;
+};
+size_t dispatch_workspace_bytes(int T, int k, int E);
+hipError_t launch_dispatch(const DispatchArgs& a, int32_t* table, bool bf16, hipStream_t st);
+struct CombineRowsArgs {
+  const void* rows;       // n_rows rows of H, rows_ld elements apart
+  const float* topk_w;    // [T][k]; the forward sum: null for weights of 1
+  const int32_t* inv_rows;
+  void* y;                // T rows of H, y_ld elements apart (backward: dy, read)
+  void* d_rows;           // backward: n_rows rows of H, dr_ld elements apart
+  float* d_w;             // backward: [T][k]
+  int64_t rows_ld, y_ld, dr_ld;
+  int T, k, H, n_rows;
+};
+hipError_t launch_combine_rows(const CombineRowsArgs& a, bool rows_bf16, bool y_bf16, hipStream_t st);
+hipError_t launch_combine_rows_backward(const CombineRowsArgs& a, bool dy_bf16, bool rows_bf16, hipStream_t st);
+hipError_t launch_gate_backward(const int32_t* ids, const float* w, const float* d_w, int T, int E, int k,
+                                float* d_logits, hipStream_t st);
+
 }  // namespace moe

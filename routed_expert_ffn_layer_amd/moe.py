@@ -14,6 +14,8 @@ LIB_PATH = os.path.join(HERE, "lib", "libmoe.so")
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY, MOE_EHIP, MOE_ENOMEM, MOE_ESTATE = range(7)
 MOE_F32, MOE_BF16, MOE_MXFP4, MOE_MXFP4_A8, MOE_INT4 = 0, 1, 2, 3, 4
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
+MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_LAYER = range(3)
 MOE_LAYER_DECODE_MAX_T, MOE_LAYER_DECODE_MAX_PAIRS = 64, 512
 
 _lib = None
@@ -59,7 +61,9 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_last_error", "moe_expert_by
            "moe_cache_lookup_fill_inplace", "moe_cache_step_inplace", "moe_grouped_ffn_addr", "moe_route", "moe_cache_resize", "moe_route_project",
            "moe_grouped_ffn_workspace", "moe_grouped_ffn_kind", "moe_mx8_quantize", "moe_grouped_ffn", "moe_grouped_ffn_gate_up", "moe_grouped_ffn_down", "moe_grouped_ffn_noalloc",
            "moe_combine", "moe_layer_decode", "moe_layer_decode_workspace", "moe_w4_bytes", "moe_w4_pack",
-           "moe_w4_linear", "moe_layer_stream_create", "moe_layer_stream_destroy", "moe_layer_stream_fill",
+           "moe_w4_linear", "moe_linear", "moe_block_norm", "moe_dispatch_workspace", "moe_dispatch",
+           "moe_dispatch_backward", "moe_combine_rows", "moe_combine_rows_backward", "moe_gate_backward",
+           "moe_layer_stream_create", "moe_layer_stream_destroy", "moe_layer_stream_fill",
            "moe_layer_stream_acquire", "moe_layer_stream_release"]
 
 
@@ -71,7 +75,7 @@ def lib():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with routed_expert_ffn_layer_amd/build.py")
     L = ctypes.CDLL(LIB_PATH)
-    P, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    P, i, sz, l, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64, ctypes.c_float
     L.moe_abi_version.restype = i
     L.moe_status_str.restype = ctypes.c_char_p
     L.moe_status_str.argtypes = [i]
@@ -112,6 +116,15 @@ def lib():
     L.moe_w4_bytes.argtypes = [i, i, i, i]
     L.moe_w4_pack.argtypes = [i, P, P, P, i, i, i, P, P]
     L.moe_w4_linear.argtypes = [i, P, i, i, i, P, ctypes.c_int64, i, P, P, ctypes.c_int64, i, P]
+    L.moe_linear.argtypes = [i, P, l, i, i, P, l, i, P, i, P, i, l, P, i, l, P]
+    L.moe_block_norm.argtypes = [P, i, l, i, P, P, P, i, l, f, P, l, f, i, P, P, f, i, i, P, i, l, P, i, l, P]
+    L.moe_dispatch_workspace.restype = sz
+    L.moe_dispatch_workspace.argtypes = [i, i, i]
+    L.moe_dispatch.argtypes = [P, i, l, P, i, i, i, i, P, P, P, P, P, l, i, P, sz, P]
+    L.moe_dispatch_backward.argtypes = [P, i, l, i, P, i, i, i, P, i, l, P]
+    L.moe_combine_rows.argtypes = [P, i, l, i, P, P, i, i, i, P, i, l, P]
+    L.moe_combine_rows_backward.argtypes = [P, i, l, P, i, l, i, P, P, i, i, i, P, l, P, P]
+    L.moe_gate_backward.argtypes = [P, P, P, i, i, i, P, P]
     L.moe_layer_stream_create.argtypes = [ctypes.POINTER(LayerStreamDesc), ctypes.POINTER(P)]
     L.moe_layer_stream_destroy.argtypes = [P]
     L.moe_layer_stream_fill.argtypes = [P, i, i]
@@ -368,6 +381,167 @@ def moe_w4_linear(fmt, w, N, K, group, x, bias, y, stream=None):
     st = _stream_of(stream, w, x, bias, y)
     _check(lib().moe_w4_linear(fmt, w.data_ptr(), N, K, group, x.data_ptr(), x_ld, T, _ptr(bias), y.data_ptr(), y_ld, ydt,
                                st))
+
+
+def _code(t, name):
+    """Type code of a tensor whose elements are f32 or bf16."""
+    d = t.dtype
+    if d is _torch().bfloat16:
+        return MOE_BF16
+    if d is _torch_mod.float32:
+        return MOE_F32
+    raise MoeError(MOE_EINVAL, f"{name}: {d}, where float32 or bfloat16 is read")
+
+
+def _rows(t, name, rows, width, dt=None):
+    """(address, type code, distance between rows) of a [rows][width] tensor with unit stride along
+    its rows, (None, code of f32, width) of None."""
+    if t is None:
+        return None, MOE_F32, width
+    code = _code(t, name)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise MoeError(MOE_EINVAL, f"{name}: {tuple(t.shape)} with strides {t.stride()}, where [{rows}][{width}] with unit "
+                       "stride along the rows is used")
+    if dt is not None and code != dt:
+        raise MoeError(MOE_EINVAL, f"{name}: {t.dtype}, not the type that it has to agree with")
+    return t.data_ptr(), code, t.stride(0) if rows > 1 else width
+
+
+def moe_linear(w, x, bias, act, res, y, stream=None):
+    """y = act(x w^T + bias) + res.  w [N][K] and x [T][K] of one type (f32 or bf16); bias [N] f32 or None;
+    res [T][N] or None, y itself too; y [T][N] f32 or bf16; each with unit stride along its rows."""
+    if w.dim() != 2 or x.dim() != 2:
+        raise MoeError(MOE_EINVAL, f"w {tuple(w.shape)}, x {tuple(x.shape)}: matrices")
+    N, K = w.shape
+    T = x.shape[0]
+    wp, wdt, w_ld = _rows(w, "w", N, K)
+    xp, _, x_ld = _rows(x, "x", T, K, wdt)
+    rp, rdt, r_ld = _rows(res, "res", T, N)
+    yp, ydt, y_ld = _rows(y, "y", T, N)
+    if bias is not None:
+        _exactly(bias, "bias", "f32", 1, N)
+    st = _stream_of(stream, w, x, bias, res, y)
+    _check(lib().moe_linear(wdt, wp, w_ld, N, K, xp, x_ld, T, _ptr(bias), act, rp, rdt, r_ld, yp, ydt, y_ld, st))
+
+
+def _norm(norm, name, H):
+    """(kind, weight, bias) of a norm given as None, (kind, weight) or (kind, weight, bias)."""
+    if norm is None:
+        return MOE_NORM_NONE, None, None
+    kind, w, b = norm if len(norm) == 3 else (*norm, None)
+    if w is not None:
+        _exactly(w, name + " weight", "f32", 1, H)
+    if b is not None:
+        _exactly(b, name + " bias", "f32", 1, H)
+    return kind, w, b
+
+
+def moe_block_norm(block, post, gate, block_scale, res, res_scale, pre, eps, res_out, x, stream=None):
+    """r' = res_scale res + block_scale gate norm_post(block) -> res_out;  norm_pre(r') -> x.
+    block, res, res_out, x: [T][H] f32 or bf16 with unit stride along the rows, None where there is none
+    (res and res_out of one type); gate [H] or [T][H]; post and pre: None or (kind, weight, bias), [H] f32 each or None."""
+    first = block if block is not None else res
+    out = res_out if res_out is not None else x
+    if first is None or out is None:
+        raise MoeError(MOE_EINVAL, "neither block nor res" if first is None else "neither res_out nor x")
+    if first.dim() != 2:
+        raise MoeError(MOE_EINVAL, f"rows of {tuple(first.shape)}: a matrix")
+    T, H = first.shape
+    bp, bdt, b_ld = _rows(block, "block", T, H)
+    rp, rdt, r_ld = _rows(res, "res", T, H)
+    op, odt, o_ld = _rows(res_out, "res_out", T, H, rdt if res is not None else None)
+    xp, xdt, x_ld = _rows(x, "x", T, H)
+    if res is None:
+        rdt = odt
+    gp, gdt, g_ld = None, MOE_F32, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gp, gdt, _ = _rows(gate.unsqueeze(0), "gate", 1, H)
+        else:
+            gp, gdt, g_ld = _rows(gate, "gate", T, H)
+    post_kind, post_w, post_b = _norm(post, "post norm's", H)
+    pre_kind, pre_w, pre_b = _norm(pre, "pre norm's", H)
+    st = _stream_of(stream, block, post_w, post_b, gate, res, pre_w, pre_b, res_out, x)
+    _check(lib().moe_block_norm(bp, bdt, b_ld, post_kind, _ptr(post_w), _ptr(post_b), gp, gdt, g_ld, block_scale, rp, r_ld,
+                                res_scale, pre_kind, _ptr(pre_w), _ptr(pre_b), eps, T, H, op, rdt, o_ld, xp, xdt, x_ld,
+                                st))
+
+
+def moe_dispatch_workspace(T, k, E):
+    return int(lib().moe_dispatch_workspace(T, k, E))
+
+
+def _pairs(t, name, kind, T, k):
+    """Refuses t unless it is the [T][k] of the call, contiguous."""
+    if t is None or t.dtype not in _dtypes(kind) or not t.is_contiguous() or t.numel() != T * k:
+        raise MoeError(MOE_EINVAL, f"{name}: " + ("None" if t is None else f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+                       + f", where [{T}][{k}] of {kind} is used, contiguous")
+
+
+def moe_dispatch(x, topk_ids, E, counts, offsets, sorted_rows, inv_rows, rows, workspace=None, stream=None):
+    """Pairs sorted by expert (ids outside [0, E) to none) and x's rows at their places in rows.
+    x [T][H] and rows [n_rows][H] of one type; topk_ids [T][k]; workspace of moe_dispatch_workspace bytes."""
+    if x.dim() != 2 or topk_ids.dim() != 2 or rows.dim() != 2:
+        raise MoeError(MOE_EINVAL, f"x {tuple(x.shape)}, topk_ids {tuple(topk_ids.shape)}, rows {tuple(rows.shape)}: matrices")
+    (T, H), k, n_rows = x.shape, topk_ids.shape[1], rows.shape[0]
+    xp, xdt, x_ld = _rows(x, "x", T, H)
+    rp, _, r_ld = _rows(rows, "rows", n_rows, H, xdt)
+    _pairs(topk_ids, "topk_ids", "int32", T, k)
+    _pairs(sorted_rows, "sorted_rows", "int32", T, k)
+    _pairs(inv_rows, "inv_rows", "int32", T, k)
+    _exactly(counts, "counts", "int32", 1, E)
+    _exactly(offsets, "offsets", "int32", 1, E + 1)
+    _holds(workspace, "workspace", 0)
+    st = _stream_of(stream, x, topk_ids, counts, offsets, sorted_rows, inv_rows, rows, workspace)
+    _check(lib().moe_dispatch(xp, xdt, x_ld, _ptr(topk_ids), T, k, E, H, _ptr(counts), _ptr(offsets), _ptr(sorted_rows),
+                              _ptr(inv_rows), rp, r_ld, n_rows, _ptr(workspace),
+                              0 if workspace is None else workspace.numel() * workspace.element_size(), st))
+
+
+def moe_dispatch_backward(d_rows, inv_rows, k, dx, stream=None):
+    """dx [T][H] from the gradients d_rows [n_rows][H] of the dispatched rows."""
+    T, H = dx.shape
+    rp, rdt, r_ld = _rows(d_rows, "d_rows", d_rows.shape[0], H)
+    xp, xdt, x_ld = _rows(dx, "dx", T, H)
+    _pairs(inv_rows, "inv_rows", "int32", T, k)
+    st = _stream_of(stream, d_rows, inv_rows, dx)
+    _check(lib().moe_dispatch_backward(rp, rdt, r_ld, d_rows.shape[0], _ptr(inv_rows), T, k, H, xp, xdt, x_ld, st))
+
+
+def moe_combine_rows(rows, topk_w, inv_rows, y, stream=None):
+    """y [T][H] = sum over j of topk_w[t][j] rows[inv_rows[t][j]]; rows [n_rows][H]."""
+    (T, k), H = topk_w.shape, y.shape[-1]
+    rp, rdt, r_ld = _rows(rows, "rows", rows.shape[0], H)
+    yp, ydt, y_ld = _rows(y, "y", T, H)
+    _pairs(topk_w, "topk_w", "f32", T, k)
+    _pairs(inv_rows, "inv_rows", "int32", T, k)
+    st = _stream_of(stream, rows, topk_w, inv_rows, y)
+    _check(lib().moe_combine_rows(rp, rdt, r_ld, rows.shape[0], _ptr(topk_w), _ptr(inv_rows), T, k, H, yp, ydt, y_ld, st))
+
+
+def moe_combine_rows_backward(dy, rows, topk_w, inv_rows, d_rows, d_topk_w, stream=None):
+    """d_rows [n_rows][H] (of rows' type, rows itself too) and d_topk_w [T][k] from dy [T][H]."""
+    (T, k), H = topk_w.shape, dy.shape[-1]
+    yp, ydt, y_ld = _rows(dy, "dy", T, H)
+    rp, rdt, r_ld = _rows(rows, "rows", rows.shape[0], H)
+    dp, _, d_ld = _rows(d_rows, "d_rows", rows.shape[0], H, rdt)
+    _pairs(topk_w, "topk_w", "f32", T, k)
+    _pairs(inv_rows, "inv_rows", "int32", T, k)
+    _pairs(d_topk_w, "d_topk_w", "f32", T, k)
+    st = _stream_of(stream, dy, rows, topk_w, inv_rows, d_rows, d_topk_w)
+    _check(lib().moe_combine_rows_backward(yp, ydt, y_ld, rp, rdt, r_ld, rows.shape[0], _ptr(topk_w), _ptr(inv_rows), T, k,
+                                           H, dp, d_ld, _ptr(d_topk_w), st))
+
+
+def moe_gate_backward(topk_ids, topk_w, d_topk_w, d_logits, stream=None):
+    """d_logits [T][E] f32 from the gradient of the gate weights."""
+    (T, k), E = topk_w.shape, d_logits.shape[-1]
+    _pairs(topk_ids, "topk_ids", "int32", T, k)
+    _pairs(topk_w, "topk_w", "f32", T, k)
+    _pairs(d_topk_w, "d_topk_w", "f32", T, k)
+    _pairs(d_logits, "d_logits", "f32", T, E)
+    st = _stream_of(stream, topk_ids, topk_w, d_topk_w, d_logits)
+    _check(lib().moe_gate_backward(_ptr(topk_ids), _ptr(topk_w), _ptr(d_topk_w), T, E, k, _ptr(d_logits), st))
 
 
 class MoeCache:
