@@ -448,7 +448,7 @@ int moe_w4_linear(int fmt, const void* w, int N, int K, int group, const void* x
  *         tanh( sqrt(2 / pi) (z + 0.044715 z^3) )
  *   res   T rows of N of rdt, r_ld apart, or NULL; may be y itself (same start, type and stride)
  *   y     T rows of N of ydt, y_ld apart; apart from that overlaps no operand (MOE_EINVAL)
- * K, w_ld and x_ld multiples of 8 (bf16) or 4 (f32), K <= 2^20, w_ld and x_ld <= 2^21; y_ld and r_ld
+ * K, w_ld and x_ld multiples of 8 (bf16) or 4 (f32), K, w_ld and x_ld at most 2^20; y_ld and r_ld
  * any; T and N at most 2^22, T * N at most 2^35.  Products of bf16 are exact, sums are in f32 in an
  * order that the shape fixes, bias, activation and residual are applied in f32 before the one
  * rounding to ydt; f32 weights are multiplied in f32.  The erf inside GELU is within 1.5e-7.

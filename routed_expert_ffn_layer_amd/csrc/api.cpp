@@ -474,8 +474,8 @@ int moe_linear(int wdt, const void* w, int64_t w_ld, int N, int K, const void* x
   if (T == 0) return MOE_OK;
   if (int rc = check_rows(w, w_ld, K, "w")) return rc;
   if (int rc = check_rows(x, x_ld, K, "x")) return rc;
-  REQUIRE(w_ld % q == 0 && w_ld <= 1 << 21 && x_ld % q == 0 && x_ld <= 1 << 21,
-          "moe_linear: rows of w and x %lld and %lld apart (multiples of %d, at most 2^21)", (long long)w_ld,
+  REQUIRE(w_ld % q == 0 && w_ld <= 1 << 20 && x_ld % q == 0 && x_ld <= 1 << 20,
+          "moe_linear: rows of w and x %lld and %lld apart (multiples of %d, at most 2^20)", (long long)w_ld,
           (long long)x_ld, q);
   if (int rc = check_rows(y, y_ld, N, "y")) return rc;
   if (res)

@@ -1,22 +1,20 @@
 // linear.hip -- y = act(x W^T + bias) + res for f32 or bf16 weights stored as they come, one row of W
 // after another.
 //
-// Two kernels.  linear_stream_kernel: every wave multiplies 16 RT weight rows by 16 TT tokens over its
-// part of K with operands straight from memory in the matrix instructions' order, and the waves of a
-// workgroup, which split K between them, add up in LDS.  There is no barrier before that sum and no
-// staging, so the weights stream at the rate of memory: for few tokens, where the weights are the work,
-// and for f32, whose matrix instructions are slow enough (1/16 of bf16's rate) to be fed this way at any
-// size.  linear_tile_kernel: for many tokens in bf16, where the matrix instructions are the work:
-// workgroup tiles staged through LDS.
+// Two kernels.  linear_stream_kernel, for very few tokens: every wave multiplies 16 weight rows by up to 16
+// tokens over its part of K, operands straight from memory in the matrix instructions' order, and the waves of a
+// workgroup, which split K between them, add up in LDS; no barrier and no staging before that.
+// linear_tile_kernel, for all else: tiles staged through LDS, from 32 x 32 (weights are the work: many small
+// workgroups, deep in flight) to 256 x 256 (the matrix instructions are).  Sums in f32, in an order fixed by
+// the shape.
 //
-// A 64-byte piece of a row is one step of the stream kernel: lane group g = lane / 16 holds bytes
-// 16 g .. 16 g + 15 of it (8 bf16 or 4 f32) for row lane % 16, of weights and tokens alike.  In bf16
-// that is the operand of one v_mfma_f32_16x16x32_bf16, in f32 of four v_mfma_f32_16x16x4_f32 (the
-// k-th of them takes element k of the four lane groups).  Sums in f32, in an order fixed by the shape.
+// Measured on an MI355X, bf16, x weights x K (plain library product beside it): 1 x 4096 x 4096 7.5 us (20),
+// 16 x 12288 x 4096 17.2 (21.6), 64 x 4096 x 4096 9.1 (19), 16 x 65536 x 4096 100 (121; 537 MB at 5.4 TB/s),
+// 256 x 4096 x 4096 16.3 (19.7), 1024 x 4096 x 4096 35.6 (37.4), 4096 x 8192 x 4096 224 (220; 1.23 PFLOP/s);
+// f32: 64 x 4096 x 4096 26 (23.5), 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).
 #include "ffn_common.hpp"
 #include "kernels.hpp"
 #include "row_io.hpp"
-#include <stdlib.h>
 
 #include <type_traits>
 
@@ -92,66 +90,53 @@ __device__ __forceinline__ void finish8(const LinearArgs& a, int64_t t, int n, f
 
 constexpr int kPast = 0x7ffffff0;  // an offset past the end of every buffer made here (under 2^30 bytes): reads as 0
 
-template <bool BF16>
-__device__ __forceinline__ f32x4 mma_step(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (BF16) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
-    return c;
-  }
-}
+// ---------------------------------------------------------------------------
+// Up to 16 tokens.  A 64-byte piece of a row is one step: lane group g = lane / 16 holds bytes 16 g .. 16 g + 15 of
+// it (8 bf16 or 4 f32) for row lane % 16, of weights (the B operand) and tokens (A) alike: the operand of one
+// v_mfma_f32_16x16x32_bf16, or of four v_mfma_f32_16x16x4_f32.  Lane l of the 16 x 16 result holds tokens
+// 4 (l / 16) + v and weight row l % 16.  Rounds of 4 steps load together, the next round's while one is
+// multiplied; 8 waves of one row tile keep 64 KB in flight a workgroup (16 waves, or rounds of 8: 20% slower
+// over 65536 rows, from fewer workgroups in a CU).
+// ---------------------------------------------------------------------------
+constexpr int kStreamSteps = 4, kStreamWaves = 8;
 
-// Tokens are the A operand, weight rows the B operand: lane l of the 16 x 16 result holds tokens
-// 4 (l / 16) + v and weight row l % 16.
-// RT, TT: 16-row tiles of W and of tokens a wave holds; U: steps whose operands load together; MAXW: waves
-// at most.
-template <bool BF16, int RT, int TT, int U, int MAXW>
-__global__ __launch_bounds__(64 * MAXW) void linear_stream_kernel(LinearArgs a, int n_tiles) {
-  extern __shared__ float lds[];  // [waves][RT][TT][64][4]
-  constexpr int ES = BF16 ? 2 : 4;
+template <bool BF16>
+__global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a) {
+  __shared__ float part[kStreamWaves][256];
+  constexpr int ES = BF16 ? 2 : 4, U = kStreamSteps;
   const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6), nw = blockDim.x >> 6;
-  const int n0 = (int)(blockIdx.x % n_tiles) * 16 * RT;
-  const int64_t t0 = (int64_t)(blockIdx.x / n_tiles) * 16 * TT;
-  const int row = lane & 15, g = lane >> 4;
+  const int n0 = (int)blockIdx.x * 16, row = lane & 15, g = lane >> 4;
   const int kbytes = a.K * ES;
   // the tile's rows, and nothing behind them
   const auto wbuf = make_rsrc(static_cast<const uint8_t*>(a.w) + n0 * a.w_ld * ES,
-                              (min(a.N - n0, 16 * RT) - 1) * a.w_ld * ES + kbytes);
-  const auto xbuf = make_rsrc(static_cast<const uint8_t*>(a.x) + t0 * a.x_ld * ES,
-                              (min(a.T - (int)t0, 16 * TT) - 1) * a.x_ld * ES + kbytes);
-  int woff[RT], xoff[TT];  // this lane's rows; rows past the end read as 0
-#pragma unroll
-  for (int i = 0; i < RT; ++i) woff[i] = n0 + 16 * i + row < a.N ? (int)((16 * i + row) * a.w_ld * ES) + 16 * g : kPast;
-#pragma unroll
-  for (int i = 0; i < TT; ++i) xoff[i] = t0 + 16 * i + row < a.T ? (int)((16 * i + row) * a.x_ld * ES) + 16 * g : kPast;
+                              (min(a.N - n0, 16) - 1) * a.w_ld * ES + kbytes);
+  const auto xbuf = make_rsrc(a.x, (a.T - 1) * a.x_ld * ES + kbytes);
+  // this lane's rows; rows past the end read as 0
+  const int woff = n0 + row < a.N ? (int)(row * a.w_ld * ES) + 16 * g : kPast;
+  const int xoff = row < a.T ? (int)(row * a.x_ld * ES) + 16 * g : kPast;
   const int steps = (kbytes + 63) / 64, rounds = (steps + U - 1) / U;
-  f32x4 acc[RT][TT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < TT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  u32x4 wf[2][U][RT], xf[2][U][TT];
-  auto load = [&](int r, u32x4 (&w)[U][RT], u32x4 (&x)[U][TT]) {
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  u32x4 wf[2][U], xf[2][U];
+  auto load = [&](int r, u32x4 (&w)[U], u32x4 (&x)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int at = (r * U + u) * 64;
       const bool in = at + 16 * g < kbytes;  // whole 16-byte fragments: K is a multiple of one
-#pragma unroll
-      for (int i = 0; i < RT; ++i) w[u][i] = bld16(wbuf, in && woff[i] != kPast ? woff[i] + at : kPast, 0);
-#pragma unroll
-      for (int i = 0; i < TT; ++i) x[u][i] = bld16(xbuf, in && xoff[i] != kPast ? xoff[i] + at : kPast, 0);
+      w[u] = bld16(wbuf, in && woff != kPast ? woff + at : kPast, 0);
+      x[u] = bld16(xbuf, in && xoff != kPast ? xoff + at : kPast, 0);
     }
   };
-  auto multiply = [&](const u32x4 (&w)[U][RT], const u32x4 (&x)[U][TT]) {
+  auto multiply = [&](const u32x4 (&w)[U], const u32x4 (&x)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      if constexpr (BF16) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[u]), as_bf16x8(w[u]), acc, 0, 0, 0);
+      } else {
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < TT; ++j) acc[i][j] = mma_step<BF16>(x[u][j], w[u][i], acc[i][j]);
+        for (int i = 0; i < 4; ++i)
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[u][i]), __uint_as_float(w[u][i]), acc, 0, 0, 0);
+      }
+    }
   };
   int r = wv;
   if (r < rounds) load(r, wf[0], xf[0]);
@@ -164,48 +149,43 @@ __global__ __launch_bounds__(64 * MAXW) void linear_stream_kernel(LinearArgs a, 
     multiply(wf[1], xf[1]);
     r += nw;
   }
-  f32x4* part = reinterpret_cast<f32x4*>(lds);
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < TT; ++j) part[((wv * RT + i) * TT + j) * 64 + lane] = acc[i][j];
+  *reinterpret_cast<f32x4*>(&part[wv][lane * 4]) = acc;
   lds_barrier();
-  // element q of the tile: result (i, j), lane and register in order
-  for (int q = threadIdx.x; q < RT * TT * 256; q += blockDim.x) {
+  for (int q = threadIdx.x; q < 256; q += blockDim.x) {
     float s = 0.0f;
-    for (int w = 0; w < nw; ++w) s += lds[w * RT * TT * 256 + q];
-    const int v = q & 3, l = (q >> 2) & 63, ij = q >> 8;
-    const int n = n0 + 16 * (ij / TT) + (l & 15);
-    const int64_t t = t0 + 16 * (ij % TT) + 4 * (l >> 4) + v;
+    for (int w = 0; w < nw; ++w) s += part[w][q];
+    const int l = q >> 2, n = n0 + (l & 15), t = 4 * (l >> 4) + (q & 3);
     if (n < a.N && t < a.T) finish(a, t, n, s);
   }
 }
 
-template <bool BF16, int RT, int TT, int U, int MAXW>
+template <bool BF16>
 hipError_t launch_stream(const LinearArgs& a, hipStream_t st) {
-  const int steps = (a.K * (BF16 ? 2 : 4) + 63) / 64;
-  int waves = 1;  // no more than there are rounds of U steps
-  while (waves < MAXW && waves * U < steps) waves *= 2;
-  const int n_tiles = (a.N + 16 * RT - 1) / (16 * RT), t_tiles = (a.T + 16 * TT - 1) / (16 * TT);
-  const int lds = waves * RT * TT * 1024;
-  hipLaunchKernelGGL((linear_stream_kernel<BF16, RT, TT, U, MAXW>), dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * waves), lds, st,
-                     a, n_tiles);
+  const int rounds = (a.K * (BF16 ? 2 : 4) + 64 * kStreamSteps - 1) / (64 * kStreamSteps);
+  int waves = 1;  // no more than there are rounds
+  while (waves < kStreamWaves && waves < rounds) waves *= 2;
+  hipLaunchKernelGGL(linear_stream_kernel<BF16>, dim3((unsigned)((a.N + 15) / 16)), dim3(64 * waves), 0, st, a);
   return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens, bf16.  A workgroup of WN x WT waves computes BN weight rows by BT tokens; K goes in stages
-// of 64, both operands' rows of a stage (128 bytes each) straight from memory into one of two LDS
-// buffers, the next stage's loads in flight while this one is multiplied.  Matrix instruction
-// v_mfma_f32_32x32x16_bf16, weights as A and tokens as B: a lane then holds 4 consecutive outputs of one
-// token at a time, a vector store each.  Lane l supplies row l % 32, 16-byte piece 2 m + l / 32 of the row
-// in k-step m.  Piece p of row r sits at position p ^ swz(r): the rows that one 128-bit LDS read touches
-// land in distinct banks whether it is served 8 or 16 lanes at a time.
-constexpr int kStage = 64;                // columns of a stage
-constexpr int kStageBytes = kStage * 2;   // of one row
+// More tokens.  A workgroup computes BN weight rows by BT tokens on WN x WT x WK waves: WN x WT of them side by
+// side, and WK that share a part of the tile and split K between them (their sums meet in LDS at the end).  K
+// goes in stages of 128 bytes, both operands' rows of a stage straight from memory into one of D LDS buffers,
+// the next ones in flight while one is multiplied.  Matrix instruction v_mfma_f32_32x32x16_bf16 or
+// v_mfma_f32_32x32x2_f32, weights as A and tokens as B.  Lane l supplies row l % 32, 16-byte piece 2 m + l / 32 of
+// the row in step m of the stage.  Piece p of row r sits at place p ^ swz(r).
+//
+// Each step is laid out by hand: a product, an operand read of the next step, a load of a later stage, the next
+// product, .. (reads, loads and products one after the other: 4096 x 8192 x 4096 in 267 us, so 224).  What bounds
+// the largest tile now is the barrier that ends a stage: the matrix unit is busy in 77% of the cycles, at a
+// clock that this work holds near 1.5 GHz.
+// ---------------------------------------------------------------------------
+constexpr int kRow = 128;  // bytes of a row in a stage
 
-constexpr int kOutLd = 68;                // f32 of a row of results in LDS: 64 and 4 against bank conflicts
-constexpr int kOutBytes = 32 * kOutLd * 4;
+// Results of a wave in LDS: 32 tokens by one or two 32-row tiles, padded against bank conflicts.
+constexpr int out_ld(int tiles) { return 32 * (tiles % 2 ? 1 : 2) + 4; }
+constexpr int out_bytes(int tiles) { return 32 * out_ld(tiles) * 4; }
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
@@ -216,17 +196,43 @@ __device__ __forceinline__ void block_barrier() {
   asm volatile("" ::: "memory");
 }
 
-__device__ __forceinline__ int swz(int r) { return (r + (r >> 3)) & 7; }
+// s_waitcnt with at most N vector loads outstanding; LGKM: and no LDS access.
+template <int N, bool LGKM>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  constexpr int imm = (N & 15) | (N >> 4) << 14 | (LGKM ? 0x0070 : 0x0f70);
+  __builtin_amdgcn_s_waitcnt(imm);
+}
 
-template <int BN, int BT, int WN, int WT>
-__global__ __launch_bounds__(64 * WN * WT) void linear_tile_kernel(LinearArgs a, int n_tiles, int t_tiles) {
-  constexpr int W = WN * WT, RN = BN / WN / 32, RT = BT / WT / 32;  // 32-row tiles of a wave
-  constexpr int ROWS = BN + BT, BUF = ROWS * kStageBytes, PIECES = ROWS / 8 / W;
-  static_assert(BN % (8 * W) == 0 && BT % (8 * W) == 0, "a round of pieces is of one operand");
-  static_assert(RN * RT >= RN + RT, "a product for each operand");
+// A 128-bit LDS read is served 16 lanes at a time, over 256 bytes of banks: lanes 0-3, 12-15 and 20-27
+// of each half first, then the others.  The XOR term gives the rows of each of these groups places of their own
+// (no bank conflicts counted; (r + r / 8) % 8 for 128-byte rows cost 4 cycles a read).
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+
+// acc += A . B over 32 bytes of K: 16 bf16, or 8 f32 in four products (the k-th of both halves' pieces each).
+template <bool BF16>
+__device__ __forceinline__ f32x16 mma_tile(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (BF16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
+    return c;
+  }
+}
+
+template <bool BF16, int BN, int BT, int WN, int WT, int WK, int D>
+__global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearArgs a, int n_tiles, int t_tiles) {
+  constexpr int W = WN * WT * WK, RN = BN / WN / 32, RT = BT / WT / 32;  // 32-row tiles of a wave
+  constexpr int ES = BF16 ? 2 : 4, PPR = kRow / 16, RPP = 64 / PPR;      // 16-byte pieces of a row; rows of 1 KB
+  constexpr int BUF = (BN + BT) * kRow, LOADS = (BN + BT) / RPP / W;      // a stage's loads of a wave, 1 KB each
+  constexpr int S = kRow / 32 / WK, P = RN * RT;                           // steps of a wave in a stage, products in a step
+  static_assert(BN % (RPP * W) == 0 && BT % (RPP * W) == 0, "a round of loads is of one operand");
   extern __shared__ uint8_t smem[];
   const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
   const int rho = lane & 31, h = lane >> 5;
+  const int wk = wv % WK, wt = wv / WK % WT, wn = wv / WK / WT;
   // Workgroup b runs on XCD b % 8: each XCD takes a run of tiles, ordered so that neighbours share
   // rows in its L2: 4 weight tiles by all token tiles.
   int tn, tt;
@@ -239,26 +245,28 @@ __global__ __launch_bounds__(64 * WN * WT) void linear_tile_kernel(LinearArgs a,
   }
   const int n0 = tn * BN, t0 = tt * BT;
   const int wrows = min(BN, a.N - n0), xrows = min(BT, a.T - t0);
-  const auto wbuf = make_rsrc(static_cast<const uint16_t*>(a.w) + n0 * a.w_ld, ((wrows - 1) * a.w_ld + a.K) * 2);
-  const auto xbuf = make_rsrc(static_cast<const uint16_t*>(a.x) + t0 * a.x_ld, ((xrows - 1) * a.x_ld + a.K) * 2);
-  // 1 KB pieces of 8 rows, wave wv takes pieces wv + W i; rows past the end repeat the last one, and in a
-  // last, partial stage (of `tail` bytes) pieces past the end repeat the row's first one of the stage
-  const int stages = (a.K + kStage - 1) / kStage, tail = (a.K % kStage) * 2;
-  int voff[PIECES], past[PIECES];
+  const int64_t w_step = a.w_ld * ES, x_step = a.x_ld * ES;
+  const int kbytes = a.K * ES;
+  const auto wbuf = make_rsrc(static_cast<const uint8_t*>(a.w) + n0 * w_step, (wrows - 1) * w_step + kbytes);
+  const auto xbuf = make_rsrc(static_cast<const uint8_t*>(a.x) + t0 * x_step, (xrows - 1) * x_step + kbytes);
+  // Load i of wave wv fills rows RPP (wv + W i) .. of the stage's buffer; rows past the end repeat the last
+  // one, and in a last, partial stage (of `tail` bytes) pieces past the end repeat the row's first one of the stage.
+  const int stages = (kbytes + kRow - 1) / kRow, tail = kbytes % kRow;
+  int voff[LOADS], past[LOADS];
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i) {
-    const int row = 8 * (wv + W * i) + lane / 8, col = ((lane & 7) ^ swz(row)) * 16;
-    voff[i] = (row < BN ? (int)(min(row, wrows - 1) * a.w_ld * 2) : (int)(min(row - BN, xrows - 1) * a.x_ld * 2)) + col;
+  for (int i = 0; i < LOADS; ++i) {
+    const int row = RPP * (wv + W * i) + lane / PPR, col = ((lane % PPR) ^ swz(row)) * 16;
+    voff[i] = (row < BN ? (int)(min(row, wrows - 1) * w_step) : (int)(min(row - BN, xrows - 1) * x_step)) + col;
     past[i] = tail && col >= tail ? col : 0;
   }
-  // piece i of stage s; no branch: stages past the last repeat it
+  // load i of stage s; no branch: stages past the last repeat it
   auto load = [&](int s, uint8_t* buf, int i) {
     const int at = min(s, stages - 1), last = at == stages - 1 ? -1 : 0;
-    const int piece = wv + W * i, from = voff[i] - (past[i] & last);
-    if (W * i < BN / 8)  // known when the loops are unrolled
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_ptr)(buf + piece * 1024), 16, from, at * kStageBytes, 0, 0);
+    const int from = voff[i] - (past[i] & last);
+    if (W * i < BN / RPP)  // known when the loops are unrolled
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_ptr)(buf + (wv + W * i) * 1024), 16, from, at * kRow, 0, 0);
     else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xbuf, (lds_ptr)(buf + piece * 1024), 16, from, at * kStageBytes, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xbuf, (lds_ptr)(buf + (wv + W * i) * 1024), 16, from, at * kRow, 0, 0);
   };
   f32x16 acc[RN][RT];
 #pragma unroll
@@ -267,152 +275,196 @@ __global__ __launch_bounds__(64 * WN * WT) void linear_tile_kernel(LinearArgs a,
     for (int j = 0; j < RT; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  // this lane's rows; swz(r + 32) = swz(r) ^ 4, and so the k-step's piece 2 m + h moves to m ^ 2
-  const int wrow = (wv / WT) * (BN / WN) + rho, xrow = BN + (wv % WT) * (BT / WT) + rho;
-  int wat[4], xat[4];
+  // this lane's rows (swz is the same 32 rows on) in the wave's steps wk, wk + WK, ..
+  const int wrow = wn * (BN / WN) + rho, xrow = BN + wt * (BT / WT) + rho;
+  int wat[S], xat[S];
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    wat[m] = wrow * kStageBytes + (((2 * m + h) ^ swz(wrow)) << 4);
-    xat[m] = xrow * kStageBytes + (((2 * m + h) ^ swz(xrow)) << 4);
+  for (int m = 0; m < S; ++m) {
+    const int p = 2 * (wk + WK * m) + h;
+    wat[m] = wrow * kRow + ((p ^ swz(wrow)) << 4);
+    xat[m] = xrow * kRow + ((p ^ swz(xrow)) << 4);
   }
-  // operand q of step m: weight and token tiles by turns, in the order in which the products take them
-  auto read = [&](const uint8_t* buf, int m, int q, bf16x8 (&A)[RN], bf16x8 (&B)[RT]) {
+  // operand q of the wave's step m: weight tiles, then token tiles
+  auto read = [&](const uint8_t* buf, int m, int q, u32x4 (&A)[RN], u32x4 (&B)[RT]) {
     if (q < RN)
-      A[q] = as_bf16x8(*reinterpret_cast<const u32x4*>(buf + wat[m ^ (2 * (q & 1))] + q * 32 * kStageBytes));
+      A[q] = *reinterpret_cast<const u32x4*>(buf + wat[m] + q * 32 * kRow);
     else
-      B[q - RN] = as_bf16x8(*reinterpret_cast<const u32x4*>(buf + xat[m ^ (2 * ((q - RN) & 1))] + (q - RN) * 32 * kStageBytes));
+      B[q - RN] = *reinterpret_cast<const u32x4*>(buf + xat[m] + (q - RN) * 32 * kRow);
   };
-  // One step: the products of A and B; behind each of the first ones an operand of the next step (m of buffer
-  // `next`) is read, and with LOAD pieces of stage s go out, so that neither keeps the matrix unit waiting.
-  auto step = [&](auto LOAD, const uint8_t* next, int m, int s, uint8_t* into, const bf16x8 (&A)[RN], const bf16x8 (&B)[RT],
-                  bf16x8 (&An)[RN], bf16x8 (&Bn)[RT]) {
+  // Part e (of S) of stage s's loads, into `into`: behind the barrier that frees the buffer, under the S steps
+  // that follow, so that the loads' issue keeps up with them.  Two buffers leave no time for that: all
+  // go out at once then.
+  constexpr int SPREAD = D > 2 ? S : 1;
+  // One step: the products of A and B; behind each of them operands of the next step (m of buffer `next`) are
+  // read and part e of stage s's loads goes out, so that neither keeps the matrix unit waiting.
+  auto step = [&](const uint8_t* next, int m, auto E, int s, uint8_t* into, const u32x4 (&A)[RN], const u32x4 (&B)[RT],
+                  u32x4 (&An)[RN], u32x4 (&Bn)[RT]) {
+    constexpr int per = (RN + RT + P - 1) / P;  // operands a product
+    constexpr int e = decltype(E)::value;
+    constexpr int lo = e < SPREAD ? e * LOADS / SPREAD : 0, hi = e < SPREAD ? (e + 1) * LOADS / SPREAD : 0;
 #pragma unroll
-    for (int p = 0; p < RN * RT; ++p) {
+    for (int p = 0; p < P; ++p) {
       const int i = p % RN, j = p / RN;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A[i], B[j], acc[i][j], 0, 0, 0);
-      if (p < RN + RT) read(next, m, p, An, Bn);
-      if constexpr (decltype(LOAD)::value) {
+      acc[i][j] = mma_tile<BF16>(A[i], B[j], acc[i][j]);
 #pragma unroll
-        for (int d = p * PIECES / (RN * RT); d < (p + 1) * PIECES / (RN * RT); ++d) load(s, into, d);
-      }
+      for (int q = p * per; q < (p + 1) * per; ++q)
+        if (q < RN + RT) read(next, m, q, An, Bn);
+#pragma unroll
+      for (int d = lo + p * (hi - lo) / P; d < lo + (p + 1) * (hi - lo) / P; ++d) load(s, into, d);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // Steps m = 0 .. 3 of stage s.  The first step's operands are read behind the barrier that ends the stage
-  // before, under that stage's last products.  The barrier also frees the stage's buffer, for the loads of
-  // stage s + 2.
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i) load(0, smem, i);
+  for (int d = 0; d < D; ++d)
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i) load(1, smem + BUF, i);
+    for (int i = 0; i < (d < D - 1 ? LOADS : LOADS / SPREAD); ++i) load(d, smem + d * BUF, i);
   const int whole = tail ? stages - 1 : stages;
-  bf16x8 A[2][RN], B[2][RT];
-  constexpr int kOneStage = 0x0f70 | (PIECES & 15) | PIECES >> 4 << 14;  // vmcnt(PIECES)
-  __builtin_amdgcn_s_waitcnt(kOneStage);  // stage 0 has landed, stage 1 is on its way
+  u32x4 A[2][RN], B[2][RT];
+  wait_loads<(D - 2) * LOADS + LOADS / SPREAD, false>();  // stage 0 has landed
   block_barrier();
 #pragma unroll
   for (int q = 0; q < RN + RT; ++q) read(smem, 0, q, A[0], B[0]);
-  const std::true_type with_loads;
-  const std::false_type without;
-  for (int s = 0; s < whole; ++s) {
-    uint8_t *buf = smem + (s & 1) * BUF, *other = smem + ((s + 1) & 1) * BUF;
-    step(without, buf, 1, 0, buf, A[0], B[0], A[1], B[1]);
-    step(without, buf, 2, 0, buf, A[1], B[1], A[0], B[0]);
-    step(without, buf, 3, 0, buf, A[0], B[0], A[1], B[1]);
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0): own loads of stage s + 1, own reads of stage s
+  // The first step's operands are read behind the barrier that ends the stage before, under that stage's
+  // last products.
+  uint8_t *buf = smem, *freed = smem + (D - 1) * BUF;
+  auto stage = [&](int s, auto FIRST) {  // FIRST: the operand set that holds the stage's first step
+    constexpr int f = decltype(FIRST)::value;
+    uint8_t* other = buf == smem + (D - 1) * BUF ? smem : buf + BUF;
+    auto early = [&](auto E) {  // step E - 1 of the stage
+      constexpr int e = decltype(E)::value;
+      if constexpr (e < S)
+        step(buf, e, E, s + D - 1, freed, A[(e - 1 + f) & 1], B[(e - 1 + f) & 1], A[(e + f) & 1], B[(e + f) & 1]);
+    };
+    early(std::integral_constant<int, 1>());
+    early(std::integral_constant<int, 2>());
+    early(std::integral_constant<int, 3>());
+    wait_loads<(D - 2) * LOADS, true>();  // own loads of stage s + 1, own reads of stage s
     block_barrier();
-    step(with_loads, other, 0, s + 2, buf, A[1], B[1], A[0], B[0]);  // past the last stage: read and not used
+    step(other, 0, std::integral_constant<int, 0>(), s + D, buf, A[(S - 1 + f) & 1], B[(S - 1 + f) & 1], A[(S + f) & 1], B[(S + f) & 1]);
+    freed = buf;
+    buf = other;  // past the last stage its operands are read and not used
+  };
+  static_assert(S <= 4, "steps of a stage");
+  const std::integral_constant<int, 0> even;
+  const std::integral_constant<int, S & 1> odd;
+  int s = 0;
+  for (; s + 1 < whole; s += 2) {
+    stage(s, even);
+    stage(s + 1, odd);
   }
-  if (tail) {
-    const uint8_t* buf = smem + ((stages - 1) & 1) * BUF;  // landed and visible since the last barrier
-    for (int m = 0; 32 * m < tail; ++m) {
-      const int p = 2 * m + h;  // computed here: m is no constant
+  if (s < whole) stage(s, even);
+  if (tail) {  // landed and visible since the last barrier
+    for (int m = wk; 32 * m < tail; m += WK) {
+      const int p = 2 * m + h;
 #pragma unroll
-      for (int i = 0; i < RN; ++i) {
-        const int r = wrow + 32 * i;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(buf + r * kStageBytes + ((p ^ swz(r)) << 4));
-        A[0][i] = as_bf16x8(p * 16 < tail ? v : u32x4{0, 0, 0, 0});
+      for (int q = 0; q < RN + RT; ++q) {
+        const int r = q < RN ? wrow + 32 * q : xrow + 32 * (q - RN);
+        u32x4 v = *reinterpret_cast<const u32x4*>(buf + r * kRow + ((p ^ swz(r)) << 4));
+        if (p * 16 >= tail) v = u32x4{0, 0, 0, 0};
+        if (q < RN)
+          A[0][q] = v;
+        else
+          B[0][q - RN] = v;
       }
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const int r = xrow + 32 * j;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(buf + r * kStageBytes + ((p ^ swz(r)) << 4));
-        B[0][j] = as_bf16x8(p * 16 < tail ? v : u32x4{0, 0, 0, 0});
-      }
-#pragma unroll
-      for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int i = 0; i < RN; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A[0][i], B[0][j], acc[i][j], 0, 0, 0);
+      for (int p2 = 0; p2 < P; ++p2)
+        acc[p2 % RN][p2 / RN] = mma_tile<BF16>(A[0][p2 % RN], B[0][p2 / RN], acc[p2 % RN][p2 / RN]);
     }
   }
-  // Results: 32 tokens by 64 weight rows at a time through the wave's own part of LDS, so that a lane
-  // finishes 8 consecutive outputs and the rows of res and y are read and written in whole lines.
-  static_assert(W * kOutBytes <= 2 * BUF && RN % 2 == 0, "the results' part of LDS");
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // the loads past the last stage have landed
-  __syncthreads();                     // and nobody reads a stage any more
+  // Results: 32 tokens by up to 64 weight rows at a time through LDS, so that a lane finishes 8
+  // consecutive outputs and the rows of res and y are read and written in whole lines.  The WK waves of a part
+  // share its tokens out between them.
+  constexpr int SL = RN % 2 ? 1 : 2, LD = out_ld(RN), LANES = 4 * SL;  // tiles of a slice; lanes a token
+  constexpr int kOutBytes = out_bytes(RN);
+  wait_loads<0, false>();  // the loads past the last stage have landed
+  __syncthreads();         // and nobody reads a stage any more
   float* out = reinterpret_cast<float*>(smem + wv * kOutBytes);
+  const float* part = reinterpret_cast<const float*>(smem + (wv - wk) * kOutBytes);
 #pragma unroll
   for (int j = 0; j < RT; ++j)
 #pragma unroll
-    for (int i2 = 0; i2 < RN; i2 += 2) {
+    for (int i2 = 0; i2 < RN; i2 += SL) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < SL; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const f32x16& c = acc[i2 + i][j];  // lane: token rho, rows 8 q + 4 h + 0 .. 3
-          *reinterpret_cast<f32x4*>(out + rho * kOutLd + 32 * i + 8 * q + 4 * h) =
+          *reinterpret_cast<f32x4*>(out + rho * LD + 32 * i + 8 * q + 4 * h) =
               f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
         }
-      __builtin_amdgcn_wave_barrier();
-      const int n = n0 + (wv / WT) * (BN / WN) + 32 * i2 + 8 * (lane & 7);
-      for (int u = lane >> 3; u < 32; u += 8) {
-        const int t = t0 + (wv % WT) * (BT / WT) + 32 * j + u;
+      if constexpr (WK > 1)
+        lds_barrier();
+      else
+        __builtin_amdgcn_wave_barrier();
+      const int n = n0 + wn * (BN / WN) + 32 * i2 + 8 * (lane % LANES);
+      for (int u = wk * (64 / LANES) + lane / LANES; u < 32; u += WK * (64 / LANES)) {
+        const int t = t0 + wt * (BT / WT) + 32 * j + u;
         if (t >= a.T || n >= a.N) continue;
-        float v[8];
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(out + u * kOutLd + 8 * (lane & 7));
-        const f32x4 hi = *reinterpret_cast<const f32x4*>(out + u * kOutLd + 8 * (lane & 7) + 4);
+        float v[8] = {};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = lo[e];
-          v[4 + e] = hi[e];
+        for (int k = 0; k < WK; ++k) {
+          const float* p = part + k * (kOutBytes / 4) + u * LD + 8 * (lane % LANES);
+          const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] += lo[e];
+            v[4 + e] += hi[e];
+          }
         }
         finish8(a, t, n, v);
       }
-      __builtin_amdgcn_wave_barrier();
+      if constexpr (WK > 1)
+        lds_barrier();
+      else
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
-template <int BN, int BT, int WN, int WT>
+template <bool BF16, int BN, int BT, int WN, int WT, int WK, int D>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
   const int n_tiles = (a.N + BN - 1) / BN, t_tiles = (a.T + BT - 1) / BT;
-  constexpr int lds = 2 * (BN + BT) * kStageBytes;
-  hipLaunchKernelGGL((linear_tile_kernel<BN, BT, WN, WT>), dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * WN * WT), lds, st, a,
-                     n_tiles, t_tiles);
+  constexpr int ring = D * (BN + BT) * kRow, out = WN * WT * WK * out_bytes(BN / WN / 32);
+  constexpr int lds = ring > out ? ring : out;
+  hipLaunchKernelGGL((linear_tile_kernel<BF16, BN, BT, WN, WT, WK, D>), dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * WN * WT * WK),
+                     lds, st, a, n_tiles, t_tiles);
   return hipGetLastError();
 }
 
-template <bool BF16>
-hipError_t launch_by_size(const LinearArgs& a, hipStream_t st) {
-  if (a.T <= 16) return launch_stream<BF16, 1, 1, 8, 16>(a, st);
-  if (a.T <= 32) return launch_stream<BF16, 2, 2, 4, 8>(a, st);
-  return launch_stream<BF16, 4, 4, 2, 4>(a, st);
-}
+// Tile shapes, by the time that a stage (128 bytes of K) of a round of 256 workgroups, one for each CU, takes: us,
+// measured at K = 4096 with 256 workgroups (the first four, by the matrix unit; the others, by the latency of a
+// stage).  The shape whose rounds come out cheapest is taken: within 5% of the best of the seven shapes over
+// T = 16 .. 8192 and N = 1003 .. 65536, where single shapes lose up to 8 times.
+struct TileShape {
+  int rows, tokens;
+  float us[2];  // f32, bf16
+  hipError_t (*launch[2])(const LinearArgs&, hipStream_t);
+};
+#define TILE(BN, BT, F, B, ...) {BN, BT, {F, B}, {launch_tile<false, BN, BT, __VA_ARGS__>, launch_tile<true, BN, BT, __VA_ARGS__>}}
+const TileShape kShapes[] = {
+    TILE(256, 256, 7.4f, 1.77f, 4, 2, 1, 2), TILE(256, 128, 3.8f, 0.99f, 4, 2, 1, 3),
+    TILE(128, 128, 2.0f, 0.55f, 2, 2, 2, 4), TILE(128, 64, 1.1f, 0.37f, 2, 1, 2, 4),
+    TILE(64, 64, 0.57f, 0.25f, 1, 1, 4, 4),  TILE(64, 32, 0.31f, 0.18f, 1, 1, 4, 5),
+    TILE(32, 32, 0.20f, 0.14f, 1, 1, 4, 8),
+};
+#undef TILE
 
 }  // namespace
 
+// Few tokens: the tiles' 32 token rows would be half of the loads.  bf16, 65536 rows of 4096: 4 tokens 87 us
+// here, 97 in tiles, 16 tokens 122 and 101; f32, 4096 rows: 16 tokens 19 us and 24.
 hipError_t launch_linear(bool bf16, const LinearArgs& a, hipStream_t st) {
-  if (bf16 && a.T > 128) {
-    const char* e = getenv("LIN");
-    const int v = e ? atoi(e) : 0;
-    if (v == 1) return launch_tile<256, 256, 2, 2>(a, st);
-    if (v == 2) return launch_tile<128, 128, 2, 2>(a, st);
-    if (v == 3) return launch_tile<256, 128, 2, 2>(a, st);
-    if (v == 4) return launch_tile<256, 256, 4, 2>(a, st);
-    if (v == 5) return launch_tile<128, 128, 2, 1>(a, st);
-    if (v == 6) return launch_by_size<true>(a, st);
-    return launch_tile<256, 256, 2, 4>(a, st);
+  if (a.T <= (bf16 ? 4 : 16)) return bf16 ? launch_stream<true>(a, st) : launch_stream<false>(a, st);
+  const TileShape* best = nullptr;
+  float least = 0.0f;
+  for (const TileShape& s : kShapes) {
+    const int64_t tiles = (int64_t)((a.N + s.rows - 1) / s.rows) * ((a.T + s.tokens - 1) / s.tokens);
+    const float us = (float)((tiles + 255) / 256) * s.us[bf16];
+    if (!best || us < least) {
+      best = &s;
+      least = us;
+    }
   }
-  return bf16 ? launch_by_size<true>(a, st) : launch_by_size<false>(a, st);
+  return best->launch[bf16](a, st);
 }
 
 }  // namespace moe

@@ -65,6 +65,15 @@ def test_many_tokens(T, N, K):
     _integers(BF16, T, N, K)
 
 
+@pytest.mark.parametrize("T", [19, 61, 125, 250, 509, 1021])
+@pytest.mark.parametrize("K", [8, 72, 128, 520, 1032])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_tile_shapes(T, K, dt):
+    """Every tile shape with part tiles on both sides and part stages: the more tokens, the larger the tile
+    whose number over 12301 rows comes closest to that of the CUs."""
+    _integers(dt, T, 12301, K)
+
+
 @pytest.mark.parametrize("T", [5, 30, 90, 400])
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_strides(T, dt):
