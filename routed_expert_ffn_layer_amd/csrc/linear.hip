@@ -62,30 +62,27 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, fl
     static_cast<float*>(a.y)[t * a.y_ld + n] = v;
 }
 
-// The same for elements n .. n + 7 of token t, as far as they are in the row.
-__device__ __forceinline__ void finish8(const LinearArgs& a, int64_t t, int n, float (&v)[8]) {
-  const int left = a.N - n;
-  if (a.bias) {
-    float b[8];
-    load8(a.bias + n, left, b);
+// Elements n .. n + 7 of token t of res, 0 where there is none or past the row's end.
+__device__ __forceinline__ void residual8(const LinearArgs& a, int64_t t, int n, float (&r)[8]) {
+  if (a.res_bf16)
+    load8(static_cast<const uint16_t*>(a.res) + t * a.r_ld + n, a.N - n, r);
+  else
+    load8(static_cast<const float*>(a.res) + t * a.r_ld + n, a.N - n, r);
+}
+
+// Finished values of elements n .. n + 7 of token t from sums v, bias b and residual r.
+__device__ __forceinline__ void finish8(const LinearArgs& a, int64_t t, int n, float (&v)[8], const float (&b)[8],
+                                        const float (&r)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
+  for (int i = 0; i < 8; ++i) v[i] += b[i];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = activate(v[i], a.act);
-  if (a.res) {
-    float r[8];
-    if (a.res_bf16)
-      load8(static_cast<const uint16_t*>(a.res) + t * a.r_ld + n, left, r);
-    else
-      load8(static_cast<const float*>(a.res) + t * a.r_ld + n, left, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += r[i];
-  }
+  for (int i = 0; i < 8; ++i) v[i] += r[i];
   if (a.y_bf16)
-    store8(static_cast<uint16_t*>(a.y) + t * a.y_ld + n, left, v);
+    store8(static_cast<uint16_t*>(a.y) + t * a.y_ld + n, a.N - n, v);
   else
-    store8(static_cast<float*>(a.y) + t * a.y_ld + n, left, v);
+    store8(static_cast<float*>(a.y) + t * a.y_ld + n, a.N - n, v);
 }
 
 constexpr int kPast = 0x7ffffff0;  // an offset past the end of every buffer made here (under 2^30 bytes): reads as 0
@@ -373,17 +370,31 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
   }
   // Results: 32 tokens by up to 64 weight rows at a time through LDS, so that a lane finishes 8
   // consecutive outputs and the rows of res and y are read and written in whole lines.  The WK waves of a part
-  // share its tokens out between them.
+  // share its tokens out between them.  The residual of all of a wave's passes over a slice is on its way
+  // while the slice goes through LDS (a load and its wait for each pass instead: 36 us of the 260 that
+  // 4096 x 8192 x 4096 with a residual took).
   constexpr int SL = RN % 2 ? 1 : 2, LD = out_ld(RN), LANES = 4 * SL;  // tiles of a slice; lanes a token
+  constexpr int PER = 64 / LANES, PASSES = PER * WK >= 32 ? 1 : 32 / (PER * WK);
   constexpr int kOutBytes = out_bytes(RN);
   wait_loads<0, false>();  // the loads past the last stage have landed
   __syncthreads();         // and nobody reads a stage any more
   float* out = reinterpret_cast<float*>(smem + wv * kOutBytes);
   const float* part = reinterpret_cast<const float*>(smem + (wv - wk) * kOutBytes);
 #pragma unroll
-  for (int j = 0; j < RT; ++j)
+  for (int i2 = 0; i2 < RN; i2 += SL) {
+    const int n = n0 + wn * (BN / WN) + 32 * i2 + 8 * (lane % LANES);
+    float bias[8] = {};
+    if (a.bias && n < a.N) load8(a.bias + n, a.N - n, bias);
 #pragma unroll
-    for (int i2 = 0; i2 < RN; i2 += SL) {
+    for (int j = 0; j < RT; ++j) {
+      const int u0 = wk * PER + lane / LANES, t = t0 + wt * (BT / WT) + 32 * j + u0;
+      float r[PASSES][8];
+#pragma unroll
+      for (int u = 0; u < PASSES; ++u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[u][e] = 0.0f;
+        if (a.res && u0 < 32 && t + u * PER * WK < a.T && n < a.N) residual8(a, t + u * PER * WK, n, r[u]);
+      }
 #pragma unroll
       for (int i = 0; i < SL; ++i)
 #pragma unroll
@@ -396,14 +407,13 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
         lds_barrier();
       else
         __builtin_amdgcn_wave_barrier();
-      const int n = n0 + wn * (BN / WN) + 32 * i2 + 8 * (lane % LANES);
-      for (int u = wk * (64 / LANES) + lane / LANES; u < 32; u += WK * (64 / LANES)) {
-        const int t = t0 + wt * (BT / WT) + 32 * j + u;
-        if (t >= a.T || n >= a.N) continue;
+#pragma unroll
+      for (int u = 0; u < PASSES; ++u) {
+        if (u0 >= 32 || t + u * PER * WK >= a.T || n >= a.N) continue;
         float v[8] = {};
 #pragma unroll
         for (int k = 0; k < WK; ++k) {
-          const float* p = part + k * (kOutBytes / 4) + u * LD + 8 * (lane % LANES);
+          const float* p = part + k * (kOutBytes / 4) + (u0 + u * PER * WK) * LD + 8 * (lane % LANES);
           const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -411,13 +421,14 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
             v[4 + e] += hi[e];
           }
         }
-        finish8(a, t, n, v);
+        finish8(a, t + u * PER * WK, n, v, bias, r[u]);
       }
       if constexpr (WK > 1)
         lds_barrier();
       else
         __builtin_amdgcn_wave_barrier();
     }
+  }
 }
 
 template <bool BF16, int BN, int BT, int WN, int WT, int WK, int D>
