@@ -291,23 +291,27 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
   // Part e (of S) of stage s's loads, into `into`: behind the barrier that frees the buffer, under the S steps
   // that follow, so that the loads' issue keeps up with them.  Two buffers leave no time for that: all
   // go out at once then.
-  constexpr int SPREAD = D > 2 ? S : 1;
+  constexpr int SPREAD = D > 2 ? S : 2;
   // One step: the products of A and B; behind each of them operands of the next step (m of buffer `next`) are
   // read and part e of stage s's loads goes out, so that neither keeps the matrix unit waiting.
   auto step = [&](const uint8_t* next, int m, auto E, int s, uint8_t* into, const u32x4 (&A)[RN], const u32x4 (&B)[RT],
                   u32x4 (&An)[RN], u32x4 (&Bn)[RT]) {
-    constexpr int per = (RN + RT + P - 1) / P;  // operands a product
     constexpr int e = decltype(E)::value;
+    constexpr int X = e == 0 ? (P > 4 ? 4 : 0) : 0, per = (RN + RT + P - X - 1) / (P - X);  // operands a product
     constexpr int lo = e < SPREAD ? e * LOADS / SPREAD : 0, hi = e < SPREAD ? (e + 1) * LOADS / SPREAD : 0;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int i = p % RN, j = p / RN;
+      if (e == 0 && p == X) {
+        wait_loads<(D - 2) * LOADS, true>();  // own loads of stage s + 1, own reads of stage s
+        block_barrier();
+      }
       acc[i][j] = mma_tile<BF16>(A[i], B[j], acc[i][j]);
 #pragma unroll
-      for (int q = p * per; q < (p + 1) * per; ++q)
-        if (q < RN + RT) read(next, m, q, An, Bn);
+      for (int q = (p - X) * per; q < (p - X + 1) * per; ++q)
+        if (q >= 0 && q < RN + RT) read(next, m, q, An, Bn);
 #pragma unroll
-      for (int d = lo + p * (hi - lo) / P; d < lo + (p + 1) * (hi - lo) / P; ++d) load(s, into, d);
+      for (int d = p < X ? lo : lo + (p - X) * (hi - lo) / (P - X); d < (p < X ? lo : lo + (p - X + 1) * (hi - lo) / (P - X)); ++d) load(s, into, d);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -335,8 +339,6 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
     early(std::integral_constant<int, 1>());
     early(std::integral_constant<int, 2>());
     early(std::integral_constant<int, 3>());
-    wait_loads<(D - 2) * LOADS, true>();  // own loads of stage s + 1, own reads of stage s
-    block_barrier();
     step(other, 0, std::integral_constant<int, 0>(), s + D, buf, A[(S - 1 + f) & 1], B[(S - 1 + f) & 1], A[(S + f) & 1], B[(S + f) & 1]);
     freed = buf;
     buf = other;  // past the last stage its operands are read and not used
