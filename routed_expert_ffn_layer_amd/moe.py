@@ -383,28 +383,34 @@ def moe_w4_linear(fmt, w, N, K, group, x, bias, y, stream=None):
                                st))
 
 
-def _code(t, name):
-    """Type code of a tensor whose elements are f32 or bf16."""
-    d = t.dtype
-    if d is _torch().bfloat16:
-        return MOE_BF16
-    if d is _torch_mod.float32:
-        return MOE_F32
-    raise MoeError(MOE_EINVAL, f"{name}: {d}, where float32 or bfloat16 is read")
+_codes = {}  # type codes of the row operators' tensors, filled on first use
 
 
 def _rows(t, name, rows, width, dt=None):
-    """(address, type code, distance between rows) of a [rows][width] tensor with unit stride along
-    its rows, (None, code of f32, width) of None."""
+    """(address, type code, distance between rows) of a [rows][width] f32 or bf16 tensor with unit stride
+    along its rows, (None, code of f32, width) of None."""
     if t is None:
         return None, MOE_F32, width
-    code = _code(t, name)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise MoeError(MOE_EINVAL, f"{name}: {tuple(t.shape)} with strides {t.stride()}, where [{rows}][{width}] with unit "
+    if not _codes:
+        _codes.update({_torch().float32: MOE_F32, _torch_mod.bfloat16: MOE_BF16})
+    code, stride = _codes.get(t.dtype), t.stride()
+    if code is None:
+        raise MoeError(MOE_EINVAL, f"{name}: {t.dtype}, where float32 or bfloat16 is read")
+    if t.shape != (rows, width) or (stride[1] != 1 and width > 1):
+        raise MoeError(MOE_EINVAL, f"{name}: {tuple(t.shape)} with strides {stride}, where [{rows}][{width}] with unit "
                        "stride along the rows is used")
     if dt is not None and code != dt:
         raise MoeError(MOE_EINVAL, f"{name}: {t.dtype}, not the type that it has to agree with")
-    return t.data_ptr(), code, t.stride(0) if rows > 1 else width
+    return t.data_ptr(), code, stride[0] if rows > 1 else width
+
+
+def _vector(t, name, n):
+    """Address of n f32, None of None."""
+    if t is None:
+        return None
+    if t.dtype is not _torch().float32 or t.shape != (n,) or t.stride() != (1,):
+        _exactly(t, name, "f32", 1, n)  # other shapes that hold the same
+    return t.data_ptr()
 
 
 def moe_linear(w, x, bias, act, res, y, stream=None):
@@ -418,22 +424,17 @@ def moe_linear(w, x, bias, act, res, y, stream=None):
     xp, _, x_ld = _rows(x, "x", T, K, wdt)
     rp, rdt, r_ld = _rows(res, "res", T, N)
     yp, ydt, y_ld = _rows(y, "y", T, N)
-    if bias is not None:
-        _exactly(bias, "bias", "f32", 1, N)
+    bp = _vector(bias, "bias", N)
     st = _stream_of(stream, w, x, bias, res, y)
-    _check(lib().moe_linear(wdt, wp, w_ld, N, K, xp, x_ld, T, _ptr(bias), act, rp, rdt, r_ld, yp, ydt, y_ld, st))
+    _check(lib().moe_linear(wdt, wp, w_ld, N, K, xp, x_ld, T, bp, act, rp, rdt, r_ld, yp, ydt, y_ld, st))
 
 
 def _norm(norm, name, H):
-    """(kind, weight, bias) of a norm given as None, (kind, weight) or (kind, weight, bias)."""
+    """(kind, weight, bias, their addresses) of a norm given as None, (kind, weight) or (kind, weight, bias)."""
     if norm is None:
-        return MOE_NORM_NONE, None, None
+        return MOE_NORM_NONE, None, None, None, None
     kind, w, b = norm if len(norm) == 3 else (*norm, None)
-    if w is not None:
-        _exactly(w, name + " weight", "f32", 1, H)
-    if b is not None:
-        _exactly(b, name + " bias", "f32", 1, H)
-    return kind, w, b
+    return kind, w, b, _vector(w, name + " weight", H), _vector(b, name + " bias", H)
 
 
 def moe_block_norm(block, post, gate, block_scale, res, res_scale, pre, eps, res_out, x, stream=None):
@@ -456,15 +457,17 @@ def moe_block_norm(block, post, gate, block_scale, res, res_scale, pre, eps, res
     gp, gdt, g_ld = None, MOE_F32, 0
     if gate is not None:
         if gate.dim() == 1:
-            gp, gdt, _ = _rows(gate.unsqueeze(0), "gate", 1, H)
+            if gate.dtype is _torch_mod.float32:
+                gp = _vector(gate, "gate", H)
+            else:
+                gp, gdt, _ = _rows(gate.unsqueeze(0), "gate", 1, H)
         else:
             gp, gdt, g_ld = _rows(gate, "gate", T, H)
-    post_kind, post_w, post_b = _norm(post, "post norm's", H)
-    pre_kind, pre_w, pre_b = _norm(pre, "pre norm's", H)
+    post_kind, post_w, post_b, post_wp, post_bp = _norm(post, "post norm's", H)
+    pre_kind, pre_w, pre_b, pre_wp, pre_bp = _norm(pre, "pre norm's", H)
     st = _stream_of(stream, block, post_w, post_b, gate, res, pre_w, pre_b, res_out, x)
-    _check(lib().moe_block_norm(bp, bdt, b_ld, post_kind, _ptr(post_w), _ptr(post_b), gp, gdt, g_ld, block_scale, rp, r_ld,
-                                res_scale, pre_kind, _ptr(pre_w), _ptr(pre_b), eps, T, H, op, rdt, o_ld, xp, xdt, x_ld,
-                                st))
+    _check(lib().moe_block_norm(bp, bdt, b_ld, post_kind, post_wp, post_bp, gp, gdt, g_ld, block_scale, rp, r_ld,
+                                res_scale, pre_kind, pre_wp, pre_bp, eps, T, H, op, rdt, o_ld, xp, xdt, x_ld, st))
 
 
 def moe_dispatch_workspace(T, k, E):
@@ -473,7 +476,7 @@ def moe_dispatch_workspace(T, k, E):
 
 def _pairs(t, name, kind, T, k):
     """Refuses t unless it is the [T][k] of the call, contiguous."""
-    if t is None or t.dtype not in _dtypes(kind) or not t.is_contiguous() or t.numel() != T * k:
+    if t is None or t.dtype is not _dtypes(kind)[0] or not t.is_contiguous() or t.numel() != T * k:
         raise MoeError(MOE_EINVAL, f"{name}: " + ("None" if t is None else f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
                        + f", where [{T}][{k}] of {kind} is used, contiguous")
 
