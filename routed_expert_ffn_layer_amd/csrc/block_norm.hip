@@ -23,39 +23,16 @@ namespace {
 
 constexpr int kBnMaxWaves = 16;
 
-// Sums of a and b over the threads of a row; every thread gets them.  `red`: two floats for
-// each wave of the workgroup, of this reduction alone.
-template <bool WAVE_ROW>
-__device__ __forceinline__ void row_sum(float& a, float& b, float (*red)[2]) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    a += __shfl_xor(a, d, 64);
-    b += __shfl_xor(b, d, 64);
-  }
+// `a` reduced over the threads of a row; every thread gets it.  `red`: a float for each wave of the workgroup, of
+// this reduction alone.
+template <bool WAVE_ROW, typename Op>
+__device__ __forceinline__ float row_reduce(float a, Op op, float* red) {
+  a = reduce64(a, op);
   if constexpr (!WAVE_ROW) {
-    const int wv = threadIdx.x >> 6, nw = blockDim.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
-      red[wv][0] = a;
-      red[wv][1] = b;
-    }
+    const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63, nw = blockDim.x >> 6;
+    if (lane == 0) red[wv] = a;
     lds_barrier();
-    a = b = 0.0f;
-    for (int i = 0; i < nw; ++i) {
-      a += red[i][0];
-      b += red[i][1];
-    }
-  }
-}
-
-template <bool WAVE_ROW>
-__device__ __forceinline__ float row_max(float a, float (*red)[2]) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor(a, d, 64));
-  if constexpr (!WAVE_ROW) {
-    const int wv = threadIdx.x >> 6, nw = blockDim.x >> 6;
-    if ((threadIdx.x & 63) == 0) red[wv][0] = a;
-    lds_barrier();
-    for (int i = 0; i < nw; ++i) a = fmaxf(a, red[i][0]);
+    a = reduce16((lane & 15) < nw ? red[lane & 15] : 0.0f, op);  // sums, and maxima of magnitudes: 0 changes neither
   }
   return a;
 }
@@ -64,7 +41,7 @@ __device__ __forceinline__ float row_max(float a, float (*red)[2]) {
 // that a layer norm takes off.
 template <int NV, bool WAVE_ROW>
 __device__ __forceinline__ float statistics(const float (&v)[NV][8], int kind, float s, float eps, int H, int col0,
-                                            int step, float (*red)[kBnMaxWaves][2], float& mean, float& rest) {
+                                            int step, float (*red)[kBnMaxWaves], float& mean, float& rest) {
   // d below and in normalize() have to take off the same rounded mean: no fusing of a * inv_h into v - mean
 #pragma clang fp contract(off)
   const float inv_h = 1.0f / (float)H;
@@ -75,8 +52,7 @@ __device__ __forceinline__ float statistics(const float (&v)[NV][8], int kind, f
     for (int c = 0; c < NV; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) a = fmaf(v[c][i], s, a);  // 0 past the row's end
-    row_sum<WAVE_ROW>(a, b, red[0]);
-    mean = a * inv_h;
+    mean = row_reduce<WAVE_ROW>(a, Add(), red[0]) * inv_h;
     a = b = 0.0f;
 #pragma unroll
     for (int c = 0; c < NV; ++c)
@@ -86,8 +62,8 @@ __device__ __forceinline__ float statistics(const float (&v)[NV][8], int kind, f
         a += d;
         b = fmaf(d, d, b);
       }
-    row_sum<WAVE_ROW>(a, b, red[1]);
-    rest = a * inv_h;
+    rest = row_reduce<WAVE_ROW>(a, Add(), red[1]) * inv_h;
+    b = row_reduce<WAVE_ROW>(b, Add(), red[2]);
     const float var = fmaf(-rest, rest, b * inv_h);
     return (var < 0.0f ? 0.0f : var) + eps;  // a NaN stays one
   }
@@ -98,15 +74,14 @@ __device__ __forceinline__ float statistics(const float (&v)[NV][8], int kind, f
       const float d = v[c][i] * s;
       b = fmaf(d, d, b);
     }
-  row_sum<WAVE_ROW>(a, b, red[0]);
-  return b * inv_h + eps;
+  return row_reduce<WAVE_ROW>(b, Add(), red[0]) * inv_h + eps;
 }
 
 // v <- norm(v) * w (+ b).
 template <int NV, bool WAVE_ROW>
 __device__ __forceinline__ void normalize(float (&v)[NV][8], int kind, const float* __restrict__ w,
                                           const float* __restrict__ b, float eps, int H, int col0, int step,
-                                          float (*red)[kBnMaxWaves][2]) {
+                                          float (*red)[kBnMaxWaves]) {
   float mean, rest, s = 1.0f;
   float q = statistics<NV, WAVE_ROW>(v, kind, 1.0f, eps, H, col0, step, red, mean, rest);
   if (!(q >= 0x1p-90f && q < 0x1p126f)) {  // out of range, infinite or NaN
@@ -115,13 +90,13 @@ __device__ __forceinline__ void normalize(float (&v)[NV][8], int kind, const flo
     for (int c = 0; c < NV; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[c][i]));
-    m = row_max<WAVE_ROW>(m, red[2]);
+    m = row_reduce<WAVE_ROW>(m, Max(), red[3]);
     if (m > 0.0f && m < INFINITY) {  // else the definition's own infinities and NaN
       int e;
       frexpf(m, &e);
       s = ldexpf(1.0f, min(-e, 126));
       const float root = sqrtf(eps) * s;  // at most 1, where s^2 alone may pass the f32 range
-      // red[0] and red[1] again: row_max's barrier came after their last reads
+      // red[0] to red[2] again: the maximum's barrier came after their last reads
       q = statistics<NV, WAVE_ROW>(v, kind, s, root * root, H, col0, step, red, mean, rest);
     }
   }
@@ -147,7 +122,7 @@ __device__ __forceinline__ void normalize(float (&v)[NV][8], int kind, const flo
 // else a row per workgroup.
 template <int NV, bool WAVE_ROW, typename BT, typename RT, typename XT>
 __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void block_norm_kernel(BlockNormArgs a) {
-  __shared__ float red[2][3][kBnMaxWaves][2];
+  __shared__ float red[2][4][kBnMaxWaves];
   const int per_row = WAVE_ROW ? 64 : blockDim.x;
   const int64_t t = WAVE_ROW ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (WAVE_ROW && t >= a.T) return;  // no barriers in this form

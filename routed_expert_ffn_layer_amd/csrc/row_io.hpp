@@ -74,4 +74,35 @@ __device__ __forceinline__ void store8(uint16_t* p, int n, const float (&v)[8]) 
   }
 }
 
+// Reductions over lanes without the trip through LDS that a general shuffle takes: within 16 lanes by
+// data-parallel permutes (exchange with lane ^ 1, ^ 2, then mirrored over 8 and 16 lanes, whose halves agree by
+// then), across them by swapping 16- and 32-lane halves.  Every lane gets the result.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+struct Add {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+template <typename Op>
+__device__ __forceinline__ float reduce16(float v, Op op) {
+  v = op(v, dpp<0xb1>(v));   // quad_perm 1 0 3 2
+  v = op(v, dpp<0x4e>(v));   // quad_perm 2 3 0 1
+  v = op(v, dpp<0x141>(v));  // row_half_mirror
+  return op(v, dpp<0x140>(v));  // row_mirror
+}
+template <typename Op>
+__device__ __forceinline__ float reduce64(float v, Op op) {
+  v = reduce16(v, op);
+  const uint32_t a = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  v = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  const uint32_t b = __float_as_uint(v);
+  const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return op(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
 }  // namespace moe
