@@ -77,12 +77,12 @@ __device__ __forceinline__ float statistics(const float (&v)[NV][8], int kind, f
   return row_reduce<WAVE_ROW>(b, Add(), red[0]) * inv_h + eps;
 }
 
-// v <- norm(v) * w (+ b).
+// v <- norm(v) * w (+ b); elements past the row's end stay 0.
 template <int NV, bool WAVE_ROW>
 __device__ __forceinline__ void normalize(float (&v)[NV][8], int kind, const float* __restrict__ w,
                                           const float* __restrict__ b, float eps, int H, int col0, int step,
                                           float (*red)[kBnMaxWaves]) {
-  float mean, rest, s = 1.0f;
+  float mean, rest;
   float q = statistics<NV, WAVE_ROW>(v, kind, 1.0f, eps, H, col0, step, red, mean, rest);
   if (!(q >= 0x1p-90f && q < 0x1p126f)) {  // out of range, infinite or NaN
     float m = sqrtf(eps);
@@ -94,26 +94,42 @@ __device__ __forceinline__ void normalize(float (&v)[NV][8], int kind, const flo
     if (m > 0.0f && m < INFINITY) {  // else the definition's own infinities and NaN
       int e;
       frexpf(m, &e);
-      s = ldexpf(1.0f, min(-e, 126));
+      const float s = ldexpf(1.0f, min(-e, 126));
       const float root = sqrtf(eps) * s;  // at most 1, where s^2 alone may pass the f32 range
       // red[0] to red[2] again: the maximum's barrier came after their last reads
       q = statistics<NV, WAVE_ROW>(v, kind, s, root * root, H, col0, step, red, mean, rest);
+#pragma unroll
+      for (int c = 0; c < NV; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] *= s;
     }
   }
   const float inv = 1.0f / sqrtf(q);
+  if (kind == kNormLayer) {
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = col0 + c * step + i < H ? (v[c][i] - mean - rest) * inv : 0.0f;
+  } else {
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] *= inv;
+  }
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
     const int col = col0 + c * step, n = H - col;
     if (n <= 0) continue;
-    float wv[8], bv[8];
-    if (w) load8(w + col, n, wv);
-    if (b) load8(b + col, n, bv);
+    float wv[8];
+    if (w) {
+      load8(w + col, n, wv);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float u = (fmaf(v[c][i], s, -mean) - rest) * inv;
-      if (w) u *= wv[i];
-      if (b) u += bv[i];
-      v[c][i] = i < n ? u : 0.0f;
+      for (int i = 0; i < 8; ++i) v[c][i] *= wv[i];
+    }
+    if (b) {
+      load8(b + col, n, wv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] += wv[i];
     }
   }
 }
