@@ -44,6 +44,35 @@ __device__ __forceinline__ void load8(const uint16_t* p, int n, float (&v)[8]) {
   }
 }
 
+// load8 in two halves: what memory holds, and its values, so that several loads can be on their way.
+template <typename E>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  u32x4 a;
+  __device__ __forceinline__ void load(const uint16_t* p, int n) {
+    if (n >= 8) {
+      a = *reinterpret_cast<const u32x4_any*>(p);
+    } else {
+      a = u32x4{0, 0, 0, 0};
+      if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          a[i] = (2 * i < n ? p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+      }
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    return __uint_as_float(i & 1 ? a[i / 2] & 0xffff0000u : a[i / 2] << 16);
+  }
+};
+template <>
+struct Raw8<float> {
+  float v[8];
+  __device__ __forceinline__ void load(const float* p, int n) { load8(p, n, v); }
+  __device__ __forceinline__ float operator[](int i) const { return v[i]; }
+};
+
 // Two f32 to two bf16, round to nearest even (the conversion instruction of gfx950).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const bf16x2 v = {(__bf16)lo, (__bf16)hi};

@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(DispatchArgs a, in
     const int e = i * kPlaceThreads + threadIdx.x;
     before[i] = all[i] = 0;
     if (e < E) {
-#pragma unroll 8
+#pragma unroll 32  // loads in flight: the table's columns are the launch's longest chain
       for (int q = 0; q < nb; ++q) {
         const int c = table[q * E + e];
         all[i] += c;
@@ -236,35 +236,50 @@ __global__ __launch_bounds__(256) void gather_kernel(DispatchArgs a) {
   }
 }
 
-// y[t] = sum_j w[t][j] rows[inv[t][j]] (w null: 1), j ascending, f32.
+// A token's pairs, lane j holding pair j (k <= 32): its place, -1 where it has none, and its weight.
+struct Pairs {
+  int place;
+  float weight;
+  __device__ __forceinline__ Pairs(const CombineRowsArgs& a, int64_t t) {
+    const int lane = threadIdx.x & 63;
+    const int p = lane < a.k ? a.inv_rows[t * a.k + lane] : -1;
+    place = (unsigned)p < (unsigned)a.n_rows ? p : -1;
+    weight = a.topk_w && lane < a.k ? a.topk_w[t * a.k + lane] : 1.0f;
+  }
+  // The whole wave's view of pair j, as scalars.  Only where all lanes are active: a lane that has left a loop
+  // need not hold its pair any more.
+  __device__ __forceinline__ int at(int j) const { return __builtin_amdgcn_readlane(place, j); }
+  __device__ __forceinline__ float w(int j) const {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), j));
+  }
+};
+
+// y[t] = sum_j w[t][j] rows[inv[t][j]] (w null: 1), j ascending, f32.  The rows of 8 pairs are on their way
+// together.
 template <typename RT, typename YT, int G>
 __global__ __launch_bounds__(256) void combine_rows_kernel(CombineRowsArgs a) {
-  const int64_t t = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  const int64_t t = (int64_t)blockIdx.x * (256 / G) + uniform(threadIdx.x / 64) / (G / 64);
   if (t >= a.T) return;
-  const int32_t* inv = a.inv_rows + t * a.k;
-  const float* w = a.topk_w ? a.topk_w + t * a.k : nullptr;
+  const Pairs pairs(a, t);
   const RT* rows = static_cast<const RT*>(a.rows);
   YT* y = static_cast<YT*>(a.y) + t * a.y_ld;
-  for (int col = threadIdx.x % G * 8; col < a.H; col += G * 8) {
-    const int n = a.H - col;
+  for (int col0 = 0; col0 < a.H; col0 += G * 8) {  // all lanes stay in: those past the row's end have n <= 0
+    const int col = col0 + threadIdx.x % G * 8, n = a.H - col;
     float acc[8] = {};
-    // the indices, weights and rows of 4 pairs are on their way together
-    for (int j0 = 0; j0 < a.k; j0 += 4) {
-      int p[4];
-      float wj[4], v[4][8];
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+      Raw8<RT> v[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        p[u] = j0 + u < a.k ? inv[j0 + u] : -1;
-        wj[u] = w && j0 + u < a.k ? w[j0 + u] : 1.0f;
+      for (int u = 0; u < 8; ++u) {
+        const int p = pairs.at(j0 + u);
+        if (p >= 0) v[u].load(rows + (int64_t)p * a.rows_ld + col, n);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if ((unsigned)p[u] < (unsigned)a.n_rows) load8(rows + (int64_t)p[u] * a.rows_ld + col, n, v[u]);
+      for (int u = 0; u < 8; ++u) {
+        const int p = pairs.at(j0 + u);
+        const float w = pairs.w(j0 + u);
+        if (p < 0) continue;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if ((unsigned)p[u] >= (unsigned)a.n_rows) continue;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(wj[u], v[u][i], acc[i]);
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, v[u][i], acc[i]);
       }
     }
     store8(y + col, n, acc);
@@ -274,63 +289,53 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(CombineRowsArgs a) {
 // d_rows[p] = w dy[t], d_w = <dy[t], rows[p]> for the pairs of a token, p = inv[t][j].
 template <typename YT, typename RT, int G>
 __global__ __launch_bounds__(256) void combine_rows_backward_kernel(CombineRowsArgs a) {
-  __shared__ float s_dot[4][4];
-  const int64_t t = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  __shared__ float s_dot[4][8];
+  const int wv = uniform(threadIdx.x / 64), lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * (256 / G) + wv / (G / 64);
   if (G == 64 && t >= a.T) return;  // no barriers in this form
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int32_t* inv = a.inv_rows + t * a.k;
-  const float* w = a.topk_w + t * a.k;
+  const Pairs pairs(a, t);
   const YT* dy = static_cast<const YT*>(a.y) + t * a.y_ld;
   const RT* rows = static_cast<const RT*>(a.rows);
   RT* d_rows = static_cast<RT*>(a.d_rows);
-  for (int j0 = 0; j0 < a.k; j0 += 4) {
-    int p[4];
-    float wj[4], dot[4] = {};
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    float dot[8] = {};
+    for (int col0 = 0; col0 < a.H; col0 += G * 8) {  // all lanes stay in
+      const int col = col0 + threadIdx.x % G * 8, n = a.H - col;
+      Raw8<RT> v[8];
+      float d[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      p[u] = j0 + u < a.k ? inv[j0 + u] : -1;
-      if (p[u] >= a.n_rows) p[u] = -1;
-      wj[u] = j0 + u < a.k ? w[j0 + u] : 0.0f;
-    }
-    for (int col = threadIdx.x % G * 8; col < a.H; col += G * 8) {
-      const int n = a.H - col;
-      float d[8], v[4][8];
-      load8(dy + col, n, d);  // from the caches for the second four pairs on
+      for (int u = 0; u < 8; ++u) {
+        const int p = pairs.at(j0 + u);
+        if (p >= 0) v[u].load(rows + (int64_t)p * a.rows_ld + col, n);
+      }
+      load8(dy + col, n, d);  // from the caches for the second eight pairs on
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (p[u] >= 0) load8(rows + (int64_t)p[u] * a.rows_ld + col, n, v[u]);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (p[u] < 0) continue;
+      for (int u = 0; u < 8; ++u) {
+        const int p = pairs.at(j0 + u);
+        const float w = pairs.w(j0 + u);
+        if (p < 0) continue;
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           dot[u] = fmaf(d[i], v[u][i], dot[u]);  // both 0 past the row's end
-          o[i] = wj[u] * d[i];
+          o[i] = w * d[i];
         }
-        store8(d_rows + (int64_t)p[u] * a.dr_ld + col, n, o);
+        store8(d_rows + (int64_t)p * a.dr_ld + col, n, o);
       }
     }
+    float mine = 0.0f;  // lane u: pair j0 + u
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int s = 32; s >= 1; s >>= 1) dot[u] += __shfl_xor(dot[u], s, 64);
-    if constexpr (G == 64) {
-      if (lane < 4 && j0 + lane < a.k) {
-        const float v = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
-        a.d_w[t * a.k + j0 + lane] = v;
-      }
-    } else {
-      if (lane == 0) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) s_dot[wv][u] = dot[u];
-      }
+    for (int u = 0; u < 8; ++u) {
+      const float s = reduce64(dot[u], Add());
+      mine = lane == u ? s : mine;
+    }
+    if constexpr (G > 64) {
+      if (lane < 8) s_dot[wv][lane] = mine;
       __syncthreads();
-      if (threadIdx.x < 4 && j0 + threadIdx.x < a.k)
-        a.d_w[t * a.k + j0 + threadIdx.x] =
-            (s_dot[0][threadIdx.x] + s_dot[1][threadIdx.x]) + (s_dot[2][threadIdx.x] + s_dot[3][threadIdx.x]);
+      if (lane < 8) mine = (s_dot[0][lane] + s_dot[1][lane]) + (s_dot[2][lane] + s_dot[3][lane]);
       __syncthreads();
     }
+    if (threadIdx.x % G < 8 && j0 + lane < a.k) a.d_w[t * a.k + j0 + lane] = mine;
   }
 }
 
@@ -345,8 +350,7 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const int32_t* __res
   const int id = lane < k ? ids[t * k + lane] : -1;
   const float wj = lane < k ? w[t * k + lane] : 0.0f, dj = lane < k ? d_w[t * k + lane] : 0.0f;
   float s = wj * dj;
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d, 64);
+  s = reduce64(s, Add());
   const float g = wj * (dj - s);
   for (int e = lane; e - lane < E; e += 64) {
     float v = 0.0f;
@@ -359,8 +363,9 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const int32_t* __res
   }
 }
 
-// Threads a token: a wave where there are enough tokens to fill the chip, or a row is short.
-inline bool wave_rows(int T, int H) { return T >= 2048 || H <= 512; }
+// Threads a token: a wave for short rows, else a workgroup.  There and back and gradients (us): 4096 tokens of 2048
+// and 4096 bf16 105 + 116 in workgroups, 126 + 127 in waves; 8192 tokens of 1024 37 + 32 in waves, 45 + 35 in workgroups.
+inline bool wave_rows(int H) { return H <= 1024; }
 
 }  // namespace
 
@@ -383,7 +388,7 @@ hipError_t launch_dispatch(const DispatchArgs& a, int32_t* table, bool bf16, hip
   const int chunk = chunk_pairs(n), nb = (n + chunk - 1) / chunk;
   hipLaunchKernelGGL(count_kernel, dim3(nb), dim3(kPlaceThreads), 0, st, a, chunk, table);
   hipLaunchKernelGGL(place_kernel, dim3(nb), dim3(kPlaceThreads), 0, st, a, chunk, table);
-  if (wave_rows(a.T, a.H)) {
+  if (wave_rows(a.H)) {
     const dim3 grid((unsigned)((a.T + 3) / 4));
     if (bf16)
       hipLaunchKernelGGL((gather_kernel<uint16_t, 64>), grid, dim3(256), 0, st, a);
@@ -401,7 +406,7 @@ namespace {
 
 template <typename RT, typename YT>
 hipError_t combine_typed(const CombineRowsArgs& a, hipStream_t st) {
-  if (wave_rows(a.T, a.H))
+  if (wave_rows(a.H))
     hipLaunchKernelGGL((combine_rows_kernel<RT, YT, 64>), dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
   else
     hipLaunchKernelGGL((combine_rows_kernel<RT, YT, 256>), dim3(a.T), dim3(256), 0, st, a);
@@ -410,7 +415,7 @@ hipError_t combine_typed(const CombineRowsArgs& a, hipStream_t st) {
 
 template <typename YT, typename RT>
 hipError_t backward_typed(const CombineRowsArgs& a, hipStream_t st) {
-  if (wave_rows(a.T, a.H))
+  if (wave_rows(a.H))
     hipLaunchKernelGGL((combine_rows_backward_kernel<YT, RT, 64>), dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
   else
     hipLaunchKernelGGL((combine_rows_backward_kernel<YT, RT, 256>), dim3(a.T), dim3(256), 0, st, a);
