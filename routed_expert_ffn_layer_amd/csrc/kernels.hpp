@@ -138,9 +138,10 @@ struct DispatchArgs {
   void* rows;  // n_rows rows of H, rows_ld elements apart
   int64_t x_ld, rows_ld;
   int T, k, E, H, n_rows;
+  bool pass;  // set by the launcher: rows are written past the caches
 };
 size_t dispatch_workspace_bytes(int T, int k, int E);
-hipError_t launch_dispatch(const DispatchArgs& a, int32_t* table, bool bf16, hipStream_t st);
+hipError_t launch_dispatch(DispatchArgs a, int32_t* table, bool bf16, hipStream_t st);
 struct CombineRowsArgs {
   const void* rows;       // n_rows rows of H, rows_ld elements apart
   const float* topk_w;    // [T][k]; the forward sum: null for weights of 1
@@ -150,9 +151,10 @@ struct CombineRowsArgs {
   float* d_w;             // backward: [T][k]
   int64_t rows_ld, y_ld, dr_ld;
   int T, k, H, n_rows;
+  bool pass;              // backward, set by the launcher: d_rows are written past the caches
 };
 hipError_t launch_combine_rows(const CombineRowsArgs& a, bool rows_bf16, bool y_bf16, hipStream_t st);
-hipError_t launch_combine_rows_backward(const CombineRowsArgs& a, bool dy_bf16, bool rows_bf16, hipStream_t st);
+hipError_t launch_combine_rows_backward(CombineRowsArgs a, bool dy_bf16, bool rows_bf16, hipStream_t st);
 hipError_t launch_gate_backward(const int32_t* ids, const float* w, const float* d_w, int T, int E, int k,
                                 float* d_logits, hipStream_t st);
 

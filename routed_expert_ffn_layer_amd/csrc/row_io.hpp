@@ -15,6 +15,22 @@ typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
+// One vector from and to memory; PASS: past the caches, for what is not read again soon.
+template <bool PASS, typename V, typename P>
+__device__ __forceinline__ void put(P* p, V v) {
+  if constexpr (PASS)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+template <bool PASS, typename P>
+__device__ __forceinline__ auto get(const P* p) {
+  if constexpr (PASS)
+    return __builtin_nontemporal_load(p);
+  else
+    return *p;
+}
+
 // Eight elements from p; those at n and beyond are not read and are 0.
 __device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
   if (n >= 8) {
@@ -44,15 +60,17 @@ __device__ __forceinline__ void load8(const uint16_t* p, int n, float (&v)[8]) {
   }
 }
 
-// load8 in two halves: what memory holds, and its values, so that several loads can be on their way.
+// load8 in two halves: what memory holds, and its values, so that several loads can be on their way.  PASS: past
+// the caches, for rows that are read once.
 template <typename E>
 struct Raw8;
 template <>
 struct Raw8<uint16_t> {
   u32x4 a;
+  template <bool PASS>
   __device__ __forceinline__ void load(const uint16_t* p, int n) {
     if (n >= 8) {
-      a = *reinterpret_cast<const u32x4_any*>(p);
+      a = get<PASS>(reinterpret_cast<const u32x4_any*>(p));
     } else {
       a = u32x4{0, 0, 0, 0};
       if (n > 0) {
@@ -69,7 +87,20 @@ struct Raw8<uint16_t> {
 template <>
 struct Raw8<float> {
   float v[8];
-  __device__ __forceinline__ void load(const float* p, int n) { load8(p, n, v); }
+  template <bool PASS>
+  __device__ __forceinline__ void load(const float* p, int n) {
+    if (n >= 8) {
+      const f32x4 lo = get<PASS>(reinterpret_cast<const f32x4_any*>(p)), hi = get<PASS>(reinterpret_cast<const f32x4_any*>(p + 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = lo[i];
+        v[4 + i] = hi[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+    }
+  }
   __device__ __forceinline__ float operator[](int i) const { return v[i]; }
 };
 
@@ -79,10 +110,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+template <bool PASS = false>
 __device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
   if (n >= 8) {
-    *reinterpret_cast<f32x4_any*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4_any*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    put<PASS>(reinterpret_cast<f32x4_any*>(p), f32x4{v[0], v[1], v[2], v[3]});
+    put<PASS>(reinterpret_cast<f32x4_any*>(p + 4), f32x4{v[4], v[5], v[6], v[7]});
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -90,12 +122,13 @@ __device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
   }
 }
 
+template <bool PASS = false>
 __device__ __forceinline__ void store8(uint16_t* p, int n, const float (&v)[8]) {
   u32x4 a;
 #pragma unroll
   for (int i = 0; i < 4; ++i) a[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
   if (n >= 8) {
-    *reinterpret_cast<u32x4_any*>(p) = a;
+    put<PASS>(reinterpret_cast<u32x4_any*>(p), a);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

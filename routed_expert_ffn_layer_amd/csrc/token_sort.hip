@@ -16,6 +16,8 @@
 #include "kernels.hpp"
 #include "row_io.hpp"
 
+#include <algorithm>
+
 namespace moe {
 
 namespace {
@@ -31,7 +33,7 @@ inline int chunk_pairs(int n) {  // n <= 2^30
 }
 
 // Copies the 16-byte group at column col of a row of H elements (fewer at the row's end) to k rows.
-template <typename E_, int GROUP = 16 / sizeof(E_)>
+template <bool PASS, typename E_, int GROUP = 16 / sizeof(E_)>
 __device__ __forceinline__ void copy_group(const E_* __restrict__ src, E_* __restrict__ rows, int64_t rows_ld,
                                            const int* dest, int k, int col, int H) {
   typedef E_ Vec __attribute__((ext_vector_type(GROUP)));
@@ -42,7 +44,7 @@ __device__ __forceinline__ void copy_group(const E_* __restrict__ src, E_* __res
 #pragma unroll
     for (int j = 0; j < k; ++j) {
       const int p = dest[j];
-      if (p >= 0) *reinterpret_cast<Any*>(rows + (int64_t)p * rows_ld + col) = v;
+      if (p >= 0) put<PASS>(reinterpret_cast<Any*>(rows + (int64_t)p * rows_ld + col), v);
     }
   } else {
     for (int i = 0; i < n; ++i) {
@@ -98,7 +100,7 @@ __global__ __launch_bounds__(256) void dispatch_small_kernel(DispatchArgs a) {
   __syncthreads();
   const E_* src = static_cast<const E_*>(a.x) + t * a.x_ld;
   for (int col = threadIdx.x * (16 / sizeof(E_)); col < a.H; col += 256 * (16 / sizeof(E_)))
-    copy_group(src, static_cast<E_*>(a.rows), a.rows_ld, s_dest, a.k, col, a.H);
+    copy_group<false>(src, static_cast<E_*>(a.rows), a.rows_ld, s_dest, a.k, col, a.H);
 }
 
 // Counts of the ids of chunk blockIdx.x -> table[chunk][E].
@@ -231,8 +233,12 @@ __global__ __launch_bounds__(256) void gather_kernel(DispatchArgs a) {
       dest[u] = j0 + u < a.k ? inv[j0 + u] : -1;
       if (dest[u] >= a.n_rows) dest[u] = -1;
     }
-    for (int col = threadIdx.x % G * V; col < a.H; col += G * V)
-      copy_group(src, static_cast<E_*>(a.rows), a.rows_ld, dest, 8, col, a.H);
+    for (int col = threadIdx.x % G * V; col < a.H; col += G * V) {
+      if (a.pass)
+        copy_group<true>(src, static_cast<E_*>(a.rows), a.rows_ld, dest, 8, col, a.H);
+      else
+        copy_group<false>(src, static_cast<E_*>(a.rows), a.rows_ld, dest, 8, col, a.H);
+    }
   }
 }
 
@@ -256,7 +262,7 @@ struct Pairs {
 
 // y[t] = sum_j w[t][j] rows[inv[t][j]] (w null: 1), j ascending, f32.  The rows of 8 pairs are on their way
 // together.
-template <typename RT, typename YT, int G>
+template <typename RT, typename YT, int G, bool PASS>
 __global__ __launch_bounds__(256) void combine_rows_kernel(CombineRowsArgs a) {
   const int64_t t = (int64_t)blockIdx.x * (256 / G) + uniform(threadIdx.x / 64) / (G / 64);
   if (t >= a.T) return;
@@ -271,7 +277,7 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(CombineRowsArgs a) {
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int p = pairs.at(j0 + u);
-        if (p >= 0) v[u].load(rows + (int64_t)p * a.rows_ld + col, n);
+        if (p >= 0) v[u].template load<PASS>(rows + (int64_t)p * a.rows_ld + col, n);
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
@@ -287,7 +293,7 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(CombineRowsArgs a) {
 }
 
 // d_rows[p] = w dy[t], d_w = <dy[t], rows[p]> for the pairs of a token, p = inv[t][j].
-template <typename YT, typename RT, int G>
+template <typename YT, typename RT, int G, bool PASS>
 __global__ __launch_bounds__(256) void combine_rows_backward_kernel(CombineRowsArgs a) {
   __shared__ float s_dot[4][8];
   const int wv = uniform(threadIdx.x / 64), lane = threadIdx.x & 63;
@@ -306,7 +312,7 @@ __global__ __launch_bounds__(256) void combine_rows_backward_kernel(CombineRowsA
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int p = pairs.at(j0 + u);
-        if (p >= 0) v[u].load(rows + (int64_t)p * a.rows_ld + col, n);
+        if (p >= 0) v[u].template load<PASS>(rows + (int64_t)p * a.rows_ld + col, n);
       }
       load8(dy + col, n, d);  // from the caches for the second eight pairs on
 #pragma unroll
@@ -320,7 +326,10 @@ __global__ __launch_bounds__(256) void combine_rows_backward_kernel(CombineRowsA
           dot[u] = fmaf(d[i], v[u][i], dot[u]);  // both 0 past the row's end
           o[i] = w * d[i];
         }
-        store8(d_rows + (int64_t)p * a.dr_ld + col, n, o);
+        if (a.pass)
+          store8<true>(d_rows + (int64_t)p * a.dr_ld + col, n, o);
+        else
+          store8(d_rows + (int64_t)p * a.dr_ld + col, n, o);
       }
     }
     float mine = 0.0f;  // lane u: pair j0 + u
@@ -363,6 +372,14 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const int32_t* __res
   }
 }
 
+// Rows that pass the caches by.  Reading: rows of more than the 32 MB of the L2s, read once here (1024 tokens from 6144 rows of 4096
+// bf16 that memory holds 42 -> 34 us, that the last-level cache still holds 33 -> 34).  Writing: more than half of
+// the 256 MB of the last-level cache, which the next reader finds in memory either way (24576 rows of 4096 bf16
+// there and back: 103 -> 90 us).
+inline int64_t row_bytes(int64_t rows, int H, bool bf16) { return rows * H * (bf16 ? 2 : 4); }
+inline bool read_past(int64_t bytes) { return bytes > (int64_t)32 << 20; }
+inline bool write_past(int64_t bytes) { return bytes > (int64_t)128 << 20; }
+
 // Threads a token: a wave for short rows, else a workgroup.  There and back and gradients (us): 4096 tokens of 2048
 // and 4096 bf16 105 + 116 in workgroups, 126 + 127 in waves; 8192 tokens of 1024 37 + 32 in waves, 45 + 35 in workgroups.
 inline bool wave_rows(int H) { return H <= 1024; }
@@ -376,8 +393,9 @@ size_t dispatch_workspace_bytes(int T, int k, int E) {
   return (size_t)((n + chunk - 1) / chunk) * E * sizeof(int32_t);
 }
 
-hipError_t launch_dispatch(const DispatchArgs& a, int32_t* table, bool bf16, hipStream_t st) {
+hipError_t launch_dispatch(DispatchArgs a, int32_t* table, bool bf16, hipStream_t st) {
   const int n = a.T * a.k;
+  a.pass = write_past(row_bytes(std::min(n, a.n_rows), a.H, bf16));
   if (n <= kSmallPairs) {
     if (bf16)
       hipLaunchKernelGGL(dispatch_small_kernel<uint16_t>, dim3(a.T > 0 ? a.T : 1), dim3(256), 0, st, a);
@@ -404,34 +422,50 @@ hipError_t launch_dispatch(const DispatchArgs& a, int32_t* table, bool bf16, hip
 
 namespace {
 
-template <typename RT, typename YT>
+template <typename RT, typename YT, bool PASS>
 hipError_t combine_typed(const CombineRowsArgs& a, hipStream_t st) {
   if (wave_rows(a.H))
-    hipLaunchKernelGGL((combine_rows_kernel<RT, YT, 64>), dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((combine_rows_kernel<RT, YT, 64, PASS>), dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((combine_rows_kernel<RT, YT, 256>), dim3(a.T), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((combine_rows_kernel<RT, YT, 256, PASS>), dim3(a.T), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
-template <typename YT, typename RT>
+template <typename YT, typename RT, bool PASS>
 hipError_t backward_typed(const CombineRowsArgs& a, hipStream_t st) {
   if (wave_rows(a.H))
-    hipLaunchKernelGGL((combine_rows_backward_kernel<YT, RT, 64>), dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((combine_rows_backward_kernel<YT, RT, 64, PASS>), dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((combine_rows_backward_kernel<YT, RT, 256>), dim3(a.T), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((combine_rows_backward_kernel<YT, RT, 256, PASS>), dim3(a.T), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_combine_rows(const CombineRowsArgs& a, bool rows_bf16, bool y_bf16, hipStream_t st) {
-  if (rows_bf16) return y_bf16 ? combine_typed<uint16_t, uint16_t>(a, st) : combine_typed<uint16_t, float>(a, st);
-  return y_bf16 ? combine_typed<float, uint16_t>(a, st) : combine_typed<float, float>(a, st);
+  typedef uint16_t B;
+  typedef float F;
+  const bool pass = read_past(row_bytes(std::min(a.T * a.k, a.n_rows), a.H, rows_bf16));
+  if (rows_bf16) {
+    if (y_bf16) return pass ? combine_typed<B, B, true>(a, st) : combine_typed<B, B, false>(a, st);
+    return pass ? combine_typed<B, F, true>(a, st) : combine_typed<B, F, false>(a, st);
+  }
+  if (y_bf16) return pass ? combine_typed<F, B, true>(a, st) : combine_typed<F, B, false>(a, st);
+  return pass ? combine_typed<F, F, true>(a, st) : combine_typed<F, F, false>(a, st);
 }
 
-hipError_t launch_combine_rows_backward(const CombineRowsArgs& a, bool dy_bf16, bool rows_bf16, hipStream_t st) {
-  if (dy_bf16) return rows_bf16 ? backward_typed<uint16_t, uint16_t>(a, st) : backward_typed<uint16_t, float>(a, st);
-  return rows_bf16 ? backward_typed<float, uint16_t>(a, st) : backward_typed<float, float>(a, st);
+hipError_t launch_combine_rows_backward(CombineRowsArgs a, bool dy_bf16, bool rows_bf16, hipStream_t st) {
+  typedef uint16_t B;
+  typedef float F;
+  const int64_t bytes = row_bytes(std::min(a.T * a.k, a.n_rows), a.H, rows_bf16);
+  const bool pass = read_past(bytes);
+  a.pass = write_past(bytes);
+  if (dy_bf16) {
+    if (rows_bf16) return pass ? backward_typed<B, B, true>(a, st) : backward_typed<B, B, false>(a, st);
+    return pass ? backward_typed<B, F, true>(a, st) : backward_typed<B, F, false>(a, st);
+  }
+  if (rows_bf16) return pass ? backward_typed<F, B, true>(a, st) : backward_typed<F, B, false>(a, st);
+  return pass ? backward_typed<F, F, true>(a, st) : backward_typed<F, F, false>(a, st);
 }
 
 hipError_t launch_gate_backward(const int32_t* ids, const float* w, const float* d_w, int T, int E, int k,
