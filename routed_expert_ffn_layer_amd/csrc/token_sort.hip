@@ -372,10 +372,11 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const int32_t* __res
   }
 }
 
-// Rows that pass the caches by.  Reading: rows of more than the 32 MB of the L2s, read once here (1024 tokens from 6144 rows of 4096
-// bf16 that memory holds 42 -> 34 us, that the last-level cache still holds 33 -> 34).  Writing: more than half of
-// the 256 MB of the last-level cache, which the next reader finds in memory either way (24576 rows of 4096 bf16
-// there and back: 103 -> 90 us).
+// Rows that pass the caches by.  Reading: rows of more than the 32 MB of the L2s, read once here (1024 tokens from
+// 6144 rows of 4096 bf16 that memory holds 42 -> 34 us, that the last-level cache still holds 33 -> 34).  Writing:
+// rows of more than half the 256 MB of the last-level cache (24576 rows of 4096 there and back: 103 -> 90 us).  Up to
+// there the next reader loses more than the call gains: gradients of 16384 rows of 4096 30.0 and 30.4 us, with a
+// copy of them behind 49 and 57; of 32768 rows of 2048 91 and 106.
 inline int64_t row_bytes(int64_t rows, int H, bool bf16) { return rows * H * (bf16 ? 2 : 4); }
 inline bool read_past(int64_t bytes) { return bytes > (int64_t)32 << 20; }
 inline bool write_past(int64_t bytes) { return bytes > (int64_t)128 << 20; }

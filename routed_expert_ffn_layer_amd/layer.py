@@ -37,6 +37,18 @@ class LayerBuffers:
         self.addr_inplace = torch.empty(E, dtype=torch.int64, device=dev)
 
 
+class BlockBuffers(LayerBuffers):
+    """LayerBuffers and what `forward_block` needs besides: the router's logits, the layer's input and
+    the next block's."""
+
+    def __init__(self, T, E, k, H, I, wdt, I_shared=0, device="cuda"):
+        super().__init__(T, E, k, H, I, wdt, I_shared, device)
+        dev, dt = self.y.device, self.y.dtype
+        self.logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        self.x = torch.empty((T, H), dtype=dt, device=dev)
+        self.x_next = torch.empty((T, H), dtype=dt, device=dev)
+
+
 def identity_slots(E, device="cuda"):
     """Slot table of an all-resident layer: expert e lives in slot e."""
     return torch.arange(E, dtype=torch.int32, device=device)
@@ -74,6 +86,35 @@ def forward_decode(b: LayerBuffers, logits, x, slot_pool, slot_stride, slot_of_e
                          b.I_shared if shared_w is not None else 0, x, logits, b.T, b.k, b.E, b.H, b.I, b.topk_ids,
                          b.topk_w, b.y, b.ydt, b.workspace, stream)
     return b.y
+
+
+def few_tokens(b: LayerBuffers):
+    """Whether `forward_decode` is the faster form of `forward` for these buffers."""
+    return (b.T <= 40 and b.T * b.k <= moe.MOE_LAYER_DECODE_MAX_PAIRS and b.wdt in (moe.MOE_BF16, moe.MOE_MXFP4)
+            and b.H <= 65536)
+
+
+def forward_block(b: BlockBuffers, res, w_router, pre, post, slot_pool, slot_stride, slot_of_expert, shared_w=None,
+                  gate=None, block_scale=1.0, res_scale=1.0, next_pre=None, eps=1e-6, x=None, stream=None):
+    """The layer as a block of a model, on the residual stream res [T][H] (f32 or bf16), which is updated in place:
+
+        x = norm_pre(res);  y = layer(x), routed by x . w_router^T;
+        res = res_scale * res + block_scale * gate * norm_post(y)
+
+    pre, post: norms as moe_block_norm takes them, None for none; w_router [E][H] of the activations' type
+    (f32 for f32 experts, else bf16); gate [H], [T][H] or None.  x: the layer's input where the block before
+    has made it (its next_pre), pre is not looked at then.  With next_pre the norm of the next block is taken in
+    the same call, and its input, b.x_next, returned; otherwise res is.  The whole block is 4 calls of the
+    library for up to 40 tokens (few_tokens), 6 above."""
+    if x is None:
+        moe.moe_block_norm(None, None, None, 1.0, res, 1.0, pre, eps, None, b.x, stream)
+        x = b.x
+    moe.moe_linear(w_router, x, None, moe.MOE_ACT_NONE, None, b.logits, stream)
+    run = forward_decode if few_tokens(b) else forward
+    y = run(b, b.logits, x, slot_pool, slot_stride, slot_of_expert, shared_w, stream)
+    moe.moe_block_norm(y, post, gate, block_scale, res, res_scale, next_pre, eps, res,
+                       b.x_next if next_pre is not None else None, stream)
+    return res if next_pre is None else b.x_next
 
 
 def forward_cached(b: LayerBuffers, cache: moe.MoeCache, layer, logits, x, slot_pool, slot_stride, shared_w=None,
