@@ -449,7 +449,7 @@ int moe_w4_linear(int fmt, const void* w, int N, int K, int group, const void* x
  *   res   T rows of N of rdt, r_ld apart, or NULL; may be y itself (same start, type and stride)
  *   y     T rows of N of ydt, y_ld apart; apart from that overlaps no operand (MOE_EINVAL)
  * K, w_ld and x_ld multiples of 8 (bf16) or 4 (f32), K, w_ld and x_ld at most 2^20; y_ld and r_ld
- * any; T and N at most 2^22, T * N at most 2^35.  Products of bf16 are exact, sums are in f32 in an
+ * any (up to 2^36); T and N at most 2^22, T * N at most 2^35.  Products of bf16 are exact, sums are in f32 in an
  * order that the shape fixes, bias, activation and residual are applied in f32 before the one
  * rounding to ydt; f32 weights are multiplied in f32.  The erf inside GELU is within 1.5e-7.
  * Asynchronous, no workspace, may be captured into a graph. */
@@ -471,7 +471,7 @@ int moe_linear(int wdt, const void* w, int64_t w_ld, int N, int K, const void* x
  *   x        T rows of xdt, x_ld apart; NULL: no next norm.  Of the f32 r', not of its rounding
  * Results may lie on block, res or a gate of T rows where start, type and stride agree (in place);
  * any other overlap is refused, as far as the addresses show it.  1 <= H <= 32768 (MOE_EUNSUPPORTED
- * beyond), T <= 2^21, strides any from H on, eps >= 0.  Statistics in f32, exact to its rounding over
+ * beyond), T <= 2^21, strides any from H on (up to 2^36), eps >= 0.  Statistics in f32, exact to its rounding over
  * the whole range of the types.  Asynchronous, no workspace, may be captured. */
 enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 };
 int moe_block_norm(const void* block, int bdt, int64_t b_ld, int post_kind, const float* post_w, const float* post_b,
@@ -487,7 +487,8 @@ int moe_block_norm(const void* block, int bdt, int64_t b_ld, int post_kind, cons
  * moe_permute, except that ids outside [0, E) are allowed: such pairs go to no expert (an expert shard,
  * a capacity limit), inv_rows is -1 for them, offsets[E] counts the others, and sorted_rows holds -1
  * from there on.  Then rows[p] = x[sorted_rows[p] / k] for p < min(offsets[E], n_rows); rows behind
- * are left as they were.  x and rows of xdt (MOE_F32 or MOE_BF16), x_ld and rows_ld apart (any from H on).
+ * are left as they were.  x and rows of xdt (MOE_F32 or MOE_BF16), x_ld and rows_ld apart (any from H on,
+ * up to 2^36).
  * workspace >= moe_dispatch_workspace() bytes (0 for few pairs: NULL is fine then), written by the call.
  *
  * moe_combine_rows: y[t] = sum_j topk_w[t][j] * rows[inv_rows[t*k+j]], j ascending, in f32, one rounding

@@ -355,11 +355,13 @@ bool is_float_type(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 // Tokens of the row operators: their grids stay under 2^32 threads.
 constexpr int kMaxRowTokens = 1 << 21;
 
-// Rows of `width` elements, ld apart, that must hold their width and be 16-byte aligned at the first.
+// Rows of `width` elements, ld apart, that must hold their width and be 16-byte aligned at the first.  The
+// limit keeps sizes in bytes far inside 64 bits.
 int check_rows(const void* p, int64_t ld, int width, const char* what) {
   if (!p) return fail(MOE_EINVAL, "%s must not be null", what);
   if (!aligned16(p)) return fail(MOE_EINVAL, "%s must be 16-byte aligned", what);
-  if (ld < width) return fail(MOE_EINVAL, "%s: rows %lld elements apart, each of %d", what, (long long)ld, width);
+  if (ld < width || ld > (int64_t)1 << 36)
+    return fail(MOE_EINVAL, "%s: rows %lld elements apart, each of %d (at most 2^36 apart)", what, (long long)ld, width);
   return MOE_OK;
 }
 

@@ -413,11 +413,17 @@ def _vector(t, name, n):
     return t.data_ptr()
 
 
+def _matrices(**tensors):
+    """Refuses tensors that are not of two dimensions."""
+    for name, t in tensors.items():
+        if t is None or t.dim() != 2:
+            raise MoeError(MOE_EINVAL, f"{name}: " + ("None" if t is None else f"{tuple(t.shape)}") + ", where a matrix is used")
+
+
 def moe_linear(w, x, bias, act, res, y, stream=None):
     """y = act(x w^T + bias) + res.  w [N][K] and x [T][K] of one type (f32 or bf16); bias [N] f32 or None;
     res [T][N] or None, y itself too; y [T][N] f32 or bf16; each with unit stride along its rows."""
-    if w.dim() != 2 or x.dim() != 2:
-        raise MoeError(MOE_EINVAL, f"w {tuple(w.shape)}, x {tuple(x.shape)}: matrices")
+    _matrices(w=w, x=x)
     N, K = w.shape
     T = x.shape[0]
     wp, wdt, w_ld = _rows(w, "w", N, K)
@@ -445,8 +451,7 @@ def moe_block_norm(block, post, gate, block_scale, res, res_scale, pre, eps, res
     out = res_out if res_out is not None else x
     if first is None or out is None:
         raise MoeError(MOE_EINVAL, "neither block nor res" if first is None else "neither res_out nor x")
-    if first.dim() != 2:
-        raise MoeError(MOE_EINVAL, f"rows of {tuple(first.shape)}: a matrix")
+    _matrices(rows=first)
     T, H = first.shape
     bp, bdt, b_ld = _rows(block, "block", T, H)
     rp, rdt, r_ld = _rows(res, "res", T, H)
@@ -484,8 +489,7 @@ def _pairs(t, name, kind, T, k):
 def moe_dispatch(x, topk_ids, E, counts, offsets, sorted_rows, inv_rows, rows, workspace=None, stream=None):
     """Pairs sorted by expert (ids outside [0, E) to none) and x's rows at their places in rows.
     x [T][H] and rows [n_rows][H] of one type; topk_ids [T][k]; workspace of moe_dispatch_workspace bytes."""
-    if x.dim() != 2 or topk_ids.dim() != 2 or rows.dim() != 2:
-        raise MoeError(MOE_EINVAL, f"x {tuple(x.shape)}, topk_ids {tuple(topk_ids.shape)}, rows {tuple(rows.shape)}: matrices")
+    _matrices(x=x, topk_ids=topk_ids, rows=rows)
     (T, H), k, n_rows = x.shape, topk_ids.shape[1], rows.shape[0]
     xp, xdt, x_ld = _rows(x, "x", T, H)
     rp, _, r_ld = _rows(rows, "rows", n_rows, H, xdt)
@@ -503,6 +507,7 @@ def moe_dispatch(x, topk_ids, E, counts, offsets, sorted_rows, inv_rows, rows, w
 
 def moe_dispatch_backward(d_rows, inv_rows, k, dx, stream=None):
     """dx [T][H] from the gradients d_rows [n_rows][H] of the dispatched rows."""
+    _matrices(d_rows=d_rows, dx=dx)
     T, H = dx.shape
     rp, rdt, r_ld = _rows(d_rows, "d_rows", d_rows.shape[0], H)
     xp, xdt, x_ld = _rows(dx, "dx", T, H)
@@ -513,6 +518,7 @@ def moe_dispatch_backward(d_rows, inv_rows, k, dx, stream=None):
 
 def moe_combine_rows(rows, topk_w, inv_rows, y, stream=None):
     """y [T][H] = sum over j of topk_w[t][j] rows[inv_rows[t][j]]; rows [n_rows][H]."""
+    _matrices(rows=rows, topk_w=topk_w, y=y)
     (T, k), H = topk_w.shape, y.shape[-1]
     rp, rdt, r_ld = _rows(rows, "rows", rows.shape[0], H)
     yp, ydt, y_ld = _rows(y, "y", T, H)
@@ -524,6 +530,7 @@ def moe_combine_rows(rows, topk_w, inv_rows, y, stream=None):
 
 def moe_combine_rows_backward(dy, rows, topk_w, inv_rows, d_rows, d_topk_w, stream=None):
     """d_rows [n_rows][H] (of rows' type, rows itself too) and d_topk_w [T][k] from dy [T][H]."""
+    _matrices(dy=dy, rows=rows, topk_w=topk_w)
     (T, k), H = topk_w.shape, dy.shape[-1]
     yp, ydt, y_ld = _rows(dy, "dy", T, H)
     rp, rdt, r_ld = _rows(rows, "rows", rows.shape[0], H)
@@ -538,6 +545,7 @@ def moe_combine_rows_backward(dy, rows, topk_w, inv_rows, d_rows, d_topk_w, stre
 
 def moe_gate_backward(topk_ids, topk_w, d_topk_w, d_logits, stream=None):
     """d_logits [T][E] f32 from the gradient of the gate weights."""
+    _matrices(topk_w=topk_w, d_logits=d_logits)
     (T, k), E = topk_w.shape, d_logits.shape[-1]
     _pairs(topk_ids, "topk_ids", "int32", T, k)
     _pairs(topk_w, "topk_w", "f32", T, k)

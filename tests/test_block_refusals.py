@@ -152,7 +152,7 @@ def test_linear_tensors(what, change):
 
 @pytest.mark.parametrize("what,change", [
     ("neither", dict(block=None, res=None)), ("neither", dict(out=None, x=None)), ("block", dict(block=torch.zeros((T, H), dtype=torch.float16))),
-    ("rows of", dict(block=torch.zeros(H))), ("res", dict(res=torch.zeros((T + 1, H)))), ("res_out", dict(out=torch.zeros((T, H), dtype=BF16))),
+    ("matrix", dict(block=torch.zeros(H))), ("res", dict(res=torch.zeros((T + 1, H)))), ("res_out", dict(out=torch.zeros((T, H), dtype=BF16))),
     ("x", dict(x=torch.zeros((T, 2 * H))[:, ::2])), ("gate", dict(gate=torch.zeros((H, H)))), ("gate", dict(gate=torch.zeros(H + 1))),
     ("gate", dict(gate=torch.zeros(2 * H)[::2])), ("gate", dict(gate=torch.zeros(H, dtype=torch.float16))),
     ("post norm's weight", dict(post=(1, torch.zeros(H, dtype=BF16)))), ("post norm's bias", dict(post=(2, torch.zeros(H), torch.zeros(1)))),
@@ -177,7 +177,7 @@ def _sorted(**change):
     ("rows", dict(rows=torch.zeros((T * TOPK, H + 1)))), ("topk_ids", dict(ids=torch.zeros((T, TOPK), dtype=torch.int64))),
     ("topk_ids", dict(ids=torch.zeros((T, 2 * TOPK), dtype=I32)[:, ::2])), ("topk_ids", dict(ids=torch.zeros((T + 1, TOPK), dtype=I32))),
     ("counts", dict(counts=torch.zeros(E + 1, dtype=I32))), ("offsets", dict(offsets=torch.zeros(E, dtype=I32))), ("sorted_rows", dict(order=torch.zeros(T, dtype=I32))),
-    ("inv_rows", dict(inv=torch.zeros(T * TOPK, dtype=torch.int64))), ("workspace", dict(ws=torch.zeros(1, dtype=U8).expand(100))), ("matrices", dict(ids=torch.zeros(T, dtype=I32)))])
+    ("inv_rows", dict(inv=torch.zeros(T * TOPK, dtype=torch.int64))), ("workspace", dict(ws=torch.zeros(1, dtype=U8).expand(100))), ("matrix", dict(ids=torch.zeros(T, dtype=I32)))])
 def test_dispatch_tensors(what, change):
     _refused(what, lambda: _sorted(**change))
 
@@ -191,6 +191,22 @@ def test_combine_tensors(what, change):
     _refused(what, lambda: moe.moe_combine_rows(*a.values()))
     if what != "y":
         _refused(what, lambda: moe.moe_combine_rows_backward(a["y"], a["rows"], a["w"], a["inv"], torch.zeros((4, H)), torch.zeros((T, TOPK))))
+
+
+def test_vectors_and_none_in_place_of_matrices():
+    v, inv, w = torch.zeros(H), torch.zeros(T * TOPK, dtype=I32), torch.zeros((T, TOPK))
+    m = torch.zeros((T, H))
+    for call in (lambda: moe.moe_combine_rows(v, w, inv, m), lambda: moe.moe_combine_rows(m, w.reshape(-1), inv, m), lambda: moe.moe_combine_rows(m, None, inv, m),
+                 lambda: moe.moe_combine_rows(m, w, inv, None), lambda: moe.moe_dispatch_backward(v, inv, TOPK, m), lambda: moe.moe_dispatch_backward(m, inv, TOPK, v),
+                 lambda: moe.moe_combine_rows_backward(m, v, w, inv, m, w), lambda: moe.moe_gate_backward(inv, w.reshape(-1), w, m),
+                 lambda: moe.moe_linear(None, m, None, 0, None, m), lambda: moe.moe_linear(m, None, None, 0, None, m)):
+        _refused("matrix", call)
+
+
+def test_rows_too_far_apart():
+    far = (1 << 36) + 8
+    assert _norm(b_ld=far) == _norm(o_ld=far) == _linear(y_ld=far) == _linear(r_ld=far) == moe.MOE_EINVAL
+    assert _dispatch(x_ld=far) == _dispatch(rows_ld=far) == _combine(rows_ld=far) == _combine_back(dr_ld=far) == moe.MOE_EINVAL
 
 
 def test_gradient_tensors():
