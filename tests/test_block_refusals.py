@@ -62,9 +62,9 @@ def test_linear_other_weights_and_no_tokens():
     assert _linear(T=0, x=None, y=None, res=None) == moe.MOE_OK
 
 
-def _dispatch(**change):
-    a = dict(x=_p(16), xdt=1, x_ld=64, ids=_p(1), T=600, k=2, E=8, H=64, counts=_p(2), offsets=_p(3), rows_order=_p(4), inv=_p(5),
-             rows=_p(32), rows_ld=64, n_rows=1200, ws=_p(6), ws_bytes=1 << 20)
+def _dispatch(**change):  # more pairs than are placed without a workspace
+    a = dict(x=_p(16), xdt=1, x_ld=64, ids=_p(1), T=20000, k=2, E=8, H=64, counts=_p(2), offsets=_p(3), rows_order=_p(4), inv=_p(5),
+             rows=_p(32), rows_ld=64, n_rows=40000, ws=_p(6), ws_bytes=1 << 20)
     a.update(change)
     return moe.lib().moe_dispatch(*a.values(), None)
 
@@ -79,9 +79,9 @@ def test_dispatch(change):
 
 
 def test_dispatch_workspace():
-    n = moe.moe_dispatch_workspace(600, 2, 8)
+    n = moe.moe_dispatch_workspace(20000, 2, 8)
     assert n > 0 and _dispatch(ws_bytes=n - 1) == moe.MOE_ECAPACITY
-    assert moe.moe_dispatch_workspace(10, 2, 8) == 0
+    assert moe.moe_dispatch_workspace(10, 2, 8) == moe.moe_dispatch_workspace(4096, 2, 8) == 0
     assert moe.moe_dispatch_workspace(10, 9, 8) == moe.moe_dispatch_workspace(-1, 1, 8) == moe.moe_dispatch_workspace(1 << 22, 1, 8) == 0
 
 
