@@ -10,8 +10,9 @@
 //
 // Measured on an MI355X, bf16, x weights x K (plain library product beside it): 1 x 4096 x 4096 7.5 us (20),
 // 16 x 12288 x 4096 17.2 (21.6), 64 x 4096 x 4096 9.1 (19), 16 x 65536 x 4096 100 (121; 537 MB at 5.4 TB/s),
-// 256 x 4096 x 4096 16.3 (19.7), 1024 x 4096 x 4096 35.6 (37.4), 4096 x 8192 x 4096 224 (220; 1.23 PFLOP/s);
-// f32: 64 x 4096 x 4096 26 (23.5), 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).
+// 256 x 4096 x 4096 16.3 (19.7), 1024 x 4096 x 4096 35.6 (37.4), 4096 x 8192 x 4096 220 (177 once both
+// are warm; 1.25 PFLOP/s);
+// f32: 64 x 1024 x 4096 17 (19), 64 x 4096 x 4096 26 (23.5), 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).
 #include "ffn_common.hpp"
 #include "kernels.hpp"
 #include "row_io.hpp"
@@ -88,29 +89,29 @@ __device__ __forceinline__ void finish8(const LinearArgs& a, int64_t t, int n, f
 constexpr int kPast = 0x7ffffff0;  // an offset past the end of every buffer made here (under 2^30 bytes): reads as 0
 
 // ---------------------------------------------------------------------------
-// Up to 16 tokens.  A 64-byte piece of a row is one step: lane group g = lane / 16 holds bytes 16 g .. 16 g + 15 of
-// it (8 bf16 or 4 f32) for row lane % 16, of weights (the B operand) and tokens (A) alike: the operand of one
-// v_mfma_f32_16x16x32_bf16, or of four v_mfma_f32_16x16x4_f32.  Lane l of the 16 x 16 result holds tokens
-// 4 (l / 16) + v and weight row l % 16.  Rounds of 4 steps load together, the next round's while one is
-// multiplied; 8 waves of one row tile keep 64 KB in flight a workgroup (16 waves, or rounds of 8: 20% slower
-// over 65536 rows, from fewer workgroups in a CU).
+// 16 weight rows by 16 tokens a workgroup.  A 64-byte piece of a row is one step: lane group g = lane / 16 holds
+// bytes 16 g .. 16 g + 15 of it (8 bf16 or 4 f32) for row lane % 16, of weights (the B operand) and tokens (A) alike:
+// the operand of one v_mfma_f32_16x16x32_bf16, or of four v_mfma_f32_16x16x4_f32.  Lane l of the 16 x 16 result
+// holds tokens 4 (l / 16) + v and weight row l % 16.  Rounds of U steps load together, the next round's while
+// one is multiplied.  8 waves and rounds of 4 steps where there are workgroups enough to fill the chip (16 waves, or
+// rounds of 8: 20% slower over 65536 rows, from fewer workgroups in a CU), 16 waves and rounds of 6 where f32's K
+// has to be walked by few.
 // ---------------------------------------------------------------------------
-constexpr int kStreamSteps = 4, kStreamWaves = 8;
-
-template <bool BF16>
-__global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a) {
-  __shared__ float part[kStreamWaves][256];
-  constexpr int ES = BF16 ? 2 : 4, U = kStreamSteps;
+template <bool BF16, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void linear_stream_kernel(LinearArgs a, int n_tiles) {
+  __shared__ float part[WAVES][256];
+  constexpr int ES = BF16 ? 2 : 4;
   const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6), nw = blockDim.x >> 6;
-  const int n0 = (int)blockIdx.x * 16, row = lane & 15, g = lane >> 4;
+  const int n0 = (int)(blockIdx.x % n_tiles) * 16, t0 = (int)(blockIdx.x / n_tiles) * 16, row = lane & 15, g = lane >> 4;
   const int kbytes = a.K * ES;
   // the tile's rows, and nothing behind them
   const auto wbuf = make_rsrc(static_cast<const uint8_t*>(a.w) + n0 * a.w_ld * ES,
                               (min(a.N - n0, 16) - 1) * a.w_ld * ES + kbytes);
-  const auto xbuf = make_rsrc(a.x, (a.T - 1) * a.x_ld * ES + kbytes);
+  const auto xbuf = make_rsrc(static_cast<const uint8_t*>(a.x) + t0 * a.x_ld * ES,
+                              (min(a.T - t0, 16) - 1) * a.x_ld * ES + kbytes);
   // this lane's rows; rows past the end read as 0
   const int woff = n0 + row < a.N ? (int)(row * a.w_ld * ES) + 16 * g : kPast;
-  const int xoff = row < a.T ? (int)(row * a.x_ld * ES) + 16 * g : kPast;
+  const int xoff = t0 + row < a.T ? (int)(row * a.x_ld * ES) + 16 * g : kPast;
   const int steps = (kbytes + 63) / 64, rounds = (steps + U - 1) / U;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   u32x4 wf[2][U], xf[2][U];
@@ -151,17 +152,19 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
   for (int q = threadIdx.x; q < 256; q += blockDim.x) {
     float s = 0.0f;
     for (int w = 0; w < nw; ++w) s += part[w][q];
-    const int l = q >> 2, n = n0 + (l & 15), t = 4 * (l >> 4) + (q & 3);
+    const int l = q >> 2, n = n0 + (l & 15), t = t0 + 4 * (l >> 4) + (q & 3);
     if (n < a.N && t < a.T) finish(a, t, n, s);
   }
 }
 
-template <bool BF16>
+template <bool BF16, int WAVES, int U>
 hipError_t launch_stream(const LinearArgs& a, hipStream_t st) {
-  const int rounds = (a.K * (BF16 ? 2 : 4) + 64 * kStreamSteps - 1) / (64 * kStreamSteps);
+  const int rounds = (a.K * (BF16 ? 2 : 4) + 64 * U - 1) / (64 * U);
   int waves = 1;  // no more than there are rounds
-  while (waves < kStreamWaves && waves < rounds) waves *= 2;
-  hipLaunchKernelGGL(linear_stream_kernel<BF16>, dim3((unsigned)((a.N + 15) / 16)), dim3(64 * waves), 0, st, a);
+  while (waves < WAVES && waves < rounds) waves *= 2;
+  const int n_tiles = (a.N + 15) / 16, t_tiles = (a.T + 15) / 16;
+  hipLaunchKernelGGL((linear_stream_kernel<BF16, WAVES, U>), dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * waves), 0, st, a,
+                     n_tiles);
   return hipGetLastError();
 }
 
@@ -463,10 +466,14 @@ const TileShape kShapes[] = {
 
 }  // namespace
 
-// Few tokens: the tiles' 32 token rows would be half of the loads.  bf16, 65536 rows of 4096: 4 tokens 87 us
-// here, 97 in tiles, 16 tokens 122 and 101; f32, 4096 rows: 16 tokens 19 us and 24.
+// Few tokens take the stream kernel (the tiles' 32 token rows would be half of the loads: bf16, 65536 rows of 4096,
+// 4 tokens 87 us here, 97 in tiles, 16 tokens 122 and 101; f32, 4096 rows, 16 tokens 19 us and 24).  So do f32
+// results of few 16 x 16 tiles: a 32 x 32 tile is bound by the matrix unit of its CU, and four CUs share it here
+// (64 x 1024 x 4096 24 us in tiles, 17 here; 64 x 64 x 16384 85 and 58).  bf16 is not (64 x 1024 x 4096 8.4 us in tiles,
+// 9.8 here).
 hipError_t launch_linear(bool bf16, const LinearArgs& a, hipStream_t st) {
-  if (a.T <= (bf16 ? 4 : 16)) return bf16 ? launch_stream<true>(a, st) : launch_stream<false>(a, st);
+  if (!bf16 && (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= 256) return launch_stream<false, 16, 6>(a, st);
+  if (a.T <= (bf16 ? 4 : 16)) return bf16 ? launch_stream<true, 8, 4>(a, st) : launch_stream<false, 8, 4>(a, st);
   const TileShape* best = nullptr;
   float least = 0.0f;
   for (const TileShape& s : kShapes) {
