@@ -63,23 +63,31 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, fl
     static_cast<float*>(a.y)[t * a.y_ld + n] = v;
 }
 
-// Elements n .. n + 7 of token t of res, 0 where there is none or past the row's end.
-__device__ __forceinline__ void residual8(const LinearArgs& a, int64_t t, int n, float (&r)[8]) {
-  if (a.res_bf16)
-    load8(static_cast<const uint16_t*>(a.res) + t * a.r_ld + n, a.N - n, r);
-  else
-    load8(static_cast<const float*>(a.res) + t * a.r_ld + n, a.N - n, r);
-}
+// Elements n .. n + 7 of token t of res as memory holds them, so that they can be on their way while others are
+// worked on; 0 where there are none.
+struct Residual8 {
+  Raw8<uint16_t> b;
+  Raw8<float> f;
+  __device__ __forceinline__ void load(const LinearArgs& a, int64_t t, int n, bool live) {
+    const int left = live && a.res ? a.N - n : 0;
+    const int64_t at = left > 0 ? t * a.r_ld + n : 0;
+    if (a.res_bf16)
+      b.load<false>(static_cast<const uint16_t*>(a.res) + at, left);
+    else
+      f.load<false>(static_cast<const float*>(a.res) + at, left);
+  }
+  __device__ __forceinline__ float value(const LinearArgs& a, int i) const { return a.res_bf16 ? b[i] : f[i]; }
+};
 
 // Finished values of elements n .. n + 7 of token t from sums v, bias b and residual r.
 __device__ __forceinline__ void finish8(const LinearArgs& a, int64_t t, int n, float (&v)[8], const float (&b)[8],
-                                        const float (&r)[8]) {
+                                        const Residual8& r) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] += b[i];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = activate(v[i], a.act);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] += r[i];
+  for (int i = 0; i < 8; ++i) v[i] += r.value(a, i);
   if (a.y_bf16)
     store8(static_cast<uint16_t*>(a.y) + t * a.y_ld + n, a.N - n, v);
   else
@@ -375,64 +383,67 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
   }
   // Results: 32 tokens by up to 64 weight rows at a time through LDS, so that a lane finishes 8
   // consecutive outputs and the rows of res and y are read and written in whole lines.  The WK waves of a part
-  // share its tokens out between them.  The residual of all of a wave's passes over a slice is on its way
-  // while the slice goes through LDS (a load and its wait for each pass instead: 36 us of the 260 that
+  // share its tokens out between them.  The residual of a slice is on its way while the slice before it
+  // is finished (a load and its wait for each of a wave's passes instead: 36 us of the 260 that
   // 4096 x 8192 x 4096 with a residual took).
   constexpr int SL = RN % 2 ? 1 : 2, LD = out_ld(RN), LANES = 4 * SL;  // tiles of a slice; lanes a token
-  constexpr int PER = 64 / LANES, PASSES = PER * WK >= 32 ? 1 : 32 / (PER * WK);
+  constexpr int PER = 64 / LANES, PASSES = PER * WK >= 32 ? 1 : 32 / (PER * WK), SLICES = RN / SL * RT;
   constexpr int kOutBytes = out_bytes(RN);
+  const int u0 = wk * PER + lane / LANES;
+  auto first_row = [&](int q) { return n0 + wn * (BN / WN) + 32 * SL * (q / RT) + 8 * (lane % LANES); };
+  auto first_token = [&](int q) { return t0 + wt * (BT / WT) + 32 * (q % RT) + u0; };
+  Residual8 r[2][PASSES];
+  auto fetch = [&](int q) {
+#pragma unroll
+    for (int u = 0; u < PASSES; ++u) {
+      const int t = first_token(q) + u * PER * WK, n = first_row(q);
+      r[q & 1][u].load(a, t, n, u0 < 32 && t < a.T && n < a.N);
+    }
+  };
+  fetch(0);
   wait_loads<0, false>();  // the loads past the last stage have landed
   __syncthreads();         // and nobody reads a stage any more
   float* out = reinterpret_cast<float*>(smem + wv * kOutBytes);
   const float* part = reinterpret_cast<const float*>(smem + (wv - wk) * kOutBytes);
+  float bias[8] = {};
 #pragma unroll
-  for (int i2 = 0; i2 < RN; i2 += SL) {
-    const int n = n0 + wn * (BN / WN) + 32 * i2 + 8 * (lane % LANES);
-    float bias[8] = {};
-    if (a.bias && n < a.N) load8(a.bias + n, a.N - n, bias);
+  for (int q = 0; q < SLICES; ++q) {
+    const int i2 = q / RT * SL, j = q % RT, n = first_row(q);
+    if (j == 0 && a.bias && n < a.N) load8(a.bias + n, a.N - n, bias);
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-      const int u0 = wk * PER + lane / LANES, t = t0 + wt * (BT / WT) + 32 * j + u0;
-      float r[PASSES][8];
+    for (int i = 0; i < SL; ++i)
 #pragma unroll
-      for (int u = 0; u < PASSES; ++u) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[u][e] = 0.0f;
-        if (a.res && u0 < 32 && t + u * PER * WK < a.T && n < a.N) residual8(a, t + u * PER * WK, n, r[u]);
+      for (int v = 0; v < 4; ++v) {
+        const f32x16& c = acc[i2 + i][j];  // lane: token rho, rows 8 v + 4 h + 0 .. 3
+        *reinterpret_cast<f32x4*>(out + rho * LD + 32 * i + 8 * v + 4 * h) =
+            f32x4{c[4 * v], c[4 * v + 1], c[4 * v + 2], c[4 * v + 3]};
       }
+    if (q + 1 < SLICES) fetch(q + 1);
+    if constexpr (WK > 1)
+      lds_barrier();
+    else
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int i = 0; i < SL; ++i)
+    for (int u = 0; u < PASSES; ++u) {
+      const int t = first_token(q) + u * PER * WK;
+      if (u0 >= 32 || t >= a.T || n >= a.N) continue;
+      float v[8] = {};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16& c = acc[i2 + i][j];  // lane: token rho, rows 8 q + 4 h + 0 .. 3
-          *reinterpret_cast<f32x4*>(out + rho * LD + 32 * i + 8 * q + 4 * h) =
-              f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+      for (int k = 0; k < WK; ++k) {
+        const float* p = part + k * (kOutBytes / 4) + (u0 + u * PER * WK) * LD + 8 * (lane % LANES);
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] += lo[e];
+          v[4 + e] += hi[e];
         }
-      if constexpr (WK > 1)
-        lds_barrier();
-      else
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int u = 0; u < PASSES; ++u) {
-        if (u0 >= 32 || t + u * PER * WK >= a.T || n >= a.N) continue;
-        float v[8] = {};
-#pragma unroll
-        for (int k = 0; k < WK; ++k) {
-          const float* p = part + k * (kOutBytes / 4) + (u0 + u * PER * WK) * LD + 8 * (lane % LANES);
-          const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] += lo[e];
-            v[4 + e] += hi[e];
-          }
-        }
-        finish8(a, t + u * PER * WK, n, v, bias, r[u]);
       }
-      if constexpr (WK > 1)
-        lds_barrier();
-      else
-        __builtin_amdgcn_wave_barrier();
+      finish8(a, t, n, v, bias, r[q & 1][u]);
     }
+    if constexpr (WK > 1)
+      lds_barrier();
+    else
+      __builtin_amdgcn_wave_barrier();
   }
 }
 
