@@ -185,9 +185,12 @@ hipError_t launch_stream(const LinearArgs& a, hipStream_t st) {
 // the row in step m of the stage.  Piece p of row r sits at place p ^ swz(r).
 //
 // Each step is laid out by hand: a product, an operand read of the next step, a load of a later stage, the next
-// product, .. (reads, loads and products one after the other: 4096 x 8192 x 4096 in 267 us, so 224).  What bounds
-// the largest tile now is the barrier that ends a stage: the matrix unit is busy in 77% of the cycles, at a
-// clock that this work holds near 1.5 GHz.
+// product, .. (reads, loads and products one after the other: 4096 x 8192 x 4096 in 267 us, so 220).  What bounds
+// the largest tile now is the loads: with the same products and none of them in the loop it takes 193 us, with all
+// of them from the same stage 216; without the barrier nothing changes.  The matrix unit is busy in 72 to 77% of
+// the cycles, at a clock that this work holds near 1.5 GHz.  Measured and not kept: 4 waves of 128 x 128 (324 us:
+// one wave per SIMD), stages of 64 bytes with 4 or 5 buffers (231), workgroups starting at other columns (neutral
+// or slower).
 // ---------------------------------------------------------------------------
 constexpr int kRow = 128;  // bytes of a row in a stage
 
@@ -384,8 +387,8 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
   // Results: 32 tokens by up to 64 weight rows at a time through LDS, so that a lane finishes 8
   // consecutive outputs and the rows of res and y are read and written in whole lines.  The WK waves of a part
   // share its tokens out between them.  The residual of a slice is on its way while the slice before it
-  // is finished (a load and its wait for each of a wave's passes instead: 36 us of the 260 that
-  // 4096 x 8192 x 4096 with a residual took).
+  // is finished (4096 x 8192 x 4096 with activation and residual: 243 us; fetched for its own slice 250, for each of a
+  // wave's passes 260).
   constexpr int SL = RN % 2 ? 1 : 2, LD = out_ld(RN), LANES = 4 * SL;  // tiles of a slice; lanes a token
   constexpr int PER = 64 / LANES, PASSES = PER * WK >= 32 ? 1 : 32 / (PER * WK), SLICES = RN / SL * RT;
   constexpr int kOutBytes = out_bytes(RN);
