@@ -302,12 +302,14 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
     else
       B[q - RN] = *reinterpret_cast<const u32x4*>(buf + xat[m] + (q - RN) * 32 * kRow);
   };
-  // Part e (of S) of stage s's loads, into `into`: behind the barrier that frees the buffer, under the S steps
-  // that follow, so that the loads' issue keeps up with them.  Two buffers leave no time for that: all
-  // go out at once then.
+  // The loads of a stage go out in parts, under the steps that follow the barrier that frees their buffer, so that
+  // their issue keeps up with the products: over S steps, with two buffers over two, which leaves the last part
+  // two steps to land in.
   constexpr int SPREAD = D > 2 ? S : 2;
   // One step: the products of A and B; behind each of them operands of the next step (m of buffer `next`) are
-  // read and part e of stage s's loads goes out, so that neither keeps the matrix unit waiting.
+  // read and part e of stage s's loads goes out, into `into`, so that neither keeps the matrix unit waiting.  Part
+  // 0 belongs to a stage's last step: after its first X products the next stage has to have landed, and this
+  // one's buffer is free.
   auto step = [&](const uint8_t* next, int m, auto E, int s, uint8_t* into, const u32x4 (&A)[RN], const u32x4 (&B)[RT],
                   u32x4 (&An)[RN], u32x4 (&Bn)[RT]) {
     constexpr int e = decltype(E)::value;
@@ -317,7 +319,7 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
     for (int p = 0; p < P; ++p) {
       const int i = p % RN, j = p / RN;
       if (e == 0 && p == X) {
-        wait_loads<(D - 2) * LOADS, true>();  // own loads of stage s + 1, own reads of stage s
+        wait_loads<(D - 2) * LOADS, true>();  // own loads of the next stage, own reads of this one
         block_barrier();
       }
       acc[i][j] = mma_tile<BF16>(A[i], B[j], acc[i][j]);
@@ -325,7 +327,8 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
       for (int q = (p - X) * per; q < (p - X + 1) * per; ++q)
         if (q >= 0 && q < RN + RT) read(next, m, q, An, Bn);
 #pragma unroll
-      for (int d = p < X ? lo : lo + (p - X) * (hi - lo) / (P - X); d < (p < X ? lo : lo + (p - X + 1) * (hi - lo) / (P - X)); ++d) load(s, into, d);
+      for (int d = lo + max(p - X, 0) * (hi - lo) / (P - X); d < lo + max(p - X + 1, 0) * (hi - lo) / (P - X); ++d)
+        load(s, into, d);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -353,7 +356,8 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void linear_tile_kernel(LinearAr
     early(std::integral_constant<int, 1>());
     early(std::integral_constant<int, 2>());
     early(std::integral_constant<int, 3>());
-    step(other, 0, std::integral_constant<int, 0>(), s + D, buf, A[(S - 1 + f) & 1], B[(S - 1 + f) & 1], A[(S + f) & 1], B[(S + f) & 1]);
+    step(other, 0, std::integral_constant<int, 0>(), s + D, buf, A[(S - 1 + f) & 1], B[(S - 1 + f) & 1], A[(S + f) & 1],
+         B[(S + f) & 1]);
     freed = buf;
     buf = other;  // past the last stage its operands are read and not used
   };

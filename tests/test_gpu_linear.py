@@ -163,3 +163,35 @@ def test_same_bits_and_other_stream_and_graph(T):
 
 def test_no_tokens():
     moe.moe_linear(torch.zeros((8, 8), device="cuda"), torch.zeros((0, 8), device="cuda"), None, 0, None, torch.zeros((0, 8), device="cuda"))
+
+
+@pytest.mark.parametrize("T", [3, 50, 300])
+def test_columns_of_one_buffer(T):
+    """x, the residual and the result side by side in the rows of one buffer: nothing overlaps."""
+    g = torch.Generator().manual_seed(T)
+    buf = torch.randint(-4, 5, (T, 64 + 24 + 40), generator=g).to(BF16)
+    w = torch.randint(-2, 3, (40, 64), generator=g).to(BF16)
+    d = buf.cuda()
+    moe.moe_linear(w.cuda(), d[:, :64], None, 0, d[:, 88:], d[:, 88:])
+    torch.cuda.synchronize()
+    ref = buf.double()[:, :64] @ w.double().t() + buf.double()[:, 88:]
+    assert torch.equal(d[:, :88].cpu(), buf[:, :88])
+    assert torch.equal(d[:, 88:].cpu(), ref.to(BF16))  # integers past 256 are rounded, the sum itself is exact
+
+
+def test_two_streams_at_once():
+    """Different products on two streams, many times over: each as alone."""
+    g = torch.Generator().manual_seed(1)
+    jobs = []
+    for T, N, K in ((300, 700, 1024), (16, 5000, 512)):
+        x, w = torch.randn(T, K, generator=g).to(BF16).cuda(), torch.randn(N, K, generator=g).to(BF16).cuda()
+        want, y = torch.empty((T, N), device="cuda"), torch.zeros((T, N), device="cuda")
+        moe.moe_linear(w, x, None, 0, None, want)
+        jobs.append((torch.cuda.Stream(), w, x, y, want))
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for st, w, x, y, _ in jobs:
+            moe.moe_linear(w, x, None, 0, None, y, stream=st)
+    torch.cuda.synchronize()
+    for _, _, _, y, want in jobs:
+        assert torch.equal(y, want)
