@@ -388,6 +388,19 @@ bool same_rows(const Span& a, const Span& b) {
   return a.p == b.p && a.dt == b.dt && (a.ld == b.ld || a.rows <= 1);
 }
 
+// n int32 or f32.
+Span words(const void* p, int n) { return Span{p, n, n > 0 ? 1 : 0, n, MOE_F32}; }
+// Whether a result lies on another of them or on an input.
+bool overlap(std::initializer_list<Span> results, std::initializer_list<Span> inputs) {
+  for (const Span* a = results.begin(); a != results.end(); ++a) {
+    for (const Span* b = a + 1; b != results.end(); ++b)
+      if (overlaps(*a, *b)) return true;
+    for (const Span& b : inputs)
+      if (overlaps(*a, b)) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 int moe_block_norm(const void* block, int bdt, int64_t b_ld, int post_kind, const float* post_w, const float* post_b,
@@ -542,12 +555,15 @@ int moe_dispatch(const void* x, int xdt, int64_t x_ld, const int32_t* topk_ids, 
     if (int rc = check_rows(x, x_ld, H, "x")) return rc;
     if (n_rows > 0) {
       if (int rc = check_rows(rows, rows_ld, H, "rows")) return rc;
-      REQUIRE(!overlaps(Span{x, x_ld, T, H, xdt}, Span{rows, rows_ld, n_rows, H, xdt}), "moe_dispatch: rows overlap x");
     }
   }
   const size_t need = moe::dispatch_workspace_bytes(T, k, E);
   if (need) REQUIRE_PTR(workspace);
   if (ws_bytes < need) return fail(MOE_ECAPACITY, "moe_dispatch: workspace %zu bytes < %zu needed", ws_bytes, need);
+  REQUIRE(!overlap({words(counts, E), words(offsets, E + 1), words(sorted_rows, T * k), words(inv_rows, T * k),
+                    words(workspace, (int)(need / 4)), Span{rows, rows_ld, T > 0 ? n_rows : 0, H, xdt}},
+                   {words(topk_ids, T * k), Span{x, x_ld, T, H, xdt}}),
+          "moe_dispatch: rows, the tables or the workspace overlap each other, x or topk_ids");
   moe::DispatchArgs a;
   a.x = x;
   a.ids = topk_ids;
@@ -578,7 +594,9 @@ int combine_rows(const void* rows, int rdt, int64_t rows_ld, int n_rows, const f
     if (int rc = check_rows(rows, rows_ld, H, "rows")) return rc;
   REQUIRE_PTR(inv_rows);
   if (int rc = check_rows(y, y_ld, H, "y")) return rc;
-  REQUIRE(!overlaps(Span{rows, rows_ld, n_rows, H, rdt}, Span{y, y_ld, T, H, ydt}), "%s: the result overlaps the rows", what);
+  REQUIRE(!overlap({Span{y, y_ld, T, H, ydt}},
+                   {Span{rows, rows_ld, n_rows, H, rdt}, words(topk_w, T * k), words(inv_rows, T * k)}),
+          "%s: the result overlaps an operand", what);
   moe::CombineRowsArgs a = {};
   a.rows = rows;
   a.topk_w = topk_w;
@@ -622,13 +640,14 @@ int moe_combine_rows_backward(const void* dy, int ydt, int64_t dy_ld, const void
   if (n_rows > 0) {
     if (int rc = check_rows(rows, rows_ld, H, "rows")) return rc;
     if (int rc = check_rows(d_rows, dr_ld, H, "d_rows")) return rc;
-    REQUIRE(!overlaps(sd, sdy), "moe_combine_rows_backward: d_rows overlap dy");
     REQUIRE(!overlaps(sd, sr) || same_rows(sd, sr), "moe_combine_rows_backward: d_rows overlap rows without being the same");
   }
   REQUIRE_PTR(topk_w);
   REQUIRE_PTR(inv_rows);
   REQUIRE_PTR(d_topk_w);
-  REQUIRE(d_topk_w != topk_w, "moe_combine_rows_backward: d_topk_w is topk_w");
+  const Span sw = words(topk_w, T * k), si = words(inv_rows, T * k);
+  REQUIRE(!overlap({sd, words(d_topk_w, T * k)}, {sdy, sw, si}) && !overlaps(words(d_topk_w, T * k), sr),
+          "moe_combine_rows_backward: d_rows or d_topk_w overlap each other or an operand");
   moe::CombineRowsArgs a = {};
   a.rows = rows;
   a.topk_w = topk_w;
@@ -657,6 +676,9 @@ int moe_gate_backward(const int32_t* topk_ids, const float* topk_w, const float*
   REQUIRE_PTR(topk_w);
   REQUIRE_PTR(d_topk_w);
   REQUIRE_PTR(d_logits);
+  REQUIRE(!overlap({Span{d_logits, E, T, E, MOE_F32}},
+                   {words(topk_ids, T * k), words(topk_w, T * k), words(d_topk_w, T * k)}),
+          "moe_gate_backward: d_logits overlap an operand");
   hipError_t e = moe::launch_gate_backward(topk_ids, topk_w, d_topk_w, T, E, k, d_logits, stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_gate_backward launch");
 }

@@ -220,3 +220,23 @@ def test_gradient_tensors():
     _refused("d_rows", lambda: moe.moe_dispatch_backward(torch.zeros((4, H - 1)), inv, TOPK, torch.zeros((T, H))))
     _refused("d_logits", lambda: moe.moe_gate_backward(torch.zeros((T, TOPK), dtype=I32), w, w, torch.zeros((T, E), dtype=BF16)))
     _refused("d_topk_w", lambda: moe.moe_gate_backward(torch.zeros((T, TOPK), dtype=I32), w, torch.zeros((T, 1)), torch.zeros((T, E))))
+
+
+# ---------------------------------------------------------------------------
+# Results on each other or on what is still read
+@pytest.mark.parametrize("change", [
+    dict(counts=_p(3)), dict(counts=_p(1)), dict(offsets=_p(2, 16)), dict(rows_order=_p(5)), dict(inv=_p(4, 16)), dict(rows_order=_p(1)),
+    dict(inv=_p(1, 159984)), dict(ws=_p(1)), dict(ws=_p(4)), dict(ws=_p(5, 64)), dict(ws=_p(2)), dict(rows=_p(1)), dict(rows=_p(5)),
+    dict(rows=_p(6)), dict(counts=_p(16)), dict(ws=_p(16)), dict(inv=_p(32, 128)), dict(rows_order=_p(16))])
+def test_dispatch_results_apart(change):
+    assert _dispatch(**change) == moe.MOE_EINVAL
+
+
+def test_combine_results_apart():
+    assert _combine(y=_p(1)) == _combine(y=_p(2)) == _combine(w=_p(17, 16)) == moe.MOE_EINVAL
+    for change in (dict(d_w=_p(2)), dict(d_w=_p(15)), dict(d_w=_p(16)), dict(d_w=_p(17)), dict(d_w=_p(1, 16)), dict(d_rows=_p(1)),
+                   dict(d_rows=_p(2)), dict(d_rows=_p(3))):
+        assert _combine_back(**change) == moe.MOE_EINVAL
+    ok = [_p(1), _p(2), _p(3), 4, 8, 2, _p(4)]
+    for on in (1, 2, 3):
+        assert moe.lib().moe_gate_backward(*ok[:6], _p(on), None) == moe.MOE_EINVAL

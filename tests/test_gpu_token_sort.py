@@ -265,3 +265,30 @@ def test_same_bits_and_graph():
         torch.cuda.synchronize()
         for a, b in zip(flat(one), flat(two)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [60, 600, 5000])
+def test_two_streams_at_once(T):
+    """The way there and back of different tokens on two streams, each with its tables and workspace."""
+    k, E, H, jobs = 6, 64, 512, []
+    for seed in range(2):
+        ids, x = _ids(T, k, E, seed), torch.randn(T, H, generator=torch.Generator().manual_seed(seed))
+        w = torch.rand(T, k, generator=torch.Generator().manual_seed(seed))
+        i32 = dict(dtype=torch.int32, device="cuda")
+        out = [torch.full((n,), -7, **i32) for n in (E, E + 1, T * k, T * k)]
+        ws = torch.empty(moe.moe_dispatch_workspace(T, k, E), dtype=torch.uint8, device="cuda")
+        jobs.append((torch.cuda.Stream(), x.cuda(), ids.cuda(), w.cuda(), out, torch.zeros((T * k, H), device="cuda"),
+                     torch.zeros((T, H), device="cuda"), ws, P.order(ids, E)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, x, ids, w, out, rows, y, ws, _ in jobs:
+            moe.moe_dispatch(x, ids, E, *out, rows, ws, stream=st)
+            moe.moe_combine_rows(rows, w, out[3], y, stream=st)
+    torch.cuda.synchronize()
+    for _, x, ids, w, out, rows, y, ws, ref in jobs:
+        for a, b in zip(out, ref):
+            assert torch.equal(a.cpu(), b)
+        assert torch.equal(rows.cpu(), x.cpu()[ref[2].long() // k])
+        want = x.cpu().double() * w.cpu().double().sum(1, keepdim=True)  # every pair brings its token's own row back
+        bound = (k + 1) * 2.0 ** -24 * 1.01 * want.abs() + 2.0 ** -126  # k products and sums, one store
+        assert ((y.cpu().double() - want).abs() <= bound).all()
