@@ -1,18 +1,19 @@
 // linear.hip -- y = act(x W^T + bias) + res for f32 or bf16 weights stored as they come, one row of W
 // after another.
 //
-// Two kernels.  linear_stream_kernel, for very few tokens: every wave multiplies 16 weight rows by up to 16
-// tokens over its part of K, operands straight from memory in the matrix instructions' order, and the waves of a
-// workgroup, which split K between them, add up in LDS; no barrier and no staging before that.
+// Two kernels.  linear_stream_kernel, for few tokens or small results: every wave multiplies 16 weight rows by 4, 8
+// or 16 tokens over its part of K, operands straight from memory in registers, and the waves of a workgroup, which
+// split K between them, add up in LDS; no barrier and no staging before that.
 // linear_tile_kernel, for all else: tiles staged through LDS, from 32 x 32 (weights are the work: many small
 // workgroups, deep in flight) to 256 x 256 (the matrix instructions are).  Sums in f32, in an order fixed by
 // the shape.
 //
-// Measured on an MI355X, bf16, x weights x K (plain library product beside it): 1 x 4096 x 4096 7.5 us (20),
-// 16 x 12288 x 4096 17.2 (21.6), 64 x 4096 x 4096 9.1 (19), 16 x 65536 x 4096 100 (121; 537 MB at 5.4 TB/s),
-// 256 x 4096 x 4096 16.3 (19.7), 1024 x 4096 x 4096 35.6 (37.4), 4096 x 8192 x 4096 220 (177 once both
+// Measured on an MI355X, bf16, x weights x K (plain library product beside it): 1 x 4096 x 4096 4.5 us (10.5),
+// 16 x 512 x 4096 5.3 (8.0), 16 x 12288 x 4096 17.4 (20.7), 64 x 4096 x 4096 9.1 (19), 4 x 65536 x 4096 87 (124; 537 MB
+// at 6.2 TB/s), 256 x 4096 x 4096 16.3 (19.7), 1024 x 4096 x 4096 35.6 (37.4), 4096 x 8192 x 4096 220 (177 once both
 // are warm; 1.25 PFLOP/s);
-// f32: 64 x 1024 x 4096 17 (19), 64 x 4096 x 4096 26 (23.5), 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).
+// f32: 4 x 512 x 4096 7.4 (9.9), 32 x 2048 x 2048 8.1 (8.6), 16 x 4096 x 4096 16 (14.2), 64 x 4096 x 4096 26 (23.5),
+// 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).
 #include "ffn_common.hpp"
 #include "kernels.hpp"
 #include "row_io.hpp"
@@ -97,83 +98,163 @@ __device__ __forceinline__ void finish8(const LinearArgs& a, int64_t t, int n, f
 constexpr int kPast = 0x7ffffff0;  // an offset past the end of every buffer made here (under 2^30 bytes): reads as 0
 
 // ---------------------------------------------------------------------------
-// 16 weight rows by 16 tokens a workgroup.  A 64-byte piece of a row is one step: lane group g = lane / 16 holds
-// bytes 16 g .. 16 g + 15 of it (8 bf16 or 4 f32) for row lane % 16, of weights (the B operand) and tokens (A) alike:
-// the operand of one v_mfma_f32_16x16x32_bf16, or of four v_mfma_f32_16x16x4_f32.  Lane l of the 16 x 16 result
-// holds tokens 4 (l / 16) + v and weight row l % 16.  Rounds of U steps load together, the next round's while
-// one is multiplied.  8 waves and rounds of 4 steps where there are workgroups enough to fill the chip (16 waves, or
-// rounds of 8: 20% slower over 65536 rows, from fewer workgroups in a CU), 16 waves and rounds of 6 where f32's K
-// has to be walked by few.
+// 16 weight rows by TOKENS tokens a workgroup; its waves take steps of 256 bytes of K in turn, the next step's loads on
+// their way while one is multiplied, and add up in LDS.
+//
+// Memory is quick where four neighbouring lanes read 64 bytes in a row (with neighbours in different rows a CU
+// got 35 GB/s, 1 x 4096 x 4096 took 7.4 us; now 4.5).  So load i of a step gives lane (g, b, c), g = lane / 16,
+// b = lane / 4 % 4, c = lane % 4, the 16-byte piece 4 g + c of row 4 b + i (tokens, if fewer than 16: row (b, i) of
+// TOKENS / 4 loads).  v_mfma_f32_16x16x32_bf16 (f32: four v_mfma_f32_16x16x4_f32) takes lane % 16 for the row and
+// lane / 16 for the piece.  Two ways to make them meet:
+//  * up to 8 tokens: multiplied as it lies.  "Row" (b, c) of the product is piece c of row b alone, so of its 16 x 16
+//    results those with the same c on both sides count, four of which make up a sum, and every pair of loads has a
+//    product of its own: TOKENS / 4 times the products, with no work between load and product.
+//  * 16 tokens: registers i and lanes c change places first (a transpose inside each quad), then register c is piece
+//    4 g + c of row lane % 16.  32 moves and 32 choices a KB of f32 or bf16, where the other way would be four times the
+//    products (bf16 16 x 64 x 1024 3.3 us, 3.8 the other way).
+// 16 waves where the workgroups do not fill the chip, else 8 (bf16 4 x 8192 x 4096 12.0 us, 14.6 in 16 waves;
+// 4 x 2048 x 16384 14.9 and 13.0).
 // ---------------------------------------------------------------------------
-template <bool BF16, int WAVES, int U>
+// v of another lane of the quad.
+template <int CTRL>
+__device__ __forceinline__ unsigned quad_u32(unsigned v) {
+  return (unsigned)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+}
+__device__ __forceinline__ unsigned from_xor1(unsigned v) { return quad_u32<0xb1>(v); }
+__device__ __forceinline__ unsigned from_xor2(unsigned v) { return quad_u32<0x4e>(v); }
+
+// v[i] of lane c of each quad <-> v[c] of lane i.  Both sides of each choice are formed outside it: a lane that
+// another one reads has to be active.
+__device__ __forceinline__ void turn(u32x4 (&v)[4], bool odd, bool high) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const unsigned p0 = from_xor1(v[0][e]), p1 = from_xor1(v[1][e]), p2 = from_xor1(v[2][e]), p3 = from_xor1(v[3][e]);
+    const unsigned a0 = odd ? p1 : v[0][e], a1 = odd ? v[1][e] : p0, a2 = odd ? p3 : v[2][e], a3 = odd ? v[3][e] : p2;
+    const unsigned q0 = from_xor2(a0), q1 = from_xor2(a1), q2 = from_xor2(a2), q3 = from_xor2(a3);
+    v[0][e] = high ? q2 : a0;
+    v[1][e] = high ? q3 : a1;
+    v[2][e] = high ? a2 : q0;
+    v[3][e] = high ? a3 : q1;
+  }
+}
+
+// c += A . B: 16 rows by 16 over four pieces, 32 bf16 or 16 f32.
+template <bool BF16>
+__device__ __forceinline__ f32x4 mma_pieces(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (BF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
+    return c;
+  }
+}
+
+template <bool BF16, int TOKENS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void linear_stream_kernel(LinearArgs a, int n_tiles) {
-  __shared__ float part[WAVES][256];
-  constexpr int ES = BF16 ? 2 : 4;
+  __shared__ float part[WAVES][TOKENS * 16];
+  constexpr int ES = BF16 ? 2 : 4, X = TOKENS / 4;
+  constexpr bool TURN = TOKENS == 16;
   const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6), nw = blockDim.x >> 6;
-  const int n0 = (int)(blockIdx.x % n_tiles) * 16, t0 = (int)(blockIdx.x / n_tiles) * 16, row = lane & 15, g = lane >> 4;
+  const int g = lane >> 4, b = lane >> 2 & 3, c = lane & 3;
+  const int n0 = (int)(blockIdx.x % n_tiles) * 16, t0 = (int)(blockIdx.x / n_tiles) * TOKENS;
   const int kbytes = a.K * ES;
   // the tile's rows, and nothing behind them
   const auto wbuf = make_rsrc(static_cast<const uint8_t*>(a.w) + n0 * a.w_ld * ES,
                               (min(a.N - n0, 16) - 1) * a.w_ld * ES + kbytes);
   const auto xbuf = make_rsrc(static_cast<const uint8_t*>(a.x) + t0 * a.x_ld * ES,
-                              (min(a.T - t0, 16) - 1) * a.x_ld * ES + kbytes);
-  // this lane's rows; rows past the end read as 0
-  const int woff = n0 + row < a.N ? (int)(row * a.w_ld * ES) + 16 * g : kPast;
-  const int xoff = t0 + row < a.T ? (int)(row * a.x_ld * ES) + 16 * g : kPast;
-  const int steps = (kbytes + 63) / 64, rounds = (steps + U - 1) / U;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  u32x4 wf[2][U], xf[2][U];
-  auto load = [&](int r, u32x4 (&w)[U], u32x4 (&x)[U]) {
+                              (min(a.T - t0, TOKENS) - 1) * a.x_ld * ES + kbytes);
+  // this lane's pieces of the first step; rows past the end read as 0
+  const int piece = 16 * (4 * g + c);
+  unsigned wo[4], xo[X];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = (r * U + u) * 64;
-      const bool in = at + 16 * g < kbytes;  // whole 16-byte fragments: K is a multiple of one
-      w[u] = bld16(wbuf, in && woff != kPast ? woff + at : kPast, 0);
-      x[u] = bld16(xbuf, in && xoff != kPast ? xoff + at : kPast, 0);
+  for (int i = 0; i < 4; ++i) wo[i] = n0 + 4 * b + i < a.N ? (int)((4 * b + i) * a.w_ld * ES) + piece : kPast;
+#pragma unroll
+  for (int i = 0; i < X; ++i) xo[i] = t0 + X * b + i < a.T ? (int)((X * b + i) * a.x_ld * ES) + piece : kPast;
+  f32x4 acc[TURN ? 1 : X][TURN ? 1 : 4];
+#pragma unroll
+  for (auto& row : acc)
+#pragma unroll
+    for (f32x4& v : row) v = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 wf[2][4], xf[2][X];
+  auto load = [&](int s, u32x4 (&w)[4], u32x4 (&x)[X]) {
+    const int at = s * 256;  // kPast + at stays past the end
+    const bool in = at + piece < kbytes;  // whole pieces: K is a multiple of one
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = bld16(wbuf, (int)((in ? wo[i] : kPast) + at), 0);
+      if (i < X) x[i] = bld16(xbuf, (int)((in ? xo[i] : kPast) + at), 0);
     }
   };
-  auto multiply = [&](const u32x4 (&w)[U], const u32x4 (&x)[U]) {
+  auto multiply = [&](u32x4 (&w)[4], u32x4 (&x)[X]) {
+    if constexpr (TURN) {
+      turn(w, c & 1, c & 2);
+      turn(x, c & 1, c & 2);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if constexpr (BF16) {
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[u]), as_bf16x8(w[u]), acc, 0, 0, 0);
-      } else {
+      for (int p = 0; p < 4; ++p) acc[0][0] = mma_pieces<BF16>(x[p], w[p], acc[0][0]);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[u][i]), __uint_as_float(w[u][i]), acc, 0, 0, 0);
-      }
+      for (int j = 0; j < X; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = mma_pieces<BF16>(x[j], w[i], acc[j][i]);
     }
   };
-  int r = wv;
-  if (r < rounds) load(r, wf[0], xf[0]);
-  while (r < rounds) {
-    if (r + nw < rounds) load(r + nw, wf[1], xf[1]);
+  const int steps = (kbytes + 255) / 256;
+  int s = wv;
+  if (s < steps) load(s, wf[0], xf[0]);
+  while (s < steps) {
+    if (s + nw < steps) load(s + nw, wf[1], xf[1]);
     multiply(wf[0], xf[0]);
-    r += nw;
-    if (r >= rounds) break;
-    if (r + nw < rounds) load(r + nw, wf[0], xf[0]);
+    s += nw;
+    if (s >= steps) break;
+    if (s + nw < steps) load(s + nw, wf[0], xf[0]);
     multiply(wf[1], xf[1]);
-    r += nw;
+    s += nw;
   }
-  *reinterpret_cast<f32x4*>(&part[wv][lane * 4]) = acc;
+  // The wave's sums, [token][row].  Lane l of a product holds its rows (tokens) 4 g + v, column (weight row) l % 16.
+  if constexpr (TURN) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) part[wv][(4 * g + v) * 16 + (lane & 15)] = acc[0][0][v];
+  } else {
+#pragma unroll
+    for (int j = 0; j < X; ++j) {
+      f32x4 sum;  // token (g, j), rows (b, i)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4& v = acc[j][i];
+        const float lo = c & 1 ? v[1] : v[0], hi = c & 1 ? v[3] : v[2];
+        float mine = c & 2 ? hi : lo;  // row c of column c
+        mine += __uint_as_float(from_xor1(__float_as_uint(mine)));
+        mine += __uint_as_float(from_xor2(__float_as_uint(mine)));
+        sum[i] = mine;
+      }
+      if (c == 0) *reinterpret_cast<f32x4*>(&part[wv][(X * g + j) * 16 + 4 * b]) = sum;
+    }
+  }
   lds_barrier();
-  for (int q = threadIdx.x; q < 256; q += blockDim.x) {
-    float s = 0.0f;
-    for (int w = 0; w < nw; ++w) s += part[w][q];
-    const int l = q >> 2, n = n0 + (l & 15), t = t0 + 4 * (l >> 4) + (q & 3);
-    if (n < a.N && t < a.T) finish(a, t, n, s);
+  for (int q = threadIdx.x; q < TOKENS * 16; q += blockDim.x) {
+    float sum = 0.0f;
+    for (int w = 0; w < nw; ++w) sum += part[w][q];
+    const int n = n0 + q % 16, t = t0 + q / 16;
+    if (n < a.N && t < a.T) finish(a, t, n, sum);
   }
 }
 
-template <bool BF16, int WAVES, int U>
-hipError_t launch_stream(const LinearArgs& a, hipStream_t st) {
-  const int rounds = (a.K * (BF16 ? 2 : 4) + 64 * U - 1) / (64 * U);
-  int waves = 1;  // no more than there are rounds
-  while (waves < WAVES && waves < rounds) waves *= 2;
-  const int n_tiles = (a.N + 15) / 16, t_tiles = (a.T + 15) / 16;
-  hipLaunchKernelGGL((linear_stream_kernel<BF16, WAVES, U>), dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * waves), 0, st, a,
-                     n_tiles);
+template <bool BF16, int TOKENS, int WAVES>
+hipError_t launch_stream_waves(const LinearArgs& a, hipStream_t st) {
+  const int steps = (a.K * (BF16 ? 2 : 4) + 255) / 256;
+  int waves = 1;  // no more than there are steps
+  while (waves < WAVES && waves < steps) waves *= 2;
+  const int n_tiles = (a.N + 15) / 16, t_tiles = (a.T + TOKENS - 1) / TOKENS;
+  hipLaunchKernelGGL((linear_stream_kernel<BF16, TOKENS, WAVES>), dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * waves), 0, st,
+                     a, n_tiles);
   return hipGetLastError();
+}
+
+template <bool BF16, int TOKENS>
+hipError_t launch_stream(const LinearArgs& a, bool few, hipStream_t st) {
+  return few ? launch_stream_waves<BF16, TOKENS, 16>(a, st) : launch_stream_waves<BF16, TOKENS, 8>(a, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -484,14 +565,15 @@ const TileShape kShapes[] = {
 
 }  // namespace
 
-// Few tokens take the stream kernel (the tiles' 32 token rows would be half of the loads: bf16, 65536 rows of 4096,
-// 4 tokens 87 us here, 97 in tiles, 16 tokens 122 and 101; f32, 4096 rows, 16 tokens 19 us and 24).  So do f32
-// results of few 16 x 16 tiles: a 32 x 32 tile is bound by the matrix unit of its CU, and four CUs share it here
-// (64 x 1024 x 4096 24 us in tiles, 17 here; 64 x 64 x 16384 85 and 58).  bf16 is not (64 x 1024 x 4096 8.4 us in tiles,
-// 9.8 here).
+// The stream kernel takes up to 16 tokens, where the tiles' 32 token rows would be half of the loads (bf16: 16 x 2048 x
+// 4096 6.0 us, 8.7 in tiles, 16 x 65536 x 4096 102 and 108; f32: 16 x 4096 x 4096 16 and 24), and results of so few 16 x 16
+// tiles that each has a CU: a 32 x 32 tile there waits for one CU's loads or matrix unit while others have nothing to do
+// (bf16: 64 x 512 x 4096 5.6 and 8.7, with twice the tiles 64 x 2048 x 4096 10.0 and 9.1; f32: 64 x 64 x 16384 35 and 85).
 hipError_t launch_linear(bool bf16, const LinearArgs& a, hipStream_t st) {
-  if (!bf16 && (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= 256) return launch_stream<false, 16, 6>(a, st);
-  if (a.T <= (bf16 ? 4 : 16)) return bf16 ? launch_stream<true, 8, 4>(a, st) : launch_stream<false, 8, 4>(a, st);
+  const bool few = (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= 256;
+  if (a.T <= 4) return bf16 ? launch_stream<true, 4>(a, few, st) : launch_stream<false, 4>(a, few, st);
+  if (bf16 && a.T <= 8) return launch_stream<true, 8>(a, few, st);
+  if (few || a.T <= 16) return bf16 ? launch_stream<true, 16>(a, few, st) : launch_stream<false, 16>(a, few, st);
   const TileShape* best = nullptr;
   float least = 0.0f;
   for (const TileShape& s : kShapes) {

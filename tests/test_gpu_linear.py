@@ -195,3 +195,20 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for _, _, _, y, want in jobs:
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("K", [8, 120, 128, 136, 264, 2040, 4104])
+def test_small_results_exactly(dt, K):
+    """Whole numbers, whose sums are exact: every form for few tokens or small results, rows and K that end inside its tiles and
+    steps, and nothing written outside y."""
+    g = torch.Generator().manual_seed(K)
+    X, W = torch.randint(-3, 4, (70, K), generator=g).double(), torch.randint(-3, 4, (300, K), generator=g).double()
+    x, w, ref = X.to(dt).cuda(), W.to(dt).cuda(), X @ W.t()
+    for T in (1, 2, 3, 4, 5, 7, 8, 9, 12, 15, 16, 17, 31, 33, 70):
+        for N in (1, 7, 15, 16, 17, 40, 300):
+            y = torch.full((T + 1, N + 3), 77.0, device="cuda")
+            moe.moe_linear(w[:N], x[:T], None, 0, None, y[:T, :N])
+            got = y.cpu().double()
+            assert torch.equal(got[:T, :N], ref[:T, :N]), (T, N)
+            assert (got[T] == 77).all() and (got[:, N:] == 77).all(), (T, N)
