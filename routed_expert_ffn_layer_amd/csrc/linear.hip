@@ -112,8 +112,7 @@ constexpr int kPast = 0x7ffffff0;  // an offset past the end of every buffer mad
 //  * 16 tokens: registers i and lanes c change places first (a transpose inside each quad), then register c is piece
 //    4 g + c of row lane % 16.  32 moves and 32 choices a KB of f32 or bf16, where the other way would be four times the
 //    products (bf16 16 x 64 x 1024 3.3 us, 3.8 the other way).
-// 16 waves where the workgroups do not fill the chip, else 8 (bf16 4 x 8192 x 4096 12.0 us, 14.6 in 16 waves;
-// 4 x 2048 x 16384 14.9 and 13.0).
+// 8 waves, or as many as there are steps (weights from memory: 1 x 4096 x 4096 8.1 us, in 16 waves 9.1, in 4 9.0).
 // ---------------------------------------------------------------------------
 // v of another lane of the quad.
 template <int CTRL>
@@ -151,9 +150,11 @@ __device__ __forceinline__ f32x4 mma_pieces(u32x4 a, u32x4 b, f32x4 c) {
   }
 }
 
-template <bool BF16, int TOKENS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void linear_stream_kernel(LinearArgs a, int n_tiles) {
-  __shared__ float part[WAVES][TOKENS * 16];
+constexpr int kStreamWaves = 8;
+
+template <bool BF16, int TOKENS>
+__global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a, int n_tiles) {
+  __shared__ float part[kStreamWaves][TOKENS * 16];
   constexpr int ES = BF16 ? 2 : 4, X = TOKENS / 4;
   constexpr bool TURN = TOKENS == 16;
   const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6), nw = blockDim.x >> 6;
@@ -241,20 +242,15 @@ __global__ __launch_bounds__(64 * WAVES) void linear_stream_kernel(LinearArgs a,
   }
 }
 
-template <bool BF16, int TOKENS, int WAVES>
-hipError_t launch_stream_waves(const LinearArgs& a, hipStream_t st) {
-  const int steps = (a.K * (BF16 ? 2 : 4) + 255) / 256;
-  int waves = 1;  // no more than there are steps
-  while (waves < WAVES && waves < steps) waves *= 2;
-  const int n_tiles = (a.N + 15) / 16, t_tiles = (a.T + TOKENS - 1) / TOKENS;
-  hipLaunchKernelGGL((linear_stream_kernel<BF16, TOKENS, WAVES>), dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * waves), 0, st,
-                     a, n_tiles);
-  return hipGetLastError();
-}
-
 template <bool BF16, int TOKENS>
-hipError_t launch_stream(const LinearArgs& a, bool few, hipStream_t st) {
-  return few ? launch_stream_waves<BF16, TOKENS, 16>(a, st) : launch_stream_waves<BF16, TOKENS, 8>(a, st);
+hipError_t launch_stream(const LinearArgs& a, hipStream_t st) {
+  const int steps = (a.K * (BF16 ? 2 : 4) + 255) / 256;
+  int waves = 1;
+  while (waves < kStreamWaves && waves < steps) waves *= 2;
+  const int n_tiles = (a.N + 15) / 16, t_tiles = (a.T + TOKENS - 1) / TOKENS;
+  hipLaunchKernelGGL((linear_stream_kernel<BF16, TOKENS>), dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * waves), 0, st, a,
+                     n_tiles);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -540,8 +536,8 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
   const int n_tiles = (a.N + BN - 1) / BN, t_tiles = (a.T + BT - 1) / BT;
   constexpr int ring = D * (BN + BT) * kRow, out = WN * WT * WK * out_bytes(BN / WN / 32);
   constexpr int lds = ring > out ? ring : out;
-  hipLaunchKernelGGL((linear_tile_kernel<BF16, BN, BT, WN, WT, WK, D>), dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * WN * WT * WK),
-                     lds, st, a, n_tiles, t_tiles);
+  hipLaunchKernelGGL((linear_tile_kernel<BF16, BN, BT, WN, WT, WK, D>), dim3((unsigned)(n_tiles * t_tiles)),
+                     dim3(64 * WN * WT * WK), lds, st, a, n_tiles, t_tiles);
   return hipGetLastError();
 }
 
@@ -554,7 +550,8 @@ struct TileShape {
   float us[2];  // f32, bf16
   hipError_t (*launch[2])(const LinearArgs&, hipStream_t);
 };
-#define TILE(BN, BT, F, B, ...) {BN, BT, {F, B}, {launch_tile<false, BN, BT, __VA_ARGS__>, launch_tile<true, BN, BT, __VA_ARGS__>}}
+#define TILE(BN, BT, F, B, ...) \
+  {BN, BT, {F, B}, {launch_tile<false, BN, BT, __VA_ARGS__>, launch_tile<true, BN, BT, __VA_ARGS__>}}
 const TileShape kShapes[] = {
     TILE(256, 256, 7.4f, 1.77f, 4, 2, 1, 2), TILE(256, 128, 3.8f, 0.99f, 4, 2, 1, 3),
     TILE(128, 128, 2.0f, 0.55f, 2, 2, 2, 4), TILE(128, 64, 1.1f, 0.37f, 2, 1, 2, 4),
@@ -565,15 +562,16 @@ const TileShape kShapes[] = {
 
 }  // namespace
 
-// The stream kernel takes up to 16 tokens, where the tiles' 32 token rows would be half of the loads (bf16: 16 x 2048 x
-// 4096 6.0 us, 8.7 in tiles, 16 x 65536 x 4096 102 and 108; f32: 16 x 4096 x 4096 16 and 24), and results of so few 16 x 16
+// The stream kernel takes up to 16 tokens, where the tiles' 32 token rows would be half of the loads (weights from
+// memory, bf16: 16 x 4096 x 4096 9.3 us, 12 in tiles, 16 x 65536 x 4096 100 and 104, but 16 x 8192 x 16384 65 and 62; f32:
+// 16 x 4096 x 4096 19 and 24), and results of so few 16 x 16
 // tiles that each has a CU: a 32 x 32 tile there waits for one CU's loads or matrix unit while others have nothing to do
 // (bf16: 64 x 512 x 4096 5.6 and 8.7, with twice the tiles 64 x 2048 x 4096 10.0 and 9.1; f32: 64 x 64 x 16384 35 and 85).
 hipError_t launch_linear(bool bf16, const LinearArgs& a, hipStream_t st) {
   const bool few = (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= 256;
-  if (a.T <= 4) return bf16 ? launch_stream<true, 4>(a, few, st) : launch_stream<false, 4>(a, few, st);
-  if (bf16 && a.T <= 8) return launch_stream<true, 8>(a, few, st);
-  if (few || a.T <= 16) return bf16 ? launch_stream<true, 16>(a, few, st) : launch_stream<false, 16>(a, few, st);
+  if (a.T <= 4) return bf16 ? launch_stream<true, 4>(a, st) : launch_stream<false, 4>(a, st);
+  if (bf16 && a.T <= 8) return launch_stream<true, 8>(a, st);
+  if (few || a.T <= 16) return bf16 ? launch_stream<true, 16>(a, st) : launch_stream<false, 16>(a, st);
   const TileShape* best = nullptr;
   float least = 0.0f;
   for (const TileShape& s : kShapes) {
