@@ -13,7 +13,8 @@
 // at 6.2 TB/s), 256 x 4096 x 4096 16.3 (19.7), 1024 x 4096 x 4096 35.6 (37.4), 4096 x 8192 x 4096 220 (177 once both
 // are warm; 1.25 PFLOP/s);
 // f32: 4 x 512 x 4096 7.4 (9.9), 32 x 2048 x 2048 8.1 (8.6), 16 x 4096 x 4096 16 (14.2), 64 x 4096 x 4096 26 (23.5),
-// 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).
+// 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).  Behind the library stay f32 products of few tiles and deep K, where it
+// spreads K over the chip and adds up in memory: 64 x 64 x 16384 36 (26), 256 x 512 x 14400 66 (48).
 #include "ffn_common.hpp"
 #include "kernels.hpp"
 #include "row_io.hpp"
@@ -564,11 +565,12 @@ const TileShape kShapes[] = {
 
 // The stream kernel takes up to 16 tokens, where the tiles' 32 token rows would be half of the loads (weights from
 // memory, bf16: 16 x 4096 x 4096 9.3 us, 12 in tiles, 16 x 65536 x 4096 100 and 104, but 16 x 8192 x 16384 65 and 62; f32:
-// 16 x 4096 x 4096 19 and 24), and results of so few 16 x 16
-// tiles that each has a CU: a 32 x 32 tile there waits for one CU's loads or matrix unit while others have nothing to do
-// (bf16: 64 x 512 x 4096 5.6 and 8.7, with twice the tiles 64 x 2048 x 4096 10.0 and 9.1; f32: 64 x 64 x 16384 35 and 85).
+// 16 x 4096 x 4096 19 and 24), and results of few 16 x 16 tiles: a 32 x 32 tile there waits for one CU's loads or
+// matrix unit while others have nothing to do (bf16, up to one tile a CU: 64 x 512 x 4096 5.6 us, 8.7 in tiles of 32, with
+// twice the tiles 64 x 2048 x 4096 10.0 and 9.1; f32, up to two: 64 x 64 x 16384 35 and 85, 256 x 512 x 4096 21.9 and 24.6,
+// 1000 x 80 x 4096 26 and 24).
 hipError_t launch_linear(bool bf16, const LinearArgs& a, hipStream_t st) {
-  const bool few = (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= 256;
+  const bool few = (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= (bf16 ? 256 : 512);
   if (a.T <= 4) return bf16 ? launch_stream<true, 4>(a, st) : launch_stream<false, 4>(a, st);
   if (bf16 && a.T <= 8) return launch_stream<true, 8>(a, st);
   if (few || a.T <= 16) return bf16 ? launch_stream<true, 16>(a, st) : launch_stream<false, 16>(a, st);
