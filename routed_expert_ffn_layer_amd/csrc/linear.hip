@@ -1,20 +1,19 @@
 // linear.hip -- y = act(x W^T + bias) + res for f32 or bf16 weights stored as they come, one row of W
 // after another.
 //
-// Two kernels.  linear_stream_kernel, for few tokens or small results: every wave multiplies 16 weight rows by 4, 8
-// or 16 tokens over its part of K, operands straight from memory in registers, and the waves of a workgroup, which
-// split K between them, add up in LDS; no barrier and no staging before that.
-// linear_tile_kernel, for all else: tiles staged through LDS, from 32 x 32 (weights are the work: many small
-// workgroups, deep in flight) to 256 x 256 (the matrix instructions are).  Sums in f32, in an order fixed by
-// the shape.
+// Three kernels.  linear_stream_kernel, for up to 8 tokens: every wave multiplies 16 weight rows by 4 or 8 tokens over its
+// part of K, operands straight from memory in registers, and the waves of a workgroup, which split K between
+// them, add up in LDS.  linear_small_kernel, for up to 16 tokens or small results: the same with 16 tokens and operands
+// through LDS, each wave for itself.  linear_tile_kernel, for all else: tiles staged through LDS by the whole workgroup,
+// from 32 x 32 (weights are the work: many small workgroups, deep in flight) to 256 x 256 (the matrix instructions
+// are).  Sums in f32, in an order fixed by the shape.
 //
 // Measured on an MI355X, bf16, x weights x K (plain library product beside it): 1 x 4096 x 4096 4.5 us (10.5),
-// 16 x 512 x 4096 5.3 (8.0), 16 x 12288 x 4096 17.4 (20.7), 64 x 4096 x 4096 9.1 (19), 4 x 65536 x 4096 87 (124; 537 MB
+// 16 x 512 x 4096 4.9 (8.0), 16 x 12288 x 4096 17.5 (21), 64 x 4096 x 4096 9.1 (19), 4 x 65536 x 4096 87 (124; 537 MB
 // at 6.2 TB/s), 256 x 4096 x 4096 16.3 (19.7), 1024 x 4096 x 4096 35.6 (37.4), 4096 x 8192 x 4096 220 (177 once both
-// are warm; 1.25 PFLOP/s);
-// f32: 4 x 512 x 4096 7.4 (9.9), 32 x 2048 x 2048 8.1 (8.6), 16 x 4096 x 4096 16 (14.2), 64 x 4096 x 4096 26 (23.5),
-// 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).  Behind the library stay f32 products of few tiles and deep K, where it
-// spreads K over the chip and adds up in memory: 64 x 64 x 16384 36 (26), 256 x 512 x 14400 66 (48).
+// are warm; 1.25 PFLOP/s); f32: 4 x 512 x 4096 7.4 (9.9), 16 x 64 x 4096 7.9 (9.7), 32 x 2048 x 2048 6.0 (8.9),
+// 64 x 4096 x 4096 25 (22), 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).  Behind the library stay f32 products of about two
+// 16 x 16 tiles a CU and deep K, where it spreads K over the chip and adds up in memory: 85 x 864 x 14400 56 (41).
 #include "ffn_common.hpp"
 #include "kernels.hpp"
 #include "row_io.hpp"
@@ -99,20 +98,18 @@ __device__ __forceinline__ void finish8(const LinearArgs& a, int64_t t, int n, f
 constexpr int kPast = 0x7ffffff0;  // an offset past the end of every buffer made here (under 2^30 bytes): reads as 0
 
 // ---------------------------------------------------------------------------
-// 16 weight rows by TOKENS tokens a workgroup; its waves take steps of 256 bytes of K in turn, the next step's loads on
-// their way while one is multiplied, and add up in LDS.
+// Up to 4 or 8 tokens, 16 weight rows a workgroup; its waves take steps of 256 bytes of K in turn, the next step's loads
+// on their way while one is multiplied, and add up in LDS.
 //
 // Memory is quick where four neighbouring lanes read 64 bytes in a row (with neighbours in different rows a CU
 // got 35 GB/s, 1 x 4096 x 4096 took 7.4 us; now 4.5).  So load i of a step gives lane (g, b, c), g = lane / 16,
-// b = lane / 4 % 4, c = lane % 4, the 16-byte piece 4 g + c of row 4 b + i (tokens, if fewer than 16: row (b, i) of
-// TOKENS / 4 loads).  v_mfma_f32_16x16x32_bf16 (f32: four v_mfma_f32_16x16x4_f32) takes lane % 16 for the row and
-// lane / 16 for the piece.  Two ways to make them meet:
-//  * up to 8 tokens: multiplied as it lies.  "Row" (b, c) of the product is piece c of row b alone, so of its 16 x 16
-//    results those with the same c on both sides count, four of which make up a sum, and every pair of loads has a
-//    product of its own: TOKENS / 4 times the products, with no work between load and product.
-//  * 16 tokens: registers i and lanes c change places first (a transpose inside each quad), then register c is piece
-//    4 g + c of row lane % 16.  32 moves and 32 choices a KB of f32 or bf16, where the other way would be four times the
-//    products (bf16 16 x 64 x 1024 3.3 us, 3.8 the other way).
+// b = lane / 4 % 4, c = lane % 4, the 16-byte piece 4 g + c of weight row 4 b + i, or of token X b + i of X = TOKENS / 4
+// loads.  v_mfma_f32_16x16x32_bf16 (f32: four v_mfma_f32_16x16x4_f32) takes lane % 16 for its row, so "row" (b, c) of a
+// product is piece c of row b alone: of its 16 x 16 results those with the same c on both sides count, four of
+// which make up a sum, and every weight load is multiplied with every token load.  That is X times the products of
+// a layout by rows, with no work between load and product (moving the registers into that layout takes 64 moves and
+// choices for 4 KB: 4 x 4096 x 4096 6.5 us instead of 4.8).
+//
 // 8 waves, or as many as there are steps (weights from memory: 1 x 4096 x 4096 8.1 us, in 16 waves 9.1, in 4 9.0).
 // ---------------------------------------------------------------------------
 // v of another lane of the quad.
@@ -122,21 +119,6 @@ __device__ __forceinline__ unsigned quad_u32(unsigned v) {
 }
 __device__ __forceinline__ unsigned from_xor1(unsigned v) { return quad_u32<0xb1>(v); }
 __device__ __forceinline__ unsigned from_xor2(unsigned v) { return quad_u32<0x4e>(v); }
-
-// v[i] of lane c of each quad <-> v[c] of lane i.  Both sides of each choice are formed outside it: a lane that
-// another one reads has to be active.
-__device__ __forceinline__ void turn(u32x4 (&v)[4], bool odd, bool high) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const unsigned p0 = from_xor1(v[0][e]), p1 = from_xor1(v[1][e]), p2 = from_xor1(v[2][e]), p3 = from_xor1(v[3][e]);
-    const unsigned a0 = odd ? p1 : v[0][e], a1 = odd ? v[1][e] : p0, a2 = odd ? p3 : v[2][e], a3 = odd ? v[3][e] : p2;
-    const unsigned q0 = from_xor2(a0), q1 = from_xor2(a1), q2 = from_xor2(a2), q3 = from_xor2(a3);
-    v[0][e] = high ? q2 : a0;
-    v[1][e] = high ? q3 : a1;
-    v[2][e] = high ? a2 : q0;
-    v[3][e] = high ? a3 : q1;
-  }
-}
 
 // c += A . B: 16 rows by 16 over four pieces, 32 bf16 or 16 f32.
 template <bool BF16>
@@ -154,27 +136,25 @@ __device__ __forceinline__ f32x4 mma_pieces(u32x4 a, u32x4 b, f32x4 c) {
 constexpr int kStreamWaves = 8;
 
 template <bool BF16, int TOKENS>
-__global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a, int n_tiles) {
+__global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a) {
   __shared__ float part[kStreamWaves][TOKENS * 16];
   constexpr int ES = BF16 ? 2 : 4, X = TOKENS / 4;
-  constexpr bool TURN = TOKENS == 16;
   const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6), nw = blockDim.x >> 6;
   const int g = lane >> 4, b = lane >> 2 & 3, c = lane & 3;
-  const int n0 = (int)(blockIdx.x % n_tiles) * 16, t0 = (int)(blockIdx.x / n_tiles) * TOKENS;
+  const int n0 = (int)blockIdx.x * 16;
   const int kbytes = a.K * ES;
   // the tile's rows, and nothing behind them
   const auto wbuf = make_rsrc(static_cast<const uint8_t*>(a.w) + n0 * a.w_ld * ES,
                               (min(a.N - n0, 16) - 1) * a.w_ld * ES + kbytes);
-  const auto xbuf = make_rsrc(static_cast<const uint8_t*>(a.x) + t0 * a.x_ld * ES,
-                              (min(a.T - t0, TOKENS) - 1) * a.x_ld * ES + kbytes);
+  const auto xbuf = make_rsrc(a.x, (a.T - 1) * a.x_ld * ES + kbytes);
   // this lane's pieces of the first step; rows past the end read as 0
   const int piece = 16 * (4 * g + c);
   unsigned wo[4], xo[X];
 #pragma unroll
   for (int i = 0; i < 4; ++i) wo[i] = n0 + 4 * b + i < a.N ? (int)((4 * b + i) * a.w_ld * ES) + piece : kPast;
 #pragma unroll
-  for (int i = 0; i < X; ++i) xo[i] = t0 + X * b + i < a.T ? (int)((X * b + i) * a.x_ld * ES) + piece : kPast;
-  f32x4 acc[TURN ? 1 : X][TURN ? 1 : 4];
+  for (int i = 0; i < X; ++i) xo[i] = X * b + i < a.T ? (int)((X * b + i) * a.x_ld * ES) + piece : kPast;
+  f32x4 acc[X][4];
 #pragma unroll
   for (auto& row : acc)
 #pragma unroll
@@ -189,18 +169,11 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
       if (i < X) x[i] = bld16(xbuf, (int)((in ? xo[i] : kPast) + at), 0);
     }
   };
-  auto multiply = [&](u32x4 (&w)[4], u32x4 (&x)[X]) {
-    if constexpr (TURN) {
-      turn(w, c & 1, c & 2);
-      turn(x, c & 1, c & 2);
+  auto multiply = [&](const u32x4 (&w)[4], const u32x4 (&x)[X]) {
 #pragma unroll
-      for (int p = 0; p < 4; ++p) acc[0][0] = mma_pieces<BF16>(x[p], w[p], acc[0][0]);
-    } else {
+    for (int j = 0; j < X; ++j)
 #pragma unroll
-      for (int j = 0; j < X; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = mma_pieces<BF16>(x[j], w[i], acc[j][i]);
-    }
+      for (int i = 0; i < 4; ++i) acc[j][i] = mma_pieces<BF16>(x[j], w[i], acc[j][i]);
   };
   const int steps = (kbytes + 255) / 256;
   int s = wv;
@@ -215,30 +188,25 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
     s += nw;
   }
   // The wave's sums, [token][row].  Lane l of a product holds its rows (tokens) 4 g + v, column (weight row) l % 16.
-  if constexpr (TURN) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) part[wv][(4 * g + v) * 16 + (lane & 15)] = acc[0][0][v];
-  } else {
+  for (int j = 0; j < X; ++j) {
+    f32x4 sum;  // token (g, j), rows (b, i)
 #pragma unroll
-    for (int j = 0; j < X; ++j) {
-      f32x4 sum;  // token (g, j), rows (b, i)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4& v = acc[j][i];
-        const float lo = c & 1 ? v[1] : v[0], hi = c & 1 ? v[3] : v[2];
-        float mine = c & 2 ? hi : lo;  // row c of column c
-        mine += __uint_as_float(from_xor1(__float_as_uint(mine)));
-        mine += __uint_as_float(from_xor2(__float_as_uint(mine)));
-        sum[i] = mine;
-      }
-      if (c == 0) *reinterpret_cast<f32x4*>(&part[wv][(X * g + j) * 16 + 4 * b]) = sum;
+    for (int i = 0; i < 4; ++i) {
+      const f32x4& v = acc[j][i];
+      const float lo = c & 1 ? v[1] : v[0], hi = c & 1 ? v[3] : v[2];
+      float mine = c & 2 ? hi : lo;  // row c of column c
+      mine += __uint_as_float(from_xor1(__float_as_uint(mine)));
+      mine += __uint_as_float(from_xor2(__float_as_uint(mine)));
+      sum[i] = mine;
     }
+    if (c == 0) *reinterpret_cast<f32x4*>(&part[wv][(X * g + j) * 16 + 4 * b]) = sum;
   }
   lds_barrier();
   for (int q = threadIdx.x; q < TOKENS * 16; q += blockDim.x) {
     float sum = 0.0f;
     for (int w = 0; w < nw; ++w) sum += part[w][q];
-    const int n = n0 + q % 16, t = t0 + q / 16;
+    const int n = n0 + q % 16, t = q / 16;
     if (n < a.N && t < a.T) finish(a, t, n, sum);
   }
 }
@@ -248,33 +216,11 @@ hipError_t launch_stream(const LinearArgs& a, hipStream_t st) {
   const int steps = (a.K * (BF16 ? 2 : 4) + 255) / 256;
   int waves = 1;
   while (waves < kStreamWaves && waves < steps) waves *= 2;
-  const int n_tiles = (a.N + 15) / 16, t_tiles = (a.T + TOKENS - 1) / TOKENS;
-  hipLaunchKernelGGL((linear_stream_kernel<BF16, TOKENS>), dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * waves), 0, st, a,
-                     n_tiles);
+  hipLaunchKernelGGL((linear_stream_kernel<BF16, TOKENS>), dim3((unsigned)((a.N + 15) / 16)), dim3(64 * waves), 0, st, a);
   return hipGetLastError();
 }
 
-// ---------------------------------------------------------------------------
-// More tokens.  A workgroup computes BN weight rows by BT tokens on WN x WT x WK waves: WN x WT of them side by
-// side, and WK that share a part of the tile and split K between them (their sums meet in LDS at the end).  K
-// goes in stages of 128 bytes, both operands' rows of a stage straight from memory into one of D LDS buffers,
-// the next ones in flight while one is multiplied.  Matrix instruction v_mfma_f32_32x32x16_bf16 or
-// v_mfma_f32_32x32x2_f32, weights as A and tokens as B.  Lane l supplies row l % 32, 16-byte piece 2 m + l / 32 of
-// the row in step m of the stage.  Piece p of row r sits at place p ^ swz(r).
-//
-// Each step is laid out by hand: a product, an operand read of the next step, a load of a later stage, the next
-// product, .. (reads, loads and products one after the other: 4096 x 8192 x 4096 in 267 us, so 220).  What bounds
-// the largest tile now is the loads: with the same products and none of them in the loop it takes 193 us, with all
-// of them from the same stage 216; without the barrier nothing changes.  The matrix unit is busy in 72 to 77% of
-// the cycles, at a clock that this work holds near 1.5 GHz.  Measured and not kept: 4 waves of 128 x 128 (324 us:
-// one wave per SIMD), stages of 64 bytes with 4 or 5 buffers (231), workgroups starting at other columns (neutral
-// or slower).
-// ---------------------------------------------------------------------------
 constexpr int kRow = 128;  // bytes of a row in a stage
-
-// Results of a wave in LDS: 32 tokens by one or two 32-row tiles, padded against bank conflicts.
-constexpr int out_ld(int tiles) { return 32 * (tiles % 2 ? 1 : 2) + 4; }
-constexpr int out_bytes(int tiles) { return 32 * out_ld(tiles) * 4; }
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
@@ -297,6 +243,120 @@ __device__ __forceinline__ void wait_loads() {
 // of each half first, then the others.  The XOR term gives the rows of each of these groups places of their own
 // (no bank conflicts counted; (r + r / 8) % 8 for 128-byte rows cost 4 cycles a read).
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+
+// ---------------------------------------------------------------------------
+// More tokens with few results: 16 weight rows by 16 tokens a workgroup.  Each of its 8 waves works alone, on steps of
+// 128 bytes of K in turn: both operands' rows straight from memory into its own two LDS buffers, 8 rows of whole lines a
+// load, one step ahead; no barrier until the waves add up.  Operands as in the tile kernel below, places by the same swz:
+// lane l reads piece 4 m + l / 16 of row l % 16 for product m.  Of a step's time the loads take 64 cycles of its CU and
+// the f32 products as many.  Measured (operands in registers instead, moved into place; plain library product): f32
+// 16 x 64 x 4096 7.9 us (11.5; 9.7), 32 x 2048 x 2048 6.0 (8.4; 8.9), bf16 16 x 2048 x 4096 5.5 (6.2; 8.2).  Three or four
+// buffers instead of two: one workgroup in a CU, 16 x 65536 x 4096 102 us becomes 118 and 120.
+// ---------------------------------------------------------------------------
+constexpr int kSmallBuf = 32 * kRow;
+
+template <bool BF16>
+__global__ __launch_bounds__(64 * kStreamWaves) void linear_small_kernel(LinearArgs a, int n_tiles) {
+  extern __shared__ uint8_t smem[];
+  constexpr int ES = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6), nw = blockDim.x >> 6;
+  const int n0 = (int)(blockIdx.x % n_tiles) * 16, t0 = (int)(blockIdx.x / n_tiles) * 16;
+  const int kbytes = a.K * ES, wrows = min(16, a.N - n0), xrows = min(16, a.T - t0);
+  const auto wbuf = make_rsrc(static_cast<const uint8_t*>(a.w) + n0 * a.w_ld * ES, (wrows - 1) * a.w_ld * ES + kbytes);
+  const auto xbuf = make_rsrc(static_cast<const uint8_t*>(a.x) + t0 * a.x_ld * ES, (xrows - 1) * a.x_ld * ES + kbytes);
+  uint8_t* mine = smem + wv * 2 * kSmallBuf;
+  // load i of a step: rows 8 i .. 8 i + 7 of weights, then of tokens; rows past the end repeat the last one
+  const int col0 = ((lane & 7) ^ swz(lane >> 3)) * 16, col1 = ((lane & 7) ^ swz(8 + (lane >> 3))) * 16;
+  unsigned off[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 8 * (i & 1) + (lane >> 3);
+    off[i] = (unsigned)((i < 2 ? min(row, wrows - 1) * a.w_ld : min(row, xrows - 1) * a.x_ld) * ES) + (i & 1 ? col1 : col0);
+  }
+  auto load = [&](int s, uint8_t* buf) {  // steps past the last read nothing
+    const int at = s * kRow;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int from = (int)(at + (i & 1 ? col1 : col0) < kbytes ? off[i] + at : kPast);
+      if (i < 2)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_ptr)(buf + i * 1024), 16, from, 0, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(xbuf, (lds_ptr)(buf + i * 1024), 16, from, 0, 0, 0);
+    }
+  };
+  const int row = lane & 15, g = lane >> 4;
+  int place[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) place[m] = row * kRow + (((4 * m + g) ^ swz(row)) << 4);
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  const int steps = (kbytes + kRow - 1) / kRow;
+  load(wv, mine);
+  for (int s = wv, slot = 0; s < steps; s += nw, slot ^= 1) {
+    load(s + nw, mine + (slot ^ 1) * kSmallBuf);
+    wait_loads<4, false>();  // this step has landed
+    asm volatile("" ::: "memory");
+    const uint8_t* buf = mine + slot * kSmallBuf;
+    u32x4 w[2], x[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      w[m] = *reinterpret_cast<const u32x4*>(buf + place[m]);
+      x[m] = *reinterpret_cast<const u32x4*>(buf + 16 * kRow + place[m]);
+    }
+    if (s == steps - 1) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        if (s * kRow + 16 * (4 * m + g) >= kbytes) w[m] = x[m] = u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) acc[m] = mma_pieces<BF16>(x[m], w[m], acc[m]);
+    asm volatile("" ::: "memory");
+    wait_loads<63, true>();  // the buffer is read: the next load may go into it
+    asm volatile("" ::: "memory");
+  }
+  wait_loads<0, true>();  // no load is on its way to the sums' place
+  asm volatile("" ::: "memory");
+  float* part = reinterpret_cast<float*>(mine);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) part[(4 * g + v) * 16 + row] = acc[0][v] + acc[1][v];
+  lds_barrier();
+  for (int q = threadIdx.x; q < 256; q += blockDim.x) {
+    float sum = 0.0f;
+    for (int w = 0; w < nw; ++w) sum += reinterpret_cast<const float*>(smem + w * 2 * kSmallBuf)[q];
+    const int n = n0 + q % 16, t = t0 + q / 16;
+    if (n < a.N && t < a.T) finish(a, t, n, sum);
+  }
+}
+
+template <bool BF16>
+hipError_t launch_small(const LinearArgs& a, hipStream_t st) {
+  const int steps = (a.K * (BF16 ? 2 : 4) + kRow - 1) / kRow;
+  int waves = 1;
+  while (waves < kStreamWaves && waves < steps) waves *= 2;
+  const int n_tiles = (a.N + 15) / 16, t_tiles = (a.T + 15) / 16;
+  hipLaunchKernelGGL(linear_small_kernel<BF16>, dim3((unsigned)(n_tiles * t_tiles)), dim3(64 * waves),
+                     waves * 2 * kSmallBuf, st, a, n_tiles);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// More tokens.  A workgroup computes BN weight rows by BT tokens on WN x WT x WK waves: WN x WT of them side by
+// side, and WK that share a part of the tile and split K between them (their sums meet in LDS at the end).  K
+// goes in stages of 128 bytes, both operands' rows of a stage straight from memory into one of D LDS buffers,
+// the next ones in flight while one is multiplied.  Matrix instruction v_mfma_f32_32x32x16_bf16 or
+// v_mfma_f32_32x32x2_f32, weights as A and tokens as B.  Lane l supplies row l % 32, 16-byte piece 2 m + l / 32 of
+// the row in step m of the stage.  Piece p of row r sits at place p ^ swz(r).
+//
+// Each step is laid out by hand: a product, an operand read of the next step, a load of a later stage, the next
+// product, .. (reads, loads and products one after the other: 4096 x 8192 x 4096 in 267 us, so 220).  What bounds
+// the largest tile now is the loads: with the same products and none of them in the loop it takes 193 us, with all
+// of them from the same stage 216; without the barrier nothing changes.  The matrix unit is busy in 72 to 77% of
+// the cycles, at a clock that this work holds near 1.5 GHz.  Measured and not kept: 4 waves of 128 x 128 (324 us:
+// one wave per SIMD), stages of 64 bytes with 4 or 5 buffers (231), workgroups starting at other columns (neutral
+// or slower).
+// ---------------------------------------------------------------------------
+// Results of a wave in LDS: 32 tokens by one or two 32-row tiles, padded against bank conflicts.
+constexpr int out_ld(int tiles) { return 32 * (tiles % 2 ? 1 : 2) + 4; }
+constexpr int out_bytes(int tiles) { return 32 * out_ld(tiles) * 4; }
 
 // acc += A . B over 32 bytes of K: 16 bf16, or 8 f32 in four products (the k-th of both halves' pieces each).
 template <bool BF16>
@@ -563,17 +623,18 @@ const TileShape kShapes[] = {
 
 }  // namespace
 
-// The stream kernel takes up to 16 tokens, where the tiles' 32 token rows would be half of the loads (weights from
-// memory, bf16: 16 x 4096 x 4096 9.3 us, 12 in tiles, 16 x 65536 x 4096 100 and 104, but 16 x 8192 x 16384 65 and 62; f32:
-// 16 x 4096 x 4096 19 and 24), and results of few 16 x 16 tiles: a 32 x 32 tile there waits for one CU's loads or
-// matrix unit while others have nothing to do (bf16, up to one tile a CU: 64 x 512 x 4096 5.6 us, 8.7 in tiles of 32, with
-// twice the tiles 64 x 2048 x 4096 10.0 and 9.1; f32, up to two: 64 x 64 x 16384 35 and 85, 256 x 512 x 4096 21.9 and 24.6,
-// 1000 x 80 x 4096 26 and 24).
+// Up to 8 tokens (f32: 4) the stream kernel.  The small kernel takes up to 16, where the tiles' 32 token rows would be
+// half of the loads (weights from memory, bf16: 16 x 4096 x 4096 9.7 us, 12 in tiles, 16 x 65536 x 4096 102 and 104; f32:
+// 16 x 4096 x 4096 17.5 and 24), and few 16 x 16 tiles: a 32 x 32 tile there waits for one CU's loads or matrix unit
+// while others have nothing to do.  bf16, up to one tile a CU: 64 x 512 x 4096 4.9 us, 8.7 in tiles of 32; up to two
+// where K is short (100 x 600 x 2048 5.3 and 6.3, x 4096 7.4 and 8.8, but 1000 x 100 x 4096 12.3 and 9.0, 64 x 2048 x 16384
+// 29 and 24).  f32, up to two: 64 x 64 x 14400 22 and 75, 256 x 512 x 4096 15.4 and 24.6; four: 64 x 4096 x 4096 41
+// and 25.
 hipError_t launch_linear(bool bf16, const LinearArgs& a, hipStream_t st) {
-  const bool few = (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= (bf16 ? 256 : 512);
+  const bool few = (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= (bf16 && a.K > 2048 ? 256 : 512);
   if (a.T <= 4) return bf16 ? launch_stream<true, 4>(a, st) : launch_stream<false, 4>(a, st);
   if (bf16 && a.T <= 8) return launch_stream<true, 8>(a, st);
-  if (few || a.T <= 16) return bf16 ? launch_stream<true, 16>(a, st) : launch_stream<false, 16>(a, st);
+  if (few || a.T <= 16) return bf16 ? launch_small<true>(a, st) : launch_small<false>(a, st);
   const TileShape* best = nullptr;
   float least = 0.0f;
   for (const TileShape& s : kShapes) {
