@@ -103,12 +103,14 @@ def forward_block(b: BlockBuffers, res, w_router, pre, post, slot_pool, slot_str
 
     pre, post: norms as moe_block_norm takes them, None for none; w_router [E][H] of the activations' type
     (f32 for f32 experts, else bf16); gate [H], [T][H] or None.  x: the layer's input where the block before
-    has made it (its next_pre), pre is not looked at then.  With next_pre the norm of the next block is taken in
+    has made it (its next_pre), [T][H] of the activations' type, contiguous; pre is not looked at then.  With next_pre the norm of the next block is taken in
     the same call, and its input, b.x_next, returned; otherwise res is.  The whole block is 4 calls of the
     library for up to 40 tokens (few_tokens), 6 above."""
     if x is None:
         moe.moe_block_norm(None, None, None, 1.0, res, 1.0, pre, eps, None, b.x, stream)
         x = b.x
+    else:  # the products read x by rows, the experts its address alone
+        moe._exactly(x, "x", "f32" if b.wdt == moe.MOE_F32 else "bf16", b.T, b.H)
     moe.moe_linear(w_router, x, None, moe.MOE_ACT_NONE, None, b.logits, stream)
     run = forward_decode if few_tokens(b) else forward
     y = run(b, b.logits, x, slot_pool, slot_stride, slot_of_expert, shared_w, stream)
