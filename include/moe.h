@@ -506,9 +506,10 @@ int moe_block_norm(const void* block, int bdt, int64_t b_ld, int post_kind, cons
  *     d_logits[t][e] = sum over j with topk_ids[t][j] = e of w_j (d_w_j - sum_i w_i d_w_i)
  * for all e (0 where e was not selected; the selection itself has no gradient); [T][E] f32.
  *
- * All: 0 <= T <= 2^21, 1 <= k <= 32, H any positive up to 2^24.  Results that lie on each other or on an operand are
- * refused (MOE_EINVAL), but for d_rows on rows.  No atomics on results: the same inputs give the
- * same bits.  Asynchronous, may be captured (two calls that may overlap need a workspace each). */
+ * All: 0 <= T <= 2^21, 1 <= k <= 32, H any positive up to 2^24, n_rows times the rows' distance at most
+ * 2^59.  Results that lie on each other or on an operand are refused (MOE_EINVAL), but for d_rows on rows.  No atomics
+ * on results: the same inputs give the same bits.  Asynchronous, may be captured (two calls that may overlap need a
+ * workspace each). */
 size_t moe_dispatch_workspace(int T, int k, int E);
 int moe_dispatch(const void* x, int xdt, int64_t x_ld, const int32_t* topk_ids, int T, int k, int E, int H,
                  int32_t* counts, int32_t* offsets, int32_t* sorted_rows, int32_t* inv_rows, void* rows,

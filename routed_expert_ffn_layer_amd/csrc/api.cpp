@@ -356,12 +356,15 @@ bool is_float_type(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 constexpr int kMaxRowTokens = 1 << 21;
 
 // Rows of `width` elements, ld apart, that must hold their width and be 16-byte aligned at the first.  The
-// limit keeps sizes in bytes far inside 64 bits.
-int check_rows(const void* p, int64_t ld, int width, const char* what) {
+// limits keep sizes in bytes and the kernels' offsets inside 64 bits; `rows` is given where other checks do not
+// keep their number under 2^23.
+int check_rows(const void* p, int64_t ld, int width, const char* what, int rows = 0) {
   if (!p) return fail(MOE_EINVAL, "%s must not be null", what);
   if (!aligned16(p)) return fail(MOE_EINVAL, "%s must be 16-byte aligned", what);
   if (ld < width || ld > (int64_t)1 << 36)
     return fail(MOE_EINVAL, "%s: rows %lld elements apart, each of %d (at most 2^36 apart)", what, (long long)ld, width);
+  if (rows > ((int64_t)1 << 59) / ld)
+    return fail(MOE_EINVAL, "%s: %d rows %lld elements apart (at most 2^59 in all)", what, rows, (long long)ld);
   return MOE_OK;
 }
 
@@ -554,7 +557,7 @@ int moe_dispatch(const void* x, int xdt, int64_t x_ld, const int32_t* topk_ids, 
     REQUIRE_PTR(inv_rows);
     if (int rc = check_rows(x, x_ld, H, "x")) return rc;
     if (n_rows > 0) {
-      if (int rc = check_rows(rows, rows_ld, H, "rows")) return rc;
+      if (int rc = check_rows(rows, rows_ld, H, "rows", n_rows)) return rc;
     }
   }
   const size_t need = moe::dispatch_workspace_bytes(T, k, E);
@@ -591,7 +594,7 @@ int combine_rows(const void* rows, int rdt, int64_t rows_ld, int n_rows, const f
   REQUIRE(is_float_type(rdt) && is_float_type(ydt), "%s: rows and results are MOE_F32 or MOE_BF16", what);
   if (T == 0) return MOE_OK;
   if (n_rows > 0)
-    if (int rc = check_rows(rows, rows_ld, H, "rows")) return rc;
+    if (int rc = check_rows(rows, rows_ld, H, "rows", n_rows)) return rc;
   REQUIRE_PTR(inv_rows);
   if (int rc = check_rows(y, y_ld, H, "y")) return rc;
   REQUIRE(!overlap({Span{y, y_ld, T, H, ydt}},
@@ -638,8 +641,8 @@ int moe_combine_rows_backward(const void* dy, int ydt, int64_t dy_ld, const void
   if (int rc = check_rows(dy, dy_ld, H, "dy")) return rc;
   const Span sdy{dy, dy_ld, T, H, ydt}, sr{rows, rows_ld, n_rows, H, rdt}, sd{d_rows, dr_ld, n_rows, H, rdt};
   if (n_rows > 0) {
-    if (int rc = check_rows(rows, rows_ld, H, "rows")) return rc;
-    if (int rc = check_rows(d_rows, dr_ld, H, "d_rows")) return rc;
+    if (int rc = check_rows(rows, rows_ld, H, "rows", n_rows)) return rc;
+    if (int rc = check_rows(d_rows, dr_ld, H, "d_rows", n_rows)) return rc;
     REQUIRE(!overlaps(sd, sr) || same_rows(sd, sr), "moe_combine_rows_backward: d_rows overlap rows without being the same");
   }
   REQUIRE_PTR(topk_w);
