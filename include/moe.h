@@ -505,6 +505,9 @@ int moe_block_norm(const void* block, int bdt, int64_t b_ld, int post_kind, cons
  * moe_gate_backward: gradient of the softmax over the selected logits (moe_route_topk's weights):
  *     d_logits[t][e] = sum over j with topk_ids[t][j] = e of w_j (d_w_j - sum_i w_i d_w_i)
  * for all e (0 where e was not selected; the selection itself has no gradient); [T][E] f32.
+ * topk_ids are the router's own, also where moe_dispatch was given a copy with pairs marked as of no expert: the
+ * softmax holds those pairs too, and with their d_w of 0 their logits still get -w_j sum_i w_i d_w_i.  With the
+ * marked ids that part is lost, since no logit is named for it.  The results of the shards of one batch add up.
  *
  * All: 0 <= T <= 2^21, 1 <= k <= 32, H any positive up to 2^24, n_rows times the rows' distance at most
  * 2^59.  Results that lie on each other or on an operand are refused (MOE_EINVAL), but for d_rows on rows.  No atomics

@@ -544,7 +544,8 @@ def moe_combine_rows_backward(dy, rows, topk_w, inv_rows, d_rows, d_topk_w, stre
 
 
 def moe_gate_backward(topk_ids, topk_w, d_topk_w, d_logits, stream=None):
-    """d_logits [T][E] f32 from the gradient of the gate weights."""
+    """d_logits [T][E] f32 from the gradient of the gate weights.  topk_ids: the router's own, not a copy in which pairs are
+    marked as of no expert for moe_dispatch (their logits have a gradient through the softmax)."""
     _matrices(topk_w=topk_w, d_logits=d_logits)
     (T, k), E = topk_w.shape, d_logits.shape[-1]
     _pairs(topk_ids, "topk_ids", "int32", T, k)
