@@ -451,8 +451,8 @@ int moe_w4_linear(int fmt, const void* w, int N, int K, int group, const void* x
  * K, w_ld and x_ld multiples of 8 (bf16) or 4 (f32), K, w_ld and x_ld at most 2^20; y_ld and r_ld
  * any (up to 2^36); T and N at most 2^22, T * N at most 2^35.  Products of bf16 are exact, sums are in f32 in an
  * order that the shape fixes, bias, activation and residual are applied in f32 before the one
- * rounding to ydt; f32 weights are multiplied in f32.  The erf inside GELU is within 1.5e-7.
- * Asynchronous, no workspace, may be captured into a graph. */
+ * rounding to ydt; f32 weights are multiplied in f32.  GELU's P(Z <= z) is within (1.5 z^2 + 24) 2^-24 of
+ * itself for z < 0.  Asynchronous, no workspace, may be captured into a graph. */
 enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4 };
 int moe_linear(int wdt, const void* w, int64_t w_ld, int N, int K, const void* x, int64_t x_ld, int T,
                const float* bias, int act, const void* res, int rdt, int64_t r_ld, void* y, int ydt, int64_t y_ld,
