@@ -457,6 +457,10 @@ enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, M
 int moe_linear(int wdt, const void* w, int64_t w_ld, int N, int K, const void* x, int64_t x_ld, int T,
                const float* bias, int act, const void* res, int rdt, int64_t r_ld, void* y, int ydt, int64_t y_ld,
                hipStream_t stream);
+/* Which kernel moe_linear runs for a shape (the results agree within rounding), as the tile of a workgroup: weight
+ * rows * 65536 + tokens.  16 x 4 and 16 x 8: operands straight into registers; 16 x 16: through LDS, each wave for
+ * itself; 32 x 32 to 256 x 256: staged by the whole workgroup.  0 for no tokens or an invalid shape. */
+int moe_linear_tile(int wdt, int T, int N, int K);
 
 /* ------------------------------------------------------------------------- */
 /* The boundary of two blocks (attention, this layer, a dense part) in one call: the norm after

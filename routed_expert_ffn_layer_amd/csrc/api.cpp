@@ -476,16 +476,33 @@ int moe_block_norm(const void* block, int bdt, int64_t b_ld, int post_kind, cons
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_block_norm launch");
 }
 
+namespace {
+
+int elements16(int wdt) { return wdt == MOE_F32 ? 4 : 8; }  // elements in 16 bytes
+
+int check_linear(int wdt, int T, int N, int K) {
+  if (wdt != MOE_F32 && wdt != MOE_BF16)
+    return fail(MOE_EUNSUPPORTED, "moe_linear: weights are MOE_F32 or MOE_BF16 (4-bit ones: moe_w4_linear)");
+  const int q = elements16(wdt);
+  REQUIRE(T >= 0 && T <= 1 << 22 && N > 0 && N <= 1 << 22 && (int64_t)T * N <= (int64_t)1 << 35,
+          "moe_linear: T=%d, N=%d (each at most 2^22, together 2^35)", T, N);
+  REQUIRE(K > 0 && K % q == 0 && K <= 1 << 20, "moe_linear: K=%d must be a positive multiple of %d, at most 2^20", K, q);
+  return MOE_OK;
+}
+
+}  // namespace
+
+int moe_linear_tile(int wdt, int T, int N, int K) {
+  const CallRange range_(__func__);
+  return check_linear(wdt, T, N, K) || T == 0 ? 0 : moe::linear_tile(wdt == MOE_BF16, T, N, K);
+}
+
 int moe_linear(int wdt, const void* w, int64_t w_ld, int N, int K, const void* x, int64_t x_ld, int T,
                const float* bias, int act, const void* res, int rdt, int64_t r_ld, void* y, int ydt, int64_t y_ld,
                hipStream_t stream) {
   const CallRange range_(__func__);
-  if (wdt != MOE_F32 && wdt != MOE_BF16)
-    return fail(MOE_EUNSUPPORTED, "moe_linear: weights are MOE_F32 or MOE_BF16 (4-bit ones: moe_w4_linear)");
-  const int q = wdt == MOE_F32 ? 4 : 8;  // elements in 16 bytes
-  REQUIRE(T >= 0 && T <= 1 << 22 && N > 0 && N <= 1 << 22 && (int64_t)T * N <= (int64_t)1 << 35,
-          "moe_linear: T=%d, N=%d (each at most 2^22, together 2^35)", T, N);
-  REQUIRE(K > 0 && K % q == 0 && K <= 1 << 20, "moe_linear: K=%d must be a positive multiple of %d, at most 2^20", K, q);
+  if (int rc = check_linear(wdt, T, N, K)) return rc;
+  const int q = elements16(wdt);
   REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH, "moe_linear: unknown activation %d", act);
   REQUIRE(is_float_type(ydt), "moe_linear: ydt must be MOE_F32 or MOE_BF16");
   REQUIRE(!res || is_float_type(rdt), "moe_linear: rdt must be MOE_F32 or MOE_BF16");

@@ -125,6 +125,7 @@ struct LinearArgs {
   int T, N, K, act;
   bool res_bf16, y_bf16;
 };
+int linear_tile(bool bf16, int T, int N, int K);  // of the kernel that launch_linear takes: weight rows << 16 | tokens
 hipError_t launch_linear(bool bf16, const LinearArgs& a, hipStream_t st);
 
 // Tokens sorted by expert and back, with the gradients (token_sort.hip).

@@ -612,22 +612,23 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
 // measured at K = 4096 with 256 workgroups (the first four, by the matrix unit; the others, by the latency of a
 // stage).  The shape whose rounds come out cheapest is taken: within 5% of the best of the seven shapes over
 // T = 16 .. 8192 and N = 1003 .. 65536, where single shapes lose up to 8 times.
-struct TileShape {
+struct LinearForm {
   int rows, tokens;
-  float us[2];  // f32, bf16
+  float us[2];  // f32, bf16; of the tile shapes
   hipError_t (*launch[2])(const LinearArgs&, hipStream_t);
 };
 #define TILE(BN, BT, F, B, ...) \
   {BN, BT, {F, B}, {launch_tile<false, BN, BT, __VA_ARGS__>, launch_tile<true, BN, BT, __VA_ARGS__>}}
-const TileShape kShapes[] = {
+const LinearForm kShapes[] = {
     TILE(256, 256, 7.4f, 1.77f, 4, 2, 1, 2), TILE(256, 128, 3.8f, 0.99f, 4, 2, 1, 3),
     TILE(128, 128, 2.0f, 0.55f, 2, 2, 2, 4), TILE(128, 64, 1.1f, 0.37f, 2, 1, 2, 4),
     TILE(64, 64, 0.57f, 0.25f, 1, 1, 4, 4),  TILE(64, 32, 0.31f, 0.18f, 1, 1, 4, 5),
     TILE(32, 32, 0.20f, 0.14f, 1, 1, 4, 8),
 };
 #undef TILE
-
-}  // namespace
+const LinearForm kStream4 = {16, 4, {}, {launch_stream<false, 4>, launch_stream<true, 4>}};
+const LinearForm kStream8 = {16, 8, {}, {nullptr, launch_stream<true, 8>}};
+const LinearForm kSmall = {16, 16, {}, {launch_small<false>, launch_small<true>}};
 
 // Up to 8 tokens (f32: 4) the stream kernel.  The small kernel takes up to 16, where the tiles' 32 token rows would be
 // half of the loads (weights from memory, bf16: 16 x 4096 x 4096 9.7 us, 12 in tiles, 16 x 65536 x 4096 102 and 104; f32:
@@ -636,22 +637,33 @@ const TileShape kShapes[] = {
 // where K is short (100 x 600 x 2048 5.3 and 6.3, x 4096 7.4 and 8.8, but 1000 x 100 x 4096 12.3 and 9.0, 64 x 2048 x 16384
 // 29 and 24).  f32, up to two: 64 x 64 x 14400 22 and 75, 256 x 512 x 4096 15.4 and 24.6; four: 64 x 4096 x 4096 41
 // and 25.
-hipError_t launch_linear(bool bf16, const LinearArgs& a, hipStream_t st) {
-  const bool few = (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= (bf16 && a.K > 2048 ? 256 : 512);
-  if (a.T <= 4) return bf16 ? launch_stream<true, 4>(a, st) : launch_stream<false, 4>(a, st);
-  if (bf16 && a.T <= 8) return launch_stream<true, 8>(a, st);
-  if (few || a.T <= 16) return bf16 ? launch_small<true>(a, st) : launch_small<false>(a, st);
-  const TileShape* best = nullptr;
+const LinearForm& choose_form(bool bf16, int T, int N, int K) {
+  const bool few = (int64_t)((N + 15) / 16) * ((T + 15) / 16) <= (bf16 && K > 2048 ? 256 : 512);
+  if (T <= 4) return kStream4;
+  if (bf16 && T <= 8) return kStream8;
+  if (few || T <= 16) return kSmall;
+  const LinearForm* best = nullptr;
   float least = 0.0f;
-  for (const TileShape& s : kShapes) {
-    const int64_t tiles = (int64_t)((a.N + s.rows - 1) / s.rows) * ((a.T + s.tokens - 1) / s.tokens);
+  for (const LinearForm& s : kShapes) {
+    const int64_t tiles = (int64_t)((N + s.rows - 1) / s.rows) * ((T + s.tokens - 1) / s.tokens);
     const float us = (float)((tiles + 255) / 256) * s.us[bf16];
     if (!best || us < least) {
       best = &s;
       least = us;
     }
   }
-  return best->launch[bf16](a, st);
+  return *best;
+}
+
+}  // namespace
+
+int linear_tile(bool bf16, int T, int N, int K) {
+  const LinearForm& f = choose_form(bf16, T, N, K);
+  return f.rows << 16 | f.tokens;
+}
+
+hipError_t launch_linear(bool bf16, const LinearArgs& a, hipStream_t st) {
+  return choose_form(bf16, a.T, a.N, a.K).launch[bf16](a, st);
 }
 
 }  // namespace moe

@@ -61,7 +61,7 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_last_error", "moe_expert_by
            "moe_cache_lookup_fill_inplace", "moe_cache_step_inplace", "moe_grouped_ffn_addr", "moe_route", "moe_cache_resize", "moe_route_project",
            "moe_grouped_ffn_workspace", "moe_grouped_ffn_kind", "moe_mx8_quantize", "moe_grouped_ffn", "moe_grouped_ffn_gate_up", "moe_grouped_ffn_down", "moe_grouped_ffn_noalloc",
            "moe_combine", "moe_layer_decode", "moe_layer_decode_workspace", "moe_w4_bytes", "moe_w4_pack",
-           "moe_w4_linear", "moe_linear", "moe_block_norm", "moe_dispatch_workspace", "moe_dispatch",
+           "moe_w4_linear", "moe_linear", "moe_linear_tile", "moe_block_norm", "moe_dispatch_workspace", "moe_dispatch",
            "moe_dispatch_backward", "moe_combine_rows", "moe_combine_rows_backward", "moe_gate_backward",
            "moe_layer_stream_create", "moe_layer_stream_destroy", "moe_layer_stream_fill",
            "moe_layer_stream_acquire", "moe_layer_stream_release"]
@@ -117,6 +117,7 @@ def lib():
     L.moe_w4_pack.argtypes = [i, P, P, P, i, i, i, P, P]
     L.moe_w4_linear.argtypes = [i, P, i, i, i, P, ctypes.c_int64, i, P, P, ctypes.c_int64, i, P]
     L.moe_linear.argtypes = [i, P, l, i, i, P, l, i, P, i, P, i, l, P, i, l, P]
+    L.moe_linear_tile.argtypes = [i, i, i, i]
     L.moe_block_norm.argtypes = [P, i, l, i, P, P, P, i, l, f, P, l, f, i, P, P, f, i, i, P, i, l, P, i, l, P]
     L.moe_dispatch_workspace.restype = sz
     L.moe_dispatch_workspace.argtypes = [i, i, i]
@@ -433,6 +434,11 @@ def moe_linear(w, x, bias, act, res, y, stream=None):
     bp = _vector(bias, "bias", N)
     st = _stream_of(stream, w, x, bias, res, y)
     _check(lib().moe_linear(wdt, wp, w_ld, N, K, xp, x_ld, T, bp, act, rp, rdt, r_ld, yp, ydt, y_ld, st))
+
+
+def moe_linear_tile(wdt, T, N, K):
+    """(weight rows, tokens) of the tile that a workgroup of moe_linear's kernel for this shape computes."""
+    return divmod(lib().moe_linear_tile(wdt, T, N, K), 1 << 16)
 
 
 def _norm(norm, name, H):
