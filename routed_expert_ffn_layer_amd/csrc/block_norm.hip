@@ -10,7 +10,7 @@
 // consecutive elements.
 //
 // Statistics in f32.  RMS: sum of squares.  Layer norm: mean first, then the sums of d = v - mean
-// and of d^2 in one reduction; the mean of d is what rounding left in the first mean, and is taken
+// and of d^2, three reductions in all; the mean of d is what rounding left in the first mean, and is taken
 // from d afterwards, so large offsets cost no digits.  Sums that leave the f32 range (elements
 // past 2^63, or with a tiny eps below 2^-45) are formed again with the row scaled by a power of
 // two, a branch that the whole row takes or leaves.

@@ -11,9 +11,15 @@
 // Measured on an MI355X, bf16, x weights x K (plain library product beside it): 1 x 4096 x 4096 4.5 us (10.5),
 // 16 x 512 x 4096 4.9 (8.0), 16 x 12288 x 4096 17.5 (21), 64 x 4096 x 4096 9.1 (19), 4 x 65536 x 4096 87 (124; 537 MB
 // at 6.2 TB/s), 256 x 4096 x 4096 16.3 (19.7), 1024 x 4096 x 4096 35.6 (37.4), 4096 x 8192 x 4096 220 (177 once both
-// are warm; 1.25 PFLOP/s); f32: 4 x 512 x 4096 7.4 (9.9), 16 x 64 x 4096 7.9 (9.7), 32 x 2048 x 2048 6.0 (8.9),
-// 64 x 4096 x 4096 25 (22), 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).  Behind the library stay f32 products of about two
-// 16 x 16 tiles a CU and deep K, where it spreads K over the chip and adds up in memory: 85 x 864 x 14400 56 (41).
+// are warm; 1.25 PFLOP/s), 512 x 256 x 4096 9.4 (8.3); f32: 4 x 512 x 4096 7.4 (9.9), 16 x 64 x 4096 7.9 (9.7), 32 x 2048 x 2048 6.0 (8.9),
+// 64 x 4096 x 4096 25 (22), 4096 x 4096 x 4096 944 (920; 146 TFLOP/s).
+//
+// Against the library's product of the same type over 42 pairs of weights (100 to 12288) and K (512 to 16384), as the
+// geometric mean of the times' ratios, both captured and warm: bf16 0.67 to 0.80 for 1 to 256 tokens, 0.99 for 512, 1.04 and 1.06
+// for 1024 and 2048, 1.11 and 1.16 for 4096 and 8192; f32 0.78 to 0.93 for 1 to 256, 1.10 to 1.18 from 512 on.  Farthest behind:
+// large results of short K, whose prologue and epilogue no product covers (bf16 8192 x 12288 x 512 187 us and 114, 1024 x 12288 x
+// 1024 48 and 30), and few results of deep K, where the library spreads K over the chip and adds up in memory (bf16
+// 512 x 100 x 8192 14 and 8.6, f32 1024 x 100 x 16384 84 and 43, 85 x 864 x 14400 56 and 41, 256 x 12288 x 4096 254 and 180).
 #include "ffn_common.hpp"
 #include "kernels.hpp"
 #include "row_io.hpp"
@@ -26,7 +32,8 @@ namespace {
 
 // P(Z > a) of a normal Z, a >= 0: t P(t) e^(-a^2 / 2) with t = 1 / (1 + 0.375 a / sqrt(2)).  P, of degree 8, is fitted to
 // erfc(z) e^(z^2) / 2 over z = a / sqrt(2) in [0, 9.5] for the least relative error, 1.2e-8, so that the tail keeps its
-// digits: within (1.5 a^2 + 24) 2^-24 relative, of which the exponent's roundings are the first term.
+// digits: within (1.5 a^2 + 24) 2^-24 relative, of which the exponent's roundings are the first term.  (4096 x 8192 x 4096 with GELU
+// 239 us; 237 with degree 4 and 1.5e-7 absolutely, which at -8 is 1e-2 of the value.)
 __device__ __forceinline__ float normal_tail(float a) {
   const float t = __builtin_amdgcn_rcpf(fmaf(0.26516504294495533f, a, 1.0f));
   float p = fmaf(3.084828891e-02f, t, -1.440376043e-01f);
@@ -355,8 +362,8 @@ hipError_t launch_small(const LinearArgs& a, hipStream_t st) {
 // Each step is laid out by hand: a product, an operand read of the next step, a load of a later stage, the next
 // product, .. (reads, loads and products one after the other: 4096 x 8192 x 4096 in 267 us, so 220).  What bounds
 // the largest tile now is the loads: with the same products and none of them in the loop it takes 193 us, with all
-// of them from the same stage 216; without the barrier nothing changes.  The matrix unit is busy in 72 to 77% of
-// the cycles, at a clock that this work holds near 1.5 GHz.  Measured and not kept: 4 waves of 128 x 128 (324 us:
+// of them from the same stage 216; without the barrier nothing changes.  The matrix unit is busy in 68 to 72% of
+// the cycles (the library's 87%), at a clock of 1.7 to 1.8 GHz (counter runs).  Measured and not kept: 4 waves of 128 x 128 (324 us:
 // one wave per SIMD), stages of 64 bytes with 4 or 5 buffers (231), workgroups starting at other columns (neutral
 // or slower).
 // ---------------------------------------------------------------------------
@@ -610,8 +617,10 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
 
 // Tile shapes, by the time that a stage (128 bytes of K) of a round of 256 workgroups, one for each CU, takes: us,
 // measured at K = 4096 with 256 workgroups (the first four, by the matrix unit; the others, by the latency of a
-// stage).  The shape whose rounds come out cheapest is taken: within 5% of the best of the seven shapes over
-// T = 16 .. 8192 and N = 1003 .. 65536, where single shapes lose up to 8 times.
+// stage).  The shape whose rounds come out cheapest is taken.  Over T = 16 .. 4096 and N = 500 .. 20000 it is within 8% of the
+// best of the seven at bf16 and K = 4096; at K = 1024, where a round is mostly prologue and epilogue, that it does not
+// count, within 13% (1000 x 12288: 46.6 us, 41.2 in tiles of 256 x 256); f32 at K = 2048 within 23% (700 x 4096: 143 us, 116
+// in tiles of 64 x 32, of which a CU holds several, which it does not count either).  Single shapes lose up to 8 times.
 struct LinearForm {
   int rows, tokens;
   float us[2];  // f32, bf16; of the tile shapes
